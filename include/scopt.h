@@ -382,6 +382,75 @@ int sc_mask_pack(sc_dtype dtype, const void* x, const int32_t* idx, int64_t T, i
 int sc_mask_unpack(sc_dtype dtype, const void* packed, const int32_t* idx, int64_t T, int H, int K,
                    void* x, void* stream);
 
+/* ---- Training-step operators ------------------------------------------------------
+ * The two ends of a training step around the masked boundary: token embedding
+ * with its gradient, the residual root-mean-square norm with an 8-bit
+ * checkpoint of its output, the gradients that read the checkpoint, and softmax
+ * cross entropy over a large vocabulary with its gradients.
+ *
+ * These calls need no handle.  All pointers are device pointers on the current
+ * device, matrices row-major and contiguous, `dtype` the type of every tensor
+ * that is not given as another one; h, W, dy and workspaces must be 16-byte
+ * aligned.  Calls that take a workspace need at least the bytes that their
+ * query returns for the same sizes, keep nothing in it between calls, and
+ * allocate nothing; every call only enqueues.  Results do not depend on timing
+ * (no floating-point atomics).  Token ids and targets are int64; one outside
+ * [0, V) is no token: a zero row in sc_embed, no gradient in sc_embed_grad, not
+ * counted in sc_xent.  T = 0 is allowed everywhere.
+ * Errors: SC_ERR_INVALID_ARG (NULL or misaligned pointer, unknown dtype, too
+ * small a workspace), SC_ERR_SHAPE (sizes out of range), before any GPU work.
+ *
+ * The 8-bit checkpoint of a matrix [T][H]: int8 q [T][H] and uint8 e [T][ceil(H/32)];
+ * 32 elements along a row share e = E + 127, E = max(floor(log2 amax), -120), and
+ * stand for q * 2^(E - 6), q = round-to-even(x * 2^(6 - E)) clipped to +-127.  A
+ * block that holds a NaN or an infinity has e = 255 and reads as NaN. */
+
+/* out[t] = scale * table[ids[t]]: table [V][H], out [T][H].  1 <= H <= 2^24. */
+int sc_embed(sc_dtype dtype, const void* table, const int64_t* ids, int64_t T, int64_t V, int H, float scale,
+             void* out, void* stream);
+
+/* dW[v] = scale * sum over t with ids[t] = v of dy[t], in float32 and token order;
+ * dW [V][H] is written whole.  T < 2^31, V <= 2^22. */
+int sc_embed_grad_workspace(int64_t T, int64_t V, int H, int64_t* bytes);
+int sc_embed_grad(sc_dtype dtype, const void* dy, const int64_t* ids, int64_t T, int64_t V, int H, float scale,
+                  void* dW, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* The 8-bit checkpoint of x [T][H], and back (exact in either dtype). */
+int sc_act_pack(sc_dtype dtype, const void* x, int64_t T, int H, int8_t* q, uint8_t* e, void* stream);
+int sc_act_unpack(sc_dtype dtype, const int8_t* q, const uint8_t* e, int64_t T, int H, void* x, void* stream);
+
+/* h = x + residual, rstd = 1 / sqrt(mean(h^2) + eps), n = h * rstd, y = n * gain, all
+ * from the float32 sum; q, e: the checkpoint of n.  residual may be NULL (h = x,
+ * then h may be NULL), h may be NULL, q and e may be NULL together.  gain [H], rstd
+ * float32 [T].  h may be x or residual.  1 <= H <= 16384. */
+int sc_rmsnorm(sc_dtype dtype, const void* x, const void* residual, const void* gain, float eps, int64_t T, int H,
+               void* h, void* y, float* rstd, int8_t* q, uint8_t* e, void* stream);
+
+/* With a = dy * gain: dx = dh + rstd * (a - n * mean(a * n)), the gradient of x and of the
+ * residual; dgain [H] float32 = sum over tokens of dy * n.  dh (the gradient that reaches
+ * h past the norm) may be NULL; dx may be dy or dh. */
+int sc_rmsnorm_grad_workspace(int64_t T, int H, int64_t* bytes);
+int sc_rmsnorm_grad(sc_dtype dtype, const void* dy, const void* gain, const float* rstd, const int8_t* q,
+                    const uint8_t* e, const void* dh, int64_t T, int H, void* dx, float* dgain, void* workspace,
+                    int64_t workspace_bytes, void* stream);
+
+/* Gradient of the weight [N][H] of a projection of n * gain: dW = (dy^T n) * gain, with n read
+ * from its checkpoint; dy [T][N], gain [H] or NULL (1). T, N, H < 2^21. */
+int sc_act_wgrad_workspace(sc_dtype dtype, int64_t T, int64_t N, int H, int64_t* bytes);
+int sc_act_wgrad(sc_dtype dtype, const void* dy, const int8_t* q, const uint8_t* e, const void* gain, int64_t T,
+                 int64_t N, int H, void* dW, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Softmax cross entropy of the logits h W^T (h [T][H], W [V][H]) against targets [T]:
+ * loss float32 [T] (0 where not counted), mean float32 [1] over the counted tokens
+ * (0 if none), and the gradients of the mean: dh [T][H], dW [V][H].  The vocabulary
+ * goes by in pieces.  limit: bytes that a piece's intermediate values may take (0: 4 GiB);
+ * if the whole vocabulary's fit, they are kept between the forward and the gradient
+ * products, otherwise each piece's are computed again.  T, V < 2^21 and H < 2^16. */
+int sc_xent_workspace(sc_dtype dtype, int64_t T, int64_t V, int H, int64_t limit, int64_t* bytes);
+int sc_xent(sc_dtype dtype, const void* h, const void* W, const int64_t* targets, int64_t T, int64_t V, int H,
+            int64_t limit, float* loss, float* mean, void* dh, void* dW, void* workspace, int64_t workspace_bytes,
+            void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -15,13 +15,16 @@ G_proj = alpha G + (1 - alpha) G_filt, then AdamW.
 """
 from __future__ import annotations
 
+import collections
 import ctypes
 import os
 
 import torch  # loaded first: libscopt then binds to torch's HIP runtime
 
 __all__ = ["SpectralAdamW", "ScoptError", "library_path", "load_library", "EXPORTED_SYMBOLS",
-           "mask_keep_count", "mask_seed", "mask_indices", "mask_pack", "mask_unpack"]
+           "mask_keep_count", "mask_seed", "mask_indices", "mask_pack", "mask_unpack",
+           "ActCheckpoint", "RmsNorm", "CrossEntropy", "embed", "embed_grad", "act_pack", "act_unpack",
+           "rmsnorm", "rmsnorm_grad", "act_wgrad", "xent"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libscopt.so")
@@ -34,6 +37,9 @@ EXPORTED_SYMBOLS = (
     "sc_set_solve_waves", "sc_set_fused_gram", "sc_set_v_rounds", "sc_set_sweep_stop", "sc_set_quad",
     "sc_get_stats", "sc_get_sweep_counts", "sc_profile", "sc_get_kernel_times", "sc_last_error",
     "sc_mask_keep_count", "sc_mask_seed", "sc_mask_indices", "sc_mask_pack", "sc_mask_unpack",
+    "sc_embed", "sc_embed_grad_workspace", "sc_embed_grad", "sc_act_pack", "sc_act_unpack", "sc_rmsnorm",
+    "sc_rmsnorm_grad_workspace", "sc_rmsnorm_grad", "sc_act_wgrad_workspace", "sc_act_wgrad",
+    "sc_xent_workspace", "sc_xent",
 )
 
 SC_F32, SC_BF16 = 0, 1
@@ -125,6 +131,21 @@ def load_library():
         "sc_mask_unpack": (ctypes.c_int, [ctypes.c_int, vp, vp, ctypes.c_int64, ctypes.c_int, ctypes.c_int,
                                           vp, vp]),
     }
+    i64, i32, f32, dt = ctypes.c_int64, ctypes.c_int, ctypes.c_float, ctypes.c_int
+    sig.update({
+        "sc_embed": (i32, [dt, vp, vp, i64, i64, i32, f32, vp, vp]),
+        "sc_embed_grad_workspace": (i32, [i64, i64, i32, i64p]),
+        "sc_embed_grad": (i32, [dt, vp, vp, i64, i64, i32, f32, vp, vp, i64, vp]),
+        "sc_act_pack": (i32, [dt, vp, i64, i32, vp, vp, vp]),
+        "sc_act_unpack": (i32, [dt, vp, vp, i64, i32, vp, vp]),
+        "sc_rmsnorm": (i32, [dt, vp, vp, vp, f32, i64, i32, vp, vp, vp, vp, vp, vp]),
+        "sc_rmsnorm_grad_workspace": (i32, [i64, i32, i64p]),
+        "sc_rmsnorm_grad": (i32, [dt, vp, vp, vp, vp, vp, vp, i64, i32, vp, vp, vp, i64, vp]),
+        "sc_act_wgrad_workspace": (i32, [dt, i64, i64, i32, i64p]),
+        "sc_act_wgrad": (i32, [dt, vp, vp, vp, vp, i64, i64, i32, vp, vp, i64, vp]),
+        "sc_xent_workspace": (i32, [dt, i64, i64, i32, i64, i64p]),
+        "sc_xent": (i32, [dt, vp, vp, vp, i64, i64, i32, i64, vp, vp, vp, vp, vp, i64, vp]),
+    })
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
         f.restype = res
@@ -426,3 +447,198 @@ def mask_unpack(packed: "torch.Tensor", idx: "torch.Tensor", H: int) -> "torch.T
                                          ctypes.c_void_p(idx.data_ptr()), T, int(H), K,
                                          ctypes.c_void_p(out.data_ptr()), _cur_stream(packed.device)))
     return out
+
+
+# ---- training-step operators: stateless calls --------------------------------------
+# Tensors are contiguous and on one device; work is queued on its current stream.
+
+ActCheckpoint = collections.namedtuple("ActCheckpoint", "q e")
+ActCheckpoint.__doc__ = """An 8-bit checkpoint of a matrix [T, H]: int8 q [T, H] and uint8 e [T, ceil(H / 32)];
+32 elements along a row stand for q * 2^(e - 133).  e = 255 marks a block that held a NaN or
+an infinity; it reads as NaN."""
+
+RmsNorm = collections.namedtuple("RmsNorm", "h y rstd kept")
+RmsNorm.__doc__ = """Of rmsnorm: the residual sum h, the output y, 1 / rms (float32 [T]) and the
+checkpoint of the normalised rows (None where none was kept)."""
+
+CrossEntropy = collections.namedtuple("CrossEntropy", "loss mean dh dW")
+CrossEntropy.__doc__ = """Of xent: float32 losses [T], their mean over the counted tokens (0-dim), and the mean's
+gradients."""
+
+
+def _train_check(who, dtype, dev, *named):
+    """named: (name, tensor, dtype or None for `dtype`, shape)."""
+    if dtype not in _DT:
+        raise ValueError(f"{who}: tensors must be float32 or bfloat16, got {dtype}")
+    if dev.type != "cuda":
+        raise ValueError(f"{who}: tensors must be on a GPU, got {dev}")
+    for name, t, dt, shape in named:
+        dt = dtype if dt is None else dt
+        if t.device != dev or t.dtype != dt or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+            raise ValueError(f"{who}: {name} must be a contiguous {dt} tensor of shape {tuple(shape)} on {dev}, "
+                             f"got {t.dtype} {tuple(t.shape)} on {t.device}"
+                             f"{'' if t.is_contiguous() else ' (not contiguous)'}")
+
+
+def _matrix(who, name, t):
+    if t.dim() != 2:
+        raise ValueError(f"{who}: {name} must be a matrix, got shape {tuple(t.shape)}")
+    return t.shape
+
+
+def _at16(t):
+    """t, or a copy where a view starts off 16 bytes (the products fetch 16 bytes at a time)."""
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
+def _run(dev, fn, *args):
+    """Call with the device current and its stream last."""
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+
+
+def _workspace(dev, query, *args):
+    n = ctypes.c_int64()
+    _check(query(*args, ctypes.byref(n)))
+    return torch.empty(n.value, dtype=torch.uint8, device=dev), n.value
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def embed(table: "torch.Tensor", ids: "torch.Tensor", scale: float = 1.0) -> "torch.Tensor":
+    """scale * table[ids] (table [V, H], ids int64 of any shape); rows of zeros where an id is
+    outside [0, V)."""
+    V, H = _matrix("embed", "table", table)
+    _train_check("embed", table.dtype, table.device, ("table", table, None, (V, H)),
+                 ("ids", ids, torch.int64, ids.shape))
+    out = torch.empty((*ids.shape, H), dtype=table.dtype, device=table.device)
+    _run(table.device, load_library().sc_embed, _DT[table.dtype], table.data_ptr(), ids.data_ptr(), ids.numel(), V, H,
+         float(scale), out.data_ptr())
+    return out
+
+
+def embed_grad(dy: "torch.Tensor", ids: "torch.Tensor", V: int, scale: float = 1.0) -> "torch.Tensor":
+    """Gradient [V, H] of the table of embed: scale * the sum of dy [..., H] over each id's
+    tokens, in float32 and token order."""
+    if dy.dim() < 1 or tuple(dy.shape[:-1]) != tuple(ids.shape):
+        raise ValueError(f"embed_grad: dy {tuple(dy.shape)} must be ids {tuple(ids.shape)} and the hidden size")
+    H = dy.shape[-1]
+    _train_check("embed_grad", dy.dtype, dy.device, ("dy", dy, None, dy.shape), ("ids", ids, torch.int64, ids.shape))
+    lib, T, V = load_library(), ids.numel(), int(V)
+    ws, n = _workspace(dy.device, lib.sc_embed_grad_workspace, T, V, H)
+    dW = torch.empty((V, H), dtype=dy.dtype, device=dy.device)
+    _run(dy.device, lib.sc_embed_grad, _DT[dy.dtype], dy.data_ptr(), ids.data_ptr(), T, V, H, float(scale),
+         dW.data_ptr(), ws.data_ptr(), n)
+    return dW
+
+
+def act_pack(x: "torch.Tensor") -> ActCheckpoint:
+    """The 8-bit checkpoint of x [T, H]."""
+    T, H = _matrix("act_pack", "x", x)
+    _train_check("act_pack", x.dtype, x.device, ("x", x, None, (T, H)))
+    q = torch.empty((T, H), dtype=torch.int8, device=x.device)
+    e = torch.empty((T, -(-H // 32)), dtype=torch.uint8, device=x.device)
+    _run(x.device, load_library().sc_act_pack, _DT[x.dtype], x.data_ptr(), T, H, q.data_ptr(), e.data_ptr())
+    return ActCheckpoint(q, e)
+
+
+def _check_kept(who, kept, T, H, dtype, dev):
+    _train_check(who, dtype, dev, ("q", kept.q, torch.int8, (T, H)), ("e", kept.e, torch.uint8, (T, -(-H // 32))))
+
+
+def act_unpack(kept: ActCheckpoint, dtype: "torch.dtype" = torch.bfloat16) -> "torch.Tensor":
+    """The values of a checkpoint (exact in either dtype)."""
+    T, H = _matrix("act_unpack", "q", kept.q)
+    _check_kept("act_unpack", kept, T, H, dtype, kept.q.device)
+    x = torch.empty((T, H), dtype=dtype, device=kept.q.device)
+    _run(x.device, load_library().sc_act_unpack, _DT[dtype], kept.q.data_ptr(), kept.e.data_ptr(), T, H, x.data_ptr())
+    return x
+
+
+def rmsnorm(x: "torch.Tensor", gain: "torch.Tensor", residual: "torch.Tensor" = None, eps: float = 1e-5,
+            keep: bool = True) -> RmsNorm:
+    """h = x + residual (x without one), rstd = 1 / sqrt(mean(h^2) + eps), y = h * rstd * gain
+    for rows of x [T, H], and with keep the 8-bit checkpoint of h * rstd for the backward pass."""
+    T, H = _matrix("rmsnorm", "x", x)
+    named = [("x", x, None, (T, H)), ("gain", gain, None, (H,))]
+    if residual is not None:
+        named.append(("residual", residual, None, (T, H)))
+    dev = x.device
+    _train_check("rmsnorm", x.dtype, dev, *named)
+    h = x if residual is None else torch.empty_like(x)
+    y = torch.empty_like(x)
+    rstd = torch.empty(T, dtype=torch.float32, device=dev)
+    kept = None
+    if keep:
+        kept = ActCheckpoint(torch.empty((T, H), dtype=torch.int8, device=dev),
+                             torch.empty((T, -(-H // 32)), dtype=torch.uint8, device=dev))
+    _run(dev, load_library().sc_rmsnorm, _DT[x.dtype], x.data_ptr(), _ptr(residual), gain.data_ptr(), float(eps), T, H,
+         None if residual is None else h.data_ptr(), y.data_ptr(), rstd.data_ptr(),
+         kept.q.data_ptr() if keep else None, kept.e.data_ptr() if keep else None)
+    return RmsNorm(h, y, rstd, kept)
+
+
+def rmsnorm_grad(dy: "torch.Tensor", gain: "torch.Tensor", rstd: "torch.Tensor", kept: ActCheckpoint,
+                 dh: "torch.Tensor" = None):
+    """(dx, dgain) of rmsnorm from its checkpoint: dx [T, H] is the gradient of x and of the
+    residual, with dh, the gradient that reaches h past the norm, added; dgain float32 [H]."""
+    T, H = _matrix("rmsnorm_grad", "dy", dy)
+    named = [("dy", dy, None, (T, H)), ("gain", gain, None, (H,)), ("rstd", rstd, torch.float32, (T,))]
+    if dh is not None:
+        named.append(("dh", dh, None, (T, H)))
+    dev = dy.device
+    _train_check("rmsnorm_grad", dy.dtype, dev, *named)
+    _check_kept("rmsnorm_grad", kept, T, H, dy.dtype, dev)
+    lib = load_library()
+    ws, n = _workspace(dev, lib.sc_rmsnorm_grad_workspace, T, H)
+    dx = torch.empty_like(dy)
+    dgain = torch.empty(H, dtype=torch.float32, device=dev)
+    _run(dev, lib.sc_rmsnorm_grad, _DT[dy.dtype], dy.data_ptr(), gain.data_ptr(), rstd.data_ptr(), kept.q.data_ptr(),
+         kept.e.data_ptr(), _ptr(dh), T, H, dx.data_ptr(), dgain.data_ptr(), ws.data_ptr(), n)
+    return dx, dgain
+
+
+def act_wgrad(dy: "torch.Tensor", kept: ActCheckpoint, gain: "torch.Tensor" = None) -> "torch.Tensor":
+    """Weight gradient [N, H] of a projection whose input is n * gain, with n read from its
+    checkpoint: (dy^T n) * gain for dy [T, N]."""
+    T, N = _matrix("act_wgrad", "dy", dy)
+    H = _matrix("act_wgrad", "q", kept.q)[1]
+    dev = dy.device
+    named = [("dy", dy, None, (T, N))]
+    if gain is not None:
+        named.append(("gain", gain, None, (H,)))
+    _train_check("act_wgrad", dy.dtype, dev, *named)
+    _check_kept("act_wgrad", kept, T, H, dy.dtype, dev)
+    lib = load_library()
+    dy = _at16(dy)
+    ws, n = _workspace(dev, lib.sc_act_wgrad_workspace, _DT[dy.dtype], T, N, H)
+    dW = torch.empty((N, H), dtype=dy.dtype, device=dev)
+    _run(dev, lib.sc_act_wgrad, _DT[dy.dtype], dy.data_ptr(), kept.q.data_ptr(), kept.e.data_ptr(), _ptr(gain), T, N,
+         H, dW.data_ptr(), ws.data_ptr(), n)
+    return dW
+
+
+def xent(h: "torch.Tensor", W: "torch.Tensor", targets: "torch.Tensor", limit: int = 0) -> CrossEntropy:
+    """Softmax cross entropy of the logits h W^T (h [T, H], W [V, H]) against int64 targets [T],
+    without a matrix of logits, with the gradients of the mean over the counted tokens.  A
+    target outside [0, V) is not counted: its loss is 0.  limit: bytes for a vocabulary piece's
+    intermediate values (0: 4 GiB)."""
+    T, H = _matrix("xent", "h", h)
+    V = _matrix("xent", "W", W)[0]
+    dev = h.device
+    _train_check("xent", h.dtype, dev, ("h", h, None, (T, H)), ("W", W, None, (V, H)),
+                 ("targets", targets, torch.int64, (T,)))
+    lib = load_library()
+    h, W = _at16(h), _at16(W)
+    ws, n = _workspace(dev, lib.sc_xent_workspace, _DT[h.dtype], T, V, H, int(limit))
+    loss = torch.empty(T, dtype=torch.float32, device=dev)
+    mean = torch.empty((), dtype=torch.float32, device=dev)
+    dh, dW = torch.empty_like(h), torch.empty_like(W)
+    _run(dev, lib.sc_xent, _DT[h.dtype], h.data_ptr(), W.data_ptr(), targets.data_ptr(), T, V, H, int(limit),
+         loss.data_ptr(), mean.data_ptr(), dh.data_ptr(), dW.data_ptr(), ws.data_ptr(), n)
+    return CrossEntropy(loss, mean, dh, dW)

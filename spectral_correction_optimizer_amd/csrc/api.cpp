@@ -28,9 +28,10 @@
 using namespace scopt;
 
 namespace {
-
 thread_local std::string g_err;
+}  // namespace
 
+namespace scopt {
 int fail(int code, const char* fmt, ...) {
     char buf[512];
     va_list ap;
@@ -40,6 +41,9 @@ int fail(int code, const char* fmt, ...) {
     g_err = buf;
     return code;
 }
+}  // namespace scopt
+
+namespace {
 
 #define HIP_TRY(expr)                                                                      \
     do {                                                                                   \

@@ -34,6 +34,9 @@ __host__ __device__ inline bool quad_capable(int nb) {
 }
 __host__ __device__ inline int quad_passes(int nb) { return (nb - 1) / 3; }
 
+// Keep the message of sc_last_error for the calling thread and return `code`.
+int fail(int code, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+
 // Caller pointers of one call (weights / gradients), passed by value.
 struct PtrTable {
     const void* p[kMaxPtrs];

@@ -1,0 +1,179 @@
+// The tiled products of the training-step operators: instances of the kernel of
+// tile_product.hpp, the choice of tile and split, the sum over splits, and the copies of
+// operands into bfloat16 planes.
+#include "rows.hpp"
+#include "tile_product.hpp"
+
+namespace scopt {
+
+namespace {
+using Big = TpShape<256, 256, 2, 4, 2, 1>;    // 128 KB of LDS: one workgroup of 8 waves per CU
+using Mid = TpShape<128, 128, 2, 2, 2, 2>;    // 64 KB: two workgroups of 4 waves per CU
+using Small = TpShape<64, 128, 1, 4, 3, 2>;   // 72 KB: two workgroups of 4 waves per CU
+}  // namespace
+
+// Sum of the splits' partial products, in split order, with the store's factors.
+// acc: an earlier sum that is added (NULL: none); out_acc: the sum is kept there in float32
+// instead of being stored.
+__global__ __launch_bounds__(256) void tp_reduce_kernel(const TpArgs P, const float* acc, float* out_acc) {
+    const int64_t groups = (int64_t)P.M * ((P.N + 3) / 4);
+    const float alpha = P.alpha ? gld(P.alpha) : 1.0f;
+    const bool vec = (P.N & 3) == 0;
+    for (int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x; g < groups; g += (int64_t)gridDim.x * 256) {
+        const int64_t m = g / ((P.N + 3) / 4);
+        const int n = (int)(g - m * ((P.N + 3) / 4)) * 4;
+        const int left = P.N - n;
+        const int64_t at = m * P.N + n, stride = (int64_t)P.M * P.N;
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        auto add = [&](const float* p) {
+            if (vec) {
+                const v4f x = gld4(p);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v[r] += x[r];
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (r < left) v[r] += gld(p + r);
+            }
+        };
+        if (acc) add(acc + at);
+        for (int s = 0; s < P.splits; ++s) add(P.part + s * stride + at);
+        if (out_acc) {
+            tp_store(out_acc, 0, at, v, left, vec);
+        } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] *= alpha * tp_gain(P, min(n + r, P.N - 1));
+            tp_store(P.C, P.c_bf16, m * P.ldc + n, v, left, P.c_vec);
+        }
+    }
+}
+
+// Choice of tile and split: the least estimated time.  A workgroup's 64-deep step takes
+// `step` us with the chip full; a split's partial sums are written and read once more.
+TpPlan tp_plan(int M, int N, int K, int nseg, bool may_split) {
+    struct Shape {
+        int bm, bn, per_cu;
+        double step;
+    };
+    static const Shape shapes[3] = {{256, 256, 1, 1.95}, {128, 128, 2, 1.30}, {64, 128, 2, 0.98}};
+    const int64_t steps = (int64_t)((K + 63) / 64) * nseg;
+    TpPlan best;
+    double best_us = 1e300;
+    for (int s = 0; s < 3; ++s) {
+        const int64_t tm = (M + shapes[s].bm - 1) / shapes[s].bm, tn = (N + shapes[s].bn - 1) / shapes[s].bn;
+        for (int sp = 1; sp <= (may_split ? 64 : 1); sp *= 2) {
+            if (sp > 1 && steps / sp < 4) break;
+            const int64_t wgs = tm * tn * sp, slots = 256 * shapes[s].per_cu;
+            const int64_t rounds = (wgs + slots - 1) / slots;
+            double us = (double)rounds * ((double)((steps + sp - 1) / sp) + 3) * shapes[s].step;
+            if (sp > 1) us += 4.0 + 8.0 * sp * (double)M * N / 5e6;
+            if (us < best_us) {
+                best_us = us;
+                best.shape = s;
+                best.bm = shapes[s].bm;
+                best.bn = shapes[s].bn;
+                best.tiles_m = (int)tm;
+                best.tiles_n = (int)tn;
+                best.splits = sp;
+                best.part_bytes = sp > 1 ? 4ll * sp * M * N : 0;
+            }
+        }
+    }
+    return best;
+}
+
+namespace {
+template <class S>
+hipError_t launch_shape(TpKind kind, const TpArgs& P, bool part, hipStream_t st) {
+    const dim3 grid((unsigned)(P.tiles_m * P.tiles_n * P.splits)), blk(S::NT);
+    switch (kind) {
+        case TPK_LOGIT_STATS: hipLaunchKernelGGL((tile_product_kernel<S, true, true, TP_STATS>), grid, blk, 0, st, P); break;
+        case TPK_LOGIT_GRAD: hipLaunchKernelGGL((tile_product_kernel<S, true, true, TP_GRAD>), grid, blk, 0, st, P); break;
+        case TPK_STATES:
+            if (part) hipLaunchKernelGGL((tile_product_kernel<S, true, false, TP_PART>), grid, blk, 0, st, P);
+            else hipLaunchKernelGGL((tile_product_kernel<S, true, false, TP_STORE>), grid, blk, 0, st, P);
+            break;
+        case TPK_WEIGHTS:
+            if (part) hipLaunchKernelGGL((tile_product_kernel<S, false, false, TP_PART>), grid, blk, 0, st, P);
+            else hipLaunchKernelGGL((tile_product_kernel<S, false, false, TP_STORE>), grid, blk, 0, st, P);
+            break;
+    }
+    return hipGetLastError();
+}
+}  // namespace
+
+hipError_t launch_tp_reduce(const TpArgs& P, const float* acc, float* out_acc, hipStream_t st) {
+    const int64_t groups = (int64_t)P.M * ((P.N + 3) / 4);
+    const int64_t blocks = (groups + 255) / 256;
+    hipLaunchKernelGGL(tp_reduce_kernel, dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, st, P, acc,
+                       out_acc);
+    return hipGetLastError();
+}
+
+hipError_t launch_tile_product(TpKind kind, const TpPlan& plan, TpArgs P, const TpSum& sum, hipStream_t st) {
+    P.tiles_m = plan.tiles_m;
+    P.tiles_n = plan.tiles_n;
+    P.splits = plan.splits;
+    P.c_vec = P.C && (P.ldc & 3) == 0 && (P.N & 3) == 0 && ((uintptr_t)P.C & (P.c_bf16 ? 7 : 15)) == 0;
+    const bool part = (kind == TPK_STATES || kind == TPK_WEIGHTS) && (plan.splits > 1 || sum.acc || sum.out_acc);
+    hipError_t e = plan.shape == 0   ? launch_shape<Big>(kind, P, part, st)
+                   : plan.shape == 1 ? launch_shape<Mid>(kind, P, part, st)
+                                     : launch_shape<Small>(kind, P, part, st);
+    if (e != hipSuccess || !part) return e;
+    return launch_tp_reduce(P, sum.acc, sum.out_acc, st);
+}
+
+// zeros, by a kernel: the calls may be captured into a graph
+__global__ __launch_bounds__(256) void zero_kernel(uint16_t* p, int64_t n) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
+        gst(p + i, (uint16_t)0);
+}
+hipError_t launch_zero(void* p, int64_t bytes, hipStream_t st) {
+    const int64_t blocks = (bytes / 2 + 255) / 256;
+    if (blocks > 0)
+        hipLaunchKernelGGL(zero_kernel, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, st,
+                           (uint16_t*)p, bytes / 2);
+    return hipGetLastError();
+}
+
+// planes[p][r][c]: eight columns a thread (ld is a multiple of 8)
+template <typename E>
+__global__ __launch_bounds__(256) void to_planes_kernel(const E* __restrict__ src, int64_t rows, int64_t cols,
+                                                        uint16_t* __restrict__ dst, int64_t ld, int64_t plane,
+                                                        const int64_t* __restrict__ targets, int64_t vocab) {
+    const int64_t per_row = ld / 8, n = rows * per_row;
+    for (int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x; g < n; g += (int64_t)gridDim.x * 256) {
+        const int64_t r = g / per_row, c = (g - r * per_row) * 8;
+        const E* p = src + r * cols + c;
+        uint16_t* o = dst + r * ld + c;
+        const bool live = !targets || tp_target(targets, vocab, r) >= 0;
+        const int left = live ? (int)(cols - c < 8 ? cols - c : 8) : 0;
+        float f[8];
+        load8(p, left, f);
+        if constexpr (sizeof(E) == 2) {
+            store8(o, 8, f);  // exact
+        } else {
+            const Split8 s = split8(f);
+            *(SC_GLOBAL v8bf*)o = s.h;
+            *(SC_GLOBAL v8bf*)(o + plane) = s.m;
+            *(SC_GLOBAL v8bf*)(o + 2 * plane) = s.l;
+        }
+    }
+}
+
+hipError_t launch_to_planes(bool bf16, const void* src, int64_t rows, int64_t cols, uint16_t* dst, int64_t ld,
+                            int64_t plane, const int64_t* targets, int64_t vocab, hipStream_t st) {
+    const int64_t n = rows * (ld / 8);
+    if (n <= 0) return hipSuccess;
+    const int64_t blocks = (n + 255) / 256;
+    const dim3 grid((unsigned)(blocks < 65536 ? blocks : 65536));
+    if (bf16)
+        hipLaunchKernelGGL(to_planes_kernel<uint16_t>, grid, dim3(256), 0, st, (const uint16_t*)src, rows, cols, dst,
+                           ld, plane, targets, vocab);
+    else
+        hipLaunchKernelGGL(to_planes_kernel<float>, grid, dim3(256), 0, st, (const float*)src, rows, cols, dst, ld,
+                           plane, targets, vocab);
+    return hipGetLastError();
+}
+
+}  // namespace scopt
