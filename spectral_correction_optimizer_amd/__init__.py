@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import collections
 import ctypes
+import functools
 import os
 
 import torch  # loaded first: libscopt then binds to torch's HIP runtime
@@ -467,14 +468,13 @@ gradients."""
 
 
 def _train_check(who, dtype, dev, *named):
-    """named: (name, tensor, dtype or None for `dtype`, shape)."""
+    """named: (name, tensor, dtype, shape)."""
     if dtype not in _DT:
         raise ValueError(f"{who}: tensors must be float32 or bfloat16, got {dtype}")
     if dev.type != "cuda":
         raise ValueError(f"{who}: tensors must be on a GPU, got {dev}")
     for name, t, dt, shape in named:
-        dt = dtype if dt is None else dt
-        if t.device != dev or t.dtype != dt or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        if t.dtype is not dt or t.shape != shape or t.device != dev or not t.is_contiguous():
             raise ValueError(f"{who}: {name} must be a contiguous {dt} tensor of shape {tuple(shape)} on {dev}, "
                              f"got {t.dtype} {tuple(t.shape)} on {t.device}"
                              f"{'' if t.is_contiguous() else ' (not contiguous)'}")
@@ -494,16 +494,24 @@ def _at16(t):
 def _run(dev, fn, *args):
     """Call with the device current and its stream last."""
     if dev.index == torch.cuda.current_device():
-        _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+        rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+            rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if rc:
+        _check(rc)
 
 
-def _workspace(dev, query, *args):
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(query, *sizes):
     n = ctypes.c_int64()
-    _check(query(*args, ctypes.byref(n)))
-    return torch.empty(n.value, dtype=torch.uint8, device=dev), n.value
+    _check(getattr(load_library(), query)(*sizes, ctypes.byref(n)))
+    return n.value
+
+
+def _workspace(dev, query, *sizes):
+    n = _workspace_bytes(query, *sizes)
+    return torch.empty(n, dtype=torch.uint8, device=dev), n
 
 
 def _ptr(t):
@@ -514,7 +522,7 @@ def embed(table: "torch.Tensor", ids: "torch.Tensor", scale: float = 1.0) -> "to
     """scale * table[ids] (table [V, H], ids int64 of any shape); rows of zeros where an id is
     outside [0, V)."""
     V, H = _matrix("embed", "table", table)
-    _train_check("embed", table.dtype, table.device, ("table", table, None, (V, H)),
+    _train_check("embed", table.dtype, table.device, ("table", table, table.dtype, (V, H)),
                  ("ids", ids, torch.int64, ids.shape))
     out = torch.empty((*ids.shape, H), dtype=table.dtype, device=table.device)
     _run(table.device, load_library().sc_embed, _DT[table.dtype], table.data_ptr(), ids.data_ptr(), ids.numel(), V, H,
@@ -528,9 +536,9 @@ def embed_grad(dy: "torch.Tensor", ids: "torch.Tensor", V: int, scale: float = 1
     if dy.dim() < 1 or tuple(dy.shape[:-1]) != tuple(ids.shape):
         raise ValueError(f"embed_grad: dy {tuple(dy.shape)} must be ids {tuple(ids.shape)} and the hidden size")
     H = dy.shape[-1]
-    _train_check("embed_grad", dy.dtype, dy.device, ("dy", dy, None, dy.shape), ("ids", ids, torch.int64, ids.shape))
+    _train_check("embed_grad", dy.dtype, dy.device, ("dy", dy, dy.dtype, dy.shape), ("ids", ids, torch.int64, ids.shape))
     lib, T, V = load_library(), ids.numel(), int(V)
-    ws, n = _workspace(dy.device, lib.sc_embed_grad_workspace, T, V, H)
+    ws, n = _workspace(dy.device, "sc_embed_grad_workspace", T, V, H)
     dW = torch.empty((V, H), dtype=dy.dtype, device=dy.device)
     _run(dy.device, lib.sc_embed_grad, _DT[dy.dtype], dy.data_ptr(), ids.data_ptr(), T, V, H, float(scale),
          dW.data_ptr(), ws.data_ptr(), n)
@@ -540,7 +548,7 @@ def embed_grad(dy: "torch.Tensor", ids: "torch.Tensor", V: int, scale: float = 1
 def act_pack(x: "torch.Tensor") -> ActCheckpoint:
     """The 8-bit checkpoint of x [T, H]."""
     T, H = _matrix("act_pack", "x", x)
-    _train_check("act_pack", x.dtype, x.device, ("x", x, None, (T, H)))
+    _train_check("act_pack", x.dtype, x.device, ("x", x, x.dtype, (T, H)))
     q = torch.empty((T, H), dtype=torch.int8, device=x.device)
     e = torch.empty((T, -(-H // 32)), dtype=torch.uint8, device=x.device)
     _run(x.device, load_library().sc_act_pack, _DT[x.dtype], x.data_ptr(), T, H, q.data_ptr(), e.data_ptr())
@@ -565,9 +573,9 @@ def rmsnorm(x: "torch.Tensor", gain: "torch.Tensor", residual: "torch.Tensor" = 
     """h = x + residual (x without one), rstd = 1 / sqrt(mean(h^2) + eps), y = h * rstd * gain
     for rows of x [T, H], and with keep the 8-bit checkpoint of h * rstd for the backward pass."""
     T, H = _matrix("rmsnorm", "x", x)
-    named = [("x", x, None, (T, H)), ("gain", gain, None, (H,))]
+    named = [("x", x, x.dtype, (T, H)), ("gain", gain, x.dtype, (H,))]
     if residual is not None:
-        named.append(("residual", residual, None, (T, H)))
+        named.append(("residual", residual, x.dtype, (T, H)))
     dev = x.device
     _train_check("rmsnorm", x.dtype, dev, *named)
     h = x if residual is None else torch.empty_like(x)
@@ -588,14 +596,14 @@ def rmsnorm_grad(dy: "torch.Tensor", gain: "torch.Tensor", rstd: "torch.Tensor",
     """(dx, dgain) of rmsnorm from its checkpoint: dx [T, H] is the gradient of x and of the
     residual, with dh, the gradient that reaches h past the norm, added; dgain float32 [H]."""
     T, H = _matrix("rmsnorm_grad", "dy", dy)
-    named = [("dy", dy, None, (T, H)), ("gain", gain, None, (H,)), ("rstd", rstd, torch.float32, (T,))]
+    named = [("dy", dy, dy.dtype, (T, H)), ("gain", gain, dy.dtype, (H,)), ("rstd", rstd, torch.float32, (T,))]
     if dh is not None:
-        named.append(("dh", dh, None, (T, H)))
+        named.append(("dh", dh, dy.dtype, (T, H)))
     dev = dy.device
     _train_check("rmsnorm_grad", dy.dtype, dev, *named)
     _check_kept("rmsnorm_grad", kept, T, H, dy.dtype, dev)
     lib = load_library()
-    ws, n = _workspace(dev, lib.sc_rmsnorm_grad_workspace, T, H)
+    ws, n = _workspace(dev, "sc_rmsnorm_grad_workspace", T, H)
     dx = torch.empty_like(dy)
     dgain = torch.empty(H, dtype=torch.float32, device=dev)
     _run(dev, lib.sc_rmsnorm_grad, _DT[dy.dtype], dy.data_ptr(), gain.data_ptr(), rstd.data_ptr(), kept.q.data_ptr(),
@@ -609,14 +617,14 @@ def act_wgrad(dy: "torch.Tensor", kept: ActCheckpoint, gain: "torch.Tensor" = No
     T, N = _matrix("act_wgrad", "dy", dy)
     H = _matrix("act_wgrad", "q", kept.q)[1]
     dev = dy.device
-    named = [("dy", dy, None, (T, N))]
+    named = [("dy", dy, dy.dtype, (T, N))]
     if gain is not None:
-        named.append(("gain", gain, None, (H,)))
+        named.append(("gain", gain, dy.dtype, (H,)))
     _train_check("act_wgrad", dy.dtype, dev, *named)
     _check_kept("act_wgrad", kept, T, H, dy.dtype, dev)
     lib = load_library()
     dy = _at16(dy)
-    ws, n = _workspace(dev, lib.sc_act_wgrad_workspace, _DT[dy.dtype], T, N, H)
+    ws, n = _workspace(dev, "sc_act_wgrad_workspace", _DT[dy.dtype], T, N, H)
     dW = torch.empty((N, H), dtype=dy.dtype, device=dev)
     _run(dev, lib.sc_act_wgrad, _DT[dy.dtype], dy.data_ptr(), kept.q.data_ptr(), kept.e.data_ptr(), _ptr(gain), T, N,
          H, dW.data_ptr(), ws.data_ptr(), n)
@@ -631,11 +639,11 @@ def xent(h: "torch.Tensor", W: "torch.Tensor", targets: "torch.Tensor", limit: i
     T, H = _matrix("xent", "h", h)
     V = _matrix("xent", "W", W)[0]
     dev = h.device
-    _train_check("xent", h.dtype, dev, ("h", h, None, (T, H)), ("W", W, None, (V, H)),
+    _train_check("xent", h.dtype, dev, ("h", h, h.dtype, (T, H)), ("W", W, h.dtype, (V, H)),
                  ("targets", targets, torch.int64, (T,)))
     lib = load_library()
     h, W = _at16(h), _at16(W)
-    ws, n = _workspace(dev, lib.sc_xent_workspace, _DT[h.dtype], T, V, H, int(limit))
+    ws, n = _workspace(dev, "sc_xent_workspace", _DT[h.dtype], T, V, H, int(limit))
     loss = torch.empty(T, dtype=torch.float32, device=dev)
     mean = torch.empty((), dtype=torch.float32, device=dev)
     dh, dW = torch.empty_like(h), torch.empty_like(W)

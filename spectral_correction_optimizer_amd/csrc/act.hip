@@ -22,174 +22,230 @@ namespace scopt {
 namespace {
 int64_t up(int64_t n, int64_t a) { return (n + a - 1) / a * a; }
 
-// sum over the TPR threads of a row; red: one float per wave
-template <int TPR>
-__device__ __forceinline__ float row_sum(float v, float* red) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-    if constexpr (TPR > 64) {
-        __syncthreads();
-        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-        __syncthreads();
-        v = 0.0f;
-#pragma unroll
-        for (int w = 0; w < TPR / 64; ++w) v += red[w];
-    }
-    return v;
-}
 }  // namespace
 
-// Every group of 8 elements is a thread's; blocks of a row's end are cut, and the four
-// threads of a block are neighbours in a wave.
-template <typename E>
+// A thread converts kGroups groups of 8 elements.  The four threads of a block of 32 are neighbours in a wave, and whole blocks
+// leave the loop together (groups and strides are multiples of 4).
+template <typename E, int ENDS>
 __global__ __launch_bounds__(256) void act_pack_kernel(const E* __restrict__ x, int64_t T, int H, int8_t* q,
                                                        uint8_t* e) {
-    const int nb = (H + kActBlock - 1) / kActBlock;
-    const int64_t groups = T * nb * 4;
-    // whole blocks leave the loop together: groups and the stride are multiples of 4
-    for (int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x; g < groups; g += (int64_t)gridDim.x * 256) {
-        const int64_t t = g / (nb * 4);
-        const int in = (int)(g - t * (nb * 4)), c = in * 8, left = H - c;
-        float v[8];
-        load8(x + t * H + c, left, v);
-        int8_t k[8];
-        uint8_t ex;
-        act_encode8(v, k, ex);
-        store_q8(q + t * H + c, left, k);
-        if ((in & 3) == 0) gst(e + t * nb + in / 4, ex);
+    const int nb = (H + kActBlock - 1) / kActBlock, per_row = nb * 4;
+    const int64_t n = T * per_row;
+    const bool small = n < (int64_t)1 << 31;
+    for (int64_t g0 = (int64_t)blockIdx.x * 256 * kGroups + threadIdx.x; g0 < n;
+         g0 += (int64_t)gridDim.x * 256 * kGroups) {
+        Group8<E, ENDS> w[kGroups];
+        int64_t t[kGroups];
+        int in[kGroups];
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k) {
+            const int64_t g = g0 + k * 256;
+            split_group(g < n ? g : n - 4 + (threadIdx.x & 3), per_row, small, t[k], in[k]);
+            w[k].load(x + t[k] * H, in[k] * 8, H);
+        }
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k) {
+            const int c = in[k] * 8;
+            float v[8];
+            value8(w[k], c, H, v);
+            int8_t o[8];
+            uint8_t ex;
+            act_encode8(v, o, ex);
+            if (g0 + k * 256 >= n) continue;
+            store_q8(q + t[k] * H + c, H - c, o);
+            if ((in[k] & 3) == 0) gst(e + t[k] * nb + in[k] / 4, ex);
+        }
     }
 }
 
-template <typename E>
+// ld: columns of a row of x, zeros from H on
+template <typename E, int ENDS>
 __global__ __launch_bounds__(256) void act_unpack_kernel(const int8_t* __restrict__ q, const uint8_t* __restrict__ e,
                                                          int64_t T, int H, int64_t ld, E* x) {
     const int nb = (H + kActBlock - 1) / kActBlock, per_row = (int)((ld + 7) / 8);
-    const int64_t groups = T * per_row;
-    for (int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x; g < groups; g += (int64_t)gridDim.x * 256) {
-        const int64_t t = g / per_row;
-        const int c = (int)(g - t * per_row) * 8, left = H - c;
-        float v[8];
-        if (left > 0) {
-            load_q8(q + t * H + c, left, act_step(gld(e + t * nb + c / kActBlock)), v);
-        } else {
+    const int64_t n = T * per_row;
+    const bool small = n < (int64_t)1 << 31;
+    for (int64_t g0 = (int64_t)blockIdx.x * 256 * kGroups + threadIdx.x; g0 < n;
+         g0 += (int64_t)gridDim.x * 256 * kGroups) {
+        GroupQ8<ENDS> w[kGroups];
+        int64_t t[kGroups];
+        int in[kGroups];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+        for (int k = 0; k < kGroups; ++k) {
+            const int64_t g = g0 + k * 256;
+            split_group(g < n ? g : n - 1, per_row, small, t[k], in[k]);
+            w[k].load(q + t[k] * H, e + t[k] * nb, in[k] * 8, H);
         }
-        store8(x + t * ld + c, (int)(ld - c), v);  // bfloat16: exact, 8 significant bits
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k) {
+            const int c = in[k] * 8;
+            float v[8];
+            w[k].value(c, H, v);
+            if (g0 + k * 256 < n) store8(x + t[k] * ld + c, (int)(ld - c), v);  // bfloat16: exact, 8 significant bits
+        }
     }
 }
 
-template <typename E, int TPR, int C>
-__global__ __launch_bounds__(256) void rmsnorm_kernel(const E* __restrict__ x, const E* __restrict__ res,
-                                                      const E* __restrict__ gain, float eps, int64_t T, int H,
-                                                      E* h, E* y, float* rstd, int8_t* q, uint8_t* e) {
-    __shared__ float red[4];
-    const int in = threadIdx.x % TPR;
-    const int64_t t = (int64_t)blockIdx.x * (256 / TPR) + threadIdx.x / TPR;
-    if (t >= T) return;  // a whole wave, or (TPR 256) no row
-    const int nb = (H + kActBlock - 1) / kActBlock;
-    float v[C][8];
-    float ss = 0.0f;
+// Sum over the TPR threads of a row: `red` holds a float per wave, twice, and is used in turn
+// (`turn`), so that one barrier a row is enough.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float (*red)[TPR / 64], int turn) {
 #pragma unroll
-    for (int j = 0; j < C; ++j) {
-        const int c = (j * TPR + in) * 8;
-        load8(x + t * H + c, H - c, v[j]);
+    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+    if constexpr (TPR > 64) {
+        if ((threadIdx.x & 63) == 0) red[turn][threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < TPR / 64; ++w) v += red[turn][w];
     }
-    if (res) {
+    return v;
+}
+
+// Rows beyond the grid's are taken in turn.
+template <typename E, int ENDS, int TPR, int C>
+__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rmsnorm_kernel(const E* __restrict__ x,
+                                                                        const E* __restrict__ res,
+                                                                        const E* __restrict__ gain, float eps,
+                                                                        int64_t T, int H, E* h, E* y, float* rstd,
+                                                                        int8_t* q, uint8_t* e) {
+    constexpr int ROWS = TPR > 256 ? 1 : 256 / TPR;
+    __shared__ float red[2][TPR / 64];
+    const int in = threadIdx.x % TPR;
+    const int nb = (H + kActBlock - 1) / kActBlock;
+    int turn = 0;
+    for (int64_t t = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR; t < T;  // wave-uniform
+         t += (int64_t)gridDim.x * ROWS, turn ^= 1) {
+        Group8<E, ENDS> xw[C], rw[C], gw[C];
+#pragma unroll
+        for (int j = 0; j < C; ++j) xw[j].load(x + t * H, (j * TPR + in) * 8, H);
+        if (res) {
+#pragma unroll
+            for (int j = 0; j < C; ++j) rw[j].load(res + t * H, (j * TPR + in) * 8, H);
+        }
+#pragma unroll
+        for (int j = 0; j < C; ++j) gw[j].load(gain, (j * TPR + in) * 8, H);
+        float v[C][8], ss = 0.0f;
+#pragma unroll
+        for (int j = 0; j < C; ++j) value8(xw[j], (j * TPR + in) * 8, H, v[j]);
+        if (res) {
+#pragma unroll
+            for (int j = 0; j < C; ++j) {
+                float r[8];
+                value8(rw[j], (j * TPR + in) * 8, H, r);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[j][i] += r[i];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < C; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss = fmaf(v[j][i], v[j][i], ss);
+        ss = row_sum<TPR>(ss, red, turn);
+        const float rs = 1.0f / sqrtf(ss / (float)H + eps);
+        if (in == 0) gst(rstd + t, rs);
 #pragma unroll
         for (int j = 0; j < C; ++j) {
-            const int c = (j * TPR + in) * 8;
-            float r[8];
-            load8(res + t * H + c, H - c, r);
+            const int c = (j * TPR + in) * 8, left = H - c;
+            if (h && left > 0) store8(h + t * H + c, left, v[j]);
+            float g[8], o[8];
+            value8(gw[j], c, H, g);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[j][i] += r[i];
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < C; ++j)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(v[j][i], v[j][i], ss);
-    ss = row_sum<TPR>(ss, red);
-    const float rs = 1.0f / sqrtf(ss / (float)H + eps);
-    if (in == 0) gst(rstd + t, rs);
-#pragma unroll
-    for (int j = 0; j < C; ++j) {
-        const int c = (j * TPR + in) * 8, left = H - c;
-        if (h && left > 0) store8(h + t * H + c, left, v[j]);
-        float g[8], o[8];
-        if (left > 0) load8(gain + c, left, g);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            v[j][i] *= rs;  // the norm of the float32 sum, not of the rounded h
-            o[i] = left > 0 ? v[j][i] * g[i] : 0.0f;
-        }
-        if (left > 0) store8(y + t * H + c, left, o);
-        if (q) {
-            int8_t k[8];
-            uint8_t ex;
-            act_encode8(v[j], k, ex);
-            if (left > 0) {
-                store_q8(q + t * H + c, left, k);
-                if ((in & 3) == 0) gst(e + t * nb + c / kActBlock, ex);
+            for (int i = 0; i < 8; ++i) {
+                v[j][i] *= rs;  // the norm of the float32 sum, not of the rounded h
+                o[i] = v[j][i] * g[i];
+            }
+            if (left > 0) store8(y + t * H + c, left, o);
+            if (q) {
+                int8_t k[8];
+                uint8_t ex;
+                act_encode8(v[j], k, ex);
+                if (left > 0) {
+                    store_q8(q + t * H + c, left, k);
+                    if ((in & 3) == 0) gst(e + t * nb + c / kActBlock, ex);
+                }
             }
         }
     }
 }
 
 // Rows are dealt to the workgroups in turn; each keeps its rows' sum of dy n in registers and
-// writes one row of `partial`, summed in a fixed order by rmsnorm_dgain_kernel.
-template <typename E, int TPR, int C>
-__global__ __launch_bounds__(256) void rmsnorm_grad_kernel(const E* __restrict__ dy, const E* __restrict__ gain,
-                                                           const float* __restrict__ rstd,
-                                                           const int8_t* __restrict__ q,
-                                                           const uint8_t* __restrict__ e, const E* __restrict__ dh,
-                                                           int64_t T, int H, E* dx, float* partial) {
-    constexpr int ROWS = 256 / TPR;
-    __shared__ float red[4];
+// writes one row of `partial`, summed in a fixed order by rmsnorm_dgain_kernel.  Where the
+// registers allow (C <= 2) a row is fetched while the one before it is worked on.
+template <typename E, int ENDS, int C> struct NormGradRow {
+    Group8<E, ENDS> dy[C], dh[C];
+    GroupQ8<ENDS> n[C];
+    float rs;
+};
+template <typename E, int ENDS, int TPR, int C>
+__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rmsnorm_grad_kernel(
+    const E* __restrict__ dy, const E* __restrict__ gain, const float* __restrict__ rstd,
+    const int8_t* __restrict__ q, const uint8_t* __restrict__ e, const E* __restrict__ dh, int64_t T, int H, E* dx,
+    float* partial) {
+    constexpr int ROWS = TPR > 256 ? 1 : 256 / TPR;
+    __shared__ float red[2][TPR / 64];
     __shared__ float sums[ROWS > 1 ? TPR * 8 : 1];
     const int in = threadIdx.x % TPR, row = threadIdx.x / TPR;
     const int nb = (H + kActBlock - 1) / kActBlock;
     float g[C][8], dg[C][8];
 #pragma unroll
     for (int j = 0; j < C; ++j) {
-        const int c = (j * TPR + in) * 8;
-        load8(gain + c, H - c, g[j]);
+        load8<ENDS>(gain, (j * TPR + in) * 8, H, g[j]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) dg[j][i] = 0.0f;
     }
-    for (int64_t t = (int64_t)blockIdx.x * ROWS + row; t < T; t += (int64_t)gridDim.x * ROWS) {
-        float a[C][8], n[C][8];
-        const float rs = gld(rstd + t);
-        float dot = 0.0f;
+    const int64_t stride = (int64_t)gridDim.x * ROWS;
+    auto fetch = [&](int64_t t, NormGradRow<E, ENDS, C>& r) __attribute__((always_inline)) {
+        r.rs = gld(rstd + t);
 #pragma unroll
         for (int j = 0; j < C; ++j) {
-            const int c = (j * TPR + in) * 8, left = H - c;
-            load8(dy + t * H + c, left, a[j]);
-            load_q8(q + t * H + c, left, left > 0 ? act_step(gld(e + t * nb + c / kActBlock)) : 0.0f, n[j]);
+            const int c = (j * TPR + in) * 8;
+            r.dy[j].load(dy + t * H, c, H);
+            r.n[j].load(q + t * H, e + t * nb, c, H);
         }
+        if (dh) {
 #pragma unroll
-        for (int j = 0; j < C; ++j)
+            for (int j = 0; j < C; ++j) r.dh[j].load(dh + t * H, (j * TPR + in) * 8, H);
+        }
+    };
+    constexpr bool AHEAD = C <= 2;
+    NormGradRow<E, ENDS, C> cur, next;
+    int64_t t = (int64_t)blockIdx.x * ROWS + row;
+    int turn = 0;
+    if (AHEAD && t < T) fetch(t, next);
+    for (; t < T; t += stride, turn ^= 1) {
+        if (AHEAD) {
+            cur = next;
+            fetch(t + stride < T ? t + stride : t, next);
+        } else {
+            fetch(t, cur);
+        }
+        float a[C][8], n[C][8], dot = 0.0f;
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            value8(cur.dy[j], (j * TPR + in) * 8, H, a[j]);
+            cur.n[j].value((j * TPR + in) * 8, H, n[j]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 dg[j][i] = fmaf(a[j][i], n[j][i], dg[j][i]);
                 a[j][i] *= g[j][i];
                 dot = fmaf(a[j][i], n[j][i], dot);
             }
-        const float c1 = row_sum<TPR>(dot, red) / (float)H;
+        }
+        const float c1 = row_sum<TPR>(dot, red, turn) / (float)H;
 #pragma unroll
         for (int j = 0; j < C; ++j) {
             const int c = (j * TPR + in) * 8, left = H - c;
-            if (left <= 0) continue;
             float d[8];
             if (dh) {
-                load8(dh + t * H + c, left, d);
+                value8(cur.dh[j], c, H, d);
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) d[i] = 0.0f;
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) d[i] = fmaf(rs, fmaf(-n[j][i], c1, a[j][i]), d[i]);
-            store8(dx + t * H + c, left, d);
+            for (int i = 0; i < 8; ++i) d[i] = fmaf(cur.rs, fmaf(-n[j][i], c1, a[j][i]), d[i]);
+            if (left > 0) store8(dx + t * H + c, left, d);
         }
     }
     float* out = partial + (int64_t)blockIdx.x * H;
@@ -218,19 +274,25 @@ __global__ __launch_bounds__(256) void rmsnorm_grad_kernel(const E* __restrict__
     }
 }
 
-// 64 columns a workgroup, 16 groups of partial rows
+// 16 columns a workgroup, 64 groups of partial rows
 __global__ __launch_bounds__(1024) void rmsnorm_dgain_kernel(const float* __restrict__ partial, int parts, int H,
                                                              float* __restrict__ dgain) {
-    __shared__ float red[16][64];
-    const int lane = threadIdx.x & 63, grp = threadIdx.x >> 6;
-    const int c = blockIdx.x * 64 + lane;
+    __shared__ float red[16][16];
+    const int col = threadIdx.x & 15, grp = threadIdx.x >> 4;
+    const int c = blockIdx.x * 16 + col;
     float s = 0.0f;
-    if (c < H)
-        for (int p = grp; p < parts; p += 16) s += gld(partial + (int64_t)p * H + c);
-    red[grp][lane] = s;
+    if (c < H) {
+#pragma unroll 8
+        for (int p = grp; p < parts; p += 64) s += gld(partial + (int64_t)p * H + c);
+    }
+    s += __shfl_xor(s, 16);
+    s += __shfl_xor(s, 32);
+    if ((threadIdx.x & 63) < 16) red[threadIdx.x >> 6][col] = s;
     __syncthreads();
-    if (grp == 0 && c < H) {
-        for (int k = 1; k < 16; ++k) s += red[k][lane];
+    if (threadIdx.x < 16 && c < H) {
+        s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) s += red[k][col];
         gst(dgain + c, s);
     }
 }
@@ -244,22 +306,22 @@ dim3 grid_of(int64_t threads) {
 
 hipError_t launch_act_pack(bool bf16, const void* x, int64_t T, int H, int8_t* q, uint8_t* e, hipStream_t st) {
     if (T <= 0) return hipSuccess;
-    const dim3 grid = grid_of(T * ((H + kActBlock - 1) / kActBlock) * 4);
-    if (bf16)
-        hipLaunchKernelGGL(act_pack_kernel<uint16_t>, grid, dim3(256), 0, st, (const uint16_t*)x, T, H, q, e);
-    else
-        hipLaunchKernelGGL(act_pack_kernel<float>, grid, dim3(256), 0, st, (const float*)x, T, H, q, e);
+    const dim3 grid = grid_of((T * ((H + kActBlock - 1) / kActBlock) * 4 + kGroups - 1) / kGroups);
+#define SC_PACK(E_, ENDS_) \
+    hipLaunchKernelGGL((act_pack_kernel<E_, ENDS_>), grid, dim3(256), 0, st, (const E_*)x, T, H, q, e);
+    SC_BY_ENDS(bf16, H, SC_PACK)
+#undef SC_PACK
     return hipGetLastError();
 }
 
 static hipError_t unpack_rows(bool bf16, const int8_t* q, const uint8_t* e, int64_t T, int H, int64_t ld, void* x,
                               hipStream_t st) {
     if (T <= 0) return hipSuccess;
-    const dim3 grid = grid_of(T * ((ld + 7) / 8));
-    if (bf16)
-        hipLaunchKernelGGL(act_unpack_kernel<uint16_t>, grid, dim3(256), 0, st, q, e, T, H, ld, (uint16_t*)x);
-    else
-        hipLaunchKernelGGL(act_unpack_kernel<float>, grid, dim3(256), 0, st, q, e, T, H, ld, (float*)x);
+    const dim3 grid = grid_of((T * ((ld + 7) / 8) + kGroups - 1) / kGroups);
+#define SC_UNPACK(E_, ENDS_) \
+    hipLaunchKernelGGL((act_unpack_kernel<E_, ENDS_>), grid, dim3(256), 0, st, q, e, T, H, ld, (E_*)x);
+    SC_BY_ENDS(bf16, H, SC_UNPACK)
+#undef SC_UNPACK
     return hipGetLastError();
 }
 
@@ -268,31 +330,61 @@ hipError_t launch_act_unpack(bool bf16, const int8_t* q, const uint8_t* e, int64
     return unpack_rows(bf16, q, e, T, H, H, x, st);
 }
 
-// thread layout of a row: TPR threads, C groups of 8 elements each
-#define SC_ROW_LAYOUTS(X)                                             \
-    if (H <= 512) { X(64, 1) } else if (H <= 1024) { X(64, 2) }       \
-    else if (H <= 2048) { X(64, 4) } else if (H <= 4096) { X(256, 2) } \
-    else if (H <= 8192) { X(256, 4) } else { X(256, 8) }
+// Threads and groups of 8 a row: a wave up to 2048 elements, a workgroup beyond.
+template <typename E, int ENDS, int TPR, int C, typename... A>
+static void norm_rows(int64_t T, hipStream_t st, A... args) {
+    constexpr int64_t rows = TPR > 256 ? 1 : 256 / TPR;
+    const int64_t b = (T + rows - 1) / rows;
+    hipLaunchKernelGGL((rmsnorm_kernel<E, ENDS, TPR, C>), dim3((unsigned)(b < 1 << 20 ? b : 1 << 20)),
+                       dim3(TPR > 256 ? TPR : 256), 0, st, args...);
+}
+template <typename E, int ENDS, typename... A>
+static void norm_ends(int64_t T, int H, hipStream_t st, A... args) {
+    if (ENDS == ROW_SHORT || H <= 512) norm_rows<E, ENDS, 64, 1>(T, st, args...);
+    else if constexpr (ENDS != ROW_SHORT) {
+        if (H <= 1024) norm_rows<E, ENDS, 64, 2>(T, st, args...);
+        else if (H <= 2048) norm_rows<E, ENDS, 64, 4>(T, st, args...);
+        else if (H <= 4096) norm_rows<E, ENDS, 256, 2>(T, st, args...);
+        else if (H <= 6144) norm_rows<E, ENDS, 256, 3>(T, st, args...);
+        else if (H <= 8192) norm_rows<E, ENDS, 256, 4>(T, st, args...);
+        else norm_rows<E, ENDS, 1024, 2>(T, st, args...);
+    }
+}
 
 hipError_t launch_rmsnorm(bool bf16, const void* x, const void* residual, const void* gain, float eps, int64_t T,
                           int H, void* h, void* y, float* rstd, int8_t* q, uint8_t* e, hipStream_t st) {
     if (T <= 0) return hipSuccess;
-#define SC_NORM_E(TPR_, C_, E_)                                                                              \
-    hipLaunchKernelGGL((rmsnorm_kernel<E_, TPR_, C_>), dim3((unsigned)((T + 256 / TPR_ - 1) / (256 / TPR_))), \
-                       dim3(256), 0, st, (const E_*)x, (const E_*)residual, (const E_*)gain, eps, T, H, (E_*)h, \
-                       (E_*)y, rstd, q, e);
-#define SC_NORM(TPR_, C_)                          \
-    if (bf16) { SC_NORM_E(TPR_, C_, uint16_t) }    \
-    else { SC_NORM_E(TPR_, C_, float) }
-    SC_ROW_LAYOUTS(SC_NORM)
+#define SC_NORM(E_, ENDS_)                                                                                     \
+    norm_ends<E_, ENDS_>(T, H, st, (const E_*)x, (const E_*)residual, (const E_*)gain, eps, T, H, (E_*)h, (E_*)y, \
+                         rstd, q, e);
+    SC_BY_ENDS(bf16, H, SC_NORM)
 #undef SC_NORM
-#undef SC_NORM_E
     return hipGetLastError();
 }
 
+// Partial rows of dgain, a workgroup's each: 1024, fewer where a row takes more registers
+// (two workgroups of 4 waves run on a CU, or one of 16).
 int64_t rmsnorm_grad_parts(int64_t T, int H) {
-    const int64_t wgs = H <= 2048 ? (T + 3) / 4 : T;
-    return wgs < 1024 ? wgs : 1024;
+    const int64_t wgs = H <= 1024 ? (T + 3) / 4 : T, most = H <= 4096 ? 1024 : H <= 8192 ? 512 : 256;
+    return wgs < most ? wgs : most;
+}
+
+template <typename E, int ENDS, int TPR, int C, typename... A>
+static void grad_rows(int parts, hipStream_t st, A... args) {
+    hipLaunchKernelGGL((rmsnorm_grad_kernel<E, ENDS, TPR, C>), dim3((unsigned)parts), dim3(TPR > 256 ? TPR : 256), 0,
+                       st, args...);
+}
+template <typename E, int ENDS, typename... A>
+static void grad_ends(int parts, int H, hipStream_t st, A... args) {
+    if (ENDS == ROW_SHORT || H <= 512) grad_rows<E, ENDS, 64, 1>(parts, st, args...);
+    else if constexpr (ENDS != ROW_SHORT) {
+        if (H <= 1024) grad_rows<E, ENDS, 64, 2>(parts, st, args...);
+        else if (H <= 2048) grad_rows<E, ENDS, 256, 1>(parts, st, args...);
+        else if (H <= 4096) grad_rows<E, ENDS, 256, 2>(parts, st, args...);
+        else if (H <= 6144) grad_rows<E, ENDS, 256, 3>(parts, st, args...);
+        else if (H <= 8192) grad_rows<E, ENDS, 256, 4>(parts, st, args...);
+        else grad_rows<E, ENDS, 1024, 2>(parts, st, args...);
+    }
 }
 
 hipError_t launch_rmsnorm_grad(bool bf16, const void* dy, const void* gain, const float* rstd, const int8_t* q,
@@ -300,19 +392,15 @@ hipError_t launch_rmsnorm_grad(bool bf16, const void* dy, const void* gain, cons
                                float* partial, hipStream_t st) {
     const int parts = (int)rmsnorm_grad_parts(T, H);
     if (T > 0) {
-#define SC_GRAD_E(TPR_, C_, E_)                                                                                 \
-    hipLaunchKernelGGL((rmsnorm_grad_kernel<E_, TPR_, C_>), dim3((unsigned)parts), dim3(256), 0, st,            \
-                       (const E_*)dy, (const E_*)gain, rstd, q, e, (const E_*)dh, T, H, (E_*)dx, partial);
-#define SC_GRAD(TPR_, C_)                          \
-    if (bf16) { SC_GRAD_E(TPR_, C_, uint16_t) }    \
-    else { SC_GRAD_E(TPR_, C_, float) }
-        SC_ROW_LAYOUTS(SC_GRAD)
+#define SC_GRAD(E_, ENDS_)                                                                                      \
+    grad_ends<E_, ENDS_>(parts, H, st, (const E_*)dy, (const E_*)gain, rstd, q, e, (const E_*)dh, T, H, (E_*)dx, \
+                         partial);
+        SC_BY_ENDS(bf16, H, SC_GRAD)
 #undef SC_GRAD
-#undef SC_GRAD_E
         const hipError_t err = hipGetLastError();
         if (err != hipSuccess) return err;
     }
-    hipLaunchKernelGGL(rmsnorm_dgain_kernel, dim3((unsigned)((H + 63) / 64)), dim3(1024), 0, st, partial, parts, H,
+    hipLaunchKernelGGL(rmsnorm_dgain_kernel, dim3((unsigned)((H + 15) / 16)), dim3(1024), 0, st, partial, parts, H,
                        dgain);
     return hipGetLastError();
 }

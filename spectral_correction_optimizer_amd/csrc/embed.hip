@@ -9,14 +9,14 @@
 // commonest token of a text owns several percent of the rows), so the work is split evenly
 // over the sorted tokens and not over the table rows:
 //   1. embed_bin_count, embed_bin_scatter: stable partition of the tokens into at most 512
-//      bins of 2^shift neighbouring ids (one wavefront per block of tokens scatters, ranking
-//      64 tokens at a time by ballots);
-//   2. embed_bin_sort: each bin's tokens by id, and the table rows' starts;
-//   3. embed_sum: stretches of kRun sorted tokens, whatever their ids.  A table row
+//      bins of 2^shift neighbouring ids (each wavefront ranks its stretch of a block's
+//      tokens, 64 at a time, by ballots);
+//   2. embed_bin_sort: each bin's tokens by id in the same way, and the table rows' starts;
+//   3. embed_sum: stretches of 8 to 32 sorted tokens, whatever their ids.  A table row
 //      whose tokens lie within one stretch is stored at once; a row that crosses stretches
-//      leaves a float32 partial sum per stretch;
-//   4. embed_finish: zeros where a row has no token, the sum of the partials of a row that
-//      crossed.
+//      leaves a float32 partial sum per stretch.  Other workgroups of the same launch store
+//      the zeros of the rows without a token;
+//   4. embed_cross: the sum of the partials of each row that crossed.
 // Bound by HBM: dy read once, dW written once (most rows of a large table are zeros).
 #include "internal.hpp"
 #include "rows.hpp"
@@ -27,10 +27,32 @@ namespace scopt {
 namespace {
 constexpr int kBins = 512;     // most bins; also the scatter's workgroup size
 constexpr int kBlocks = 64;    // most token blocks
-constexpr int kRun = 32;       // sorted tokens of a stretch
+constexpr int kMaxRun = 32;    // most sorted tokens of a stretch
 constexpr int kSlab = 512;     // columns of a wavefront
 
 int64_t up(int64_t n, int64_t a) { return (n + a - 1) / a * a; }
+
+// Exclusive sum of v over the nw wavefronts of a workgroup; sums: nw ints.
+__device__ __forceinline__ int scan_exclusive(int v, int nw, int* sums) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int y = __shfl_up(x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 63) sums[wave] = x;
+    __syncthreads();
+    int before = 0;
+    for (int w = 0; w < nw; ++w) before += w < wave ? sums[w] : 0;
+    return before + x - v;
+}
+
+// LDS accesses of one wavefront stay in order; the compiler is told so
+__device__ __forceinline__ void wave_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
 
 // Among the 64 lanes with the same key (valid lanes): the mask of them.  `bits` key bits.
 __device__ __forceinline__ uint64_t same_key(uint32_t key, bool valid, int bits) {
@@ -43,25 +65,38 @@ __device__ __forceinline__ uint64_t same_key(uint32_t key, bool valid, int bits)
 }
 }  // namespace
 
-template <typename E>
+template <typename E, int ENDS>
 __global__ __launch_bounds__(256) void embed_kernel(const E* __restrict__ table, const int64_t* __restrict__ ids,
                                                     int64_t T, int64_t V, int H, float scale, E* out) {
     const int per_row = (H + 7) / 8;
     const int64_t n = T * per_row;
-    for (int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x; g < n; g += (int64_t)gridDim.x * 256) {
-        const int64_t t = g / per_row;
-        const int c = (int)(g - t * per_row) * 8;
-        const int64_t id = gld(ids + t);
-        float v[8];
-        if (id >= 0 && id < V) {
-            load8(table + id * H + c, H - c, v);
+    const bool small = n < (int64_t)1 << 31;
+    for (int64_t g0 = (int64_t)blockIdx.x * 256 * kGroups + threadIdx.x; g0 < n;
+         g0 += (int64_t)gridDim.x * 256 * kGroups) {
+        Group8<E, ENDS> w[kGroups];
+        int64_t t[kGroups], id[kGroups];
+        int in[kGroups];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] *= scale;
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+        for (int k = 0; k < kGroups; ++k) {
+            const int64_t g = g0 + k * 256;
+            split_group(g < n ? g : n - 1, per_row, small, t[k], in[k]);
+            id[k] = gld(ids + t[k]);
         }
-        store8(out + t * H + c, H - c, v);
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k) {
+            const bool real = id[k] >= 0 && id[k] < V;
+            w[k].load(table + (real ? id[k] : 0) * H, in[k] * 8, H);
+        }
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k) {
+            const int c = in[k] * 8;
+            const bool real = id[k] >= 0 && id[k] < V;
+            float v[8];
+            value8(w[k], c, H, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = real ? v[i] * scale : 0.0f;
+            if (g0 + k * 256 < n) store8(out + t[k] * H + c, H - c, v);
+        }
     }
 }
 
@@ -82,131 +117,151 @@ __global__ __launch_bounds__(256) void embed_bin_count_kernel(const int64_t* __r
 }
 
 // Stable scatter of a block's tokens to their bins: (id within the bin, token).  Every
-// workgroup sums the counts itself (at most kBlocks x kBins of them).
+// workgroup sums the counts itself (at most kBlocks x kBins of them); its 8 wavefronts take
+// a stretch of the tokens each.
 __global__ __launch_bounds__(kBins) void embed_bin_scatter_kernel(const int64_t* __restrict__ ids, int64_t T,
                                                                   int64_t V, int64_t per_block, int shift, int bins,
                                                                   int bin_bits, const int32_t* __restrict__ counts,
                                                                   int32_t* bin_start, int32_t* key, int32_t* pos) {
-    __shared__ int32_t scan[kBins], at[kBins];
-    const int b = threadIdx.x;
+    constexpr int NW = kBins / 64;
+    __shared__ int32_t at[NW][kBins];
+    __shared__ int sums[NW];
+    const int b = threadIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t from = (int64_t)blockIdx.x * per_block, to = from + per_block < T ? from + per_block : T;
+    const int64_t part = per_block / NW;  // a multiple of 64
+    const int64_t wfrom = from + wave * part, wto = wfrom + part < to ? wfrom + part : to;
+    for (int w = 0; w < NW; ++w) at[w][b] = 0;
+    __syncthreads();
+    for (int64_t t = wfrom + lane; t < wto; t += 64) {
+        const int64_t id = gld(ids + t);
+        if (id >= 0 && id < V) atomicAdd(&at[wave][id >> shift], 1);
+    }
     int before = 0, total = 0;
-    if (b < bins)
+    if (b < bins) {
+#pragma unroll 8
         for (unsigned k = 0; k < gridDim.x; ++k) {
             const int c = gld(counts + (int64_t)k * bins + b);
             total += c;
-            if (k < blockIdx.x) before += c;
+            before += k < blockIdx.x ? c : 0;
         }
-    scan[b] = total;
-    __syncthreads();
-    for (int o = 1; o < kBins; o <<= 1) {
-        const int x = b >= o ? scan[b - o] : 0;
-        __syncthreads();
-        scan[b] += x;
-        __syncthreads();
     }
-    const int start = scan[b] - total;
-    at[b] = start + before;
+    const int start = scan_exclusive(total, NW, sums);  // its barrier also ends the counting
     if (blockIdx.x == 0 && b < bins) {
         gst(bin_start + b, start);
         if (b == bins - 1) gst(bin_start + bins, start + total);
     }
+    int run = start + before;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        const int c = at[w][b];
+        at[w][b] = run;
+        run += c;
+    }
     __syncthreads();
-    if (threadIdx.x >= 64) return;
-    // one wavefront from here on: its LDS accesses stay in order
-    const int lane = threadIdx.x;
     const uint64_t below = (1ull << lane) - 1;
-    const int64_t from = (int64_t)blockIdx.x * per_block, to = from + per_block < T ? from + per_block : T;
-    int64_t next = from + lane < to ? gld(ids + from + lane) : -1;
-    for (int64_t t0 = from; t0 < to; t0 += 64) {
+    int64_t next = wfrom + lane < wto ? gld(ids + wfrom + lane) : -1;
+    for (int64_t t0 = wfrom; t0 < wto; t0 += 64) {
         const int64_t t = t0 + lane, id = next;
-        next = t + 64 < to ? gld(ids + t + 64) : -1;
+        next = t + 64 < wto ? gld(ids + t + 64) : -1;
         const bool valid = id >= 0 && id < V;
         const uint32_t bin = valid ? (uint32_t)(id >> shift) : 0;
         const uint64_t m = same_key(bin, valid, bin_bits);
         if (valid) {
-            const int base = at[bin];
-            const int o = base + __popcll(m & below);
+            const int o = at[wave][bin] + __popcll(m & below);
             gst(key + o, (int32_t)(id - ((int64_t)bin << shift)));
             gst(pos + o, (int32_t)t);
         }
-        __builtin_amdgcn_wave_barrier();
-        if (valid && (m & below) == 0) at[bin] += __popcll(m);
-        __builtin_amdgcn_wave_barrier();
+        wave_fence();
+        if (valid && (m & below) == 0) at[wave][bin] += __popcll(m);
+        wave_fence();
     }
 }
 
 // One bin: its tokens in id order (token order within an id), and the starts of its rows.
-__global__ __launch_bounds__(256) void embed_bin_sort_kernel(const int32_t* __restrict__ bin_start, int shift,
-                                                             int64_t V, const int32_t* __restrict__ key,
-                                                             const int32_t* __restrict__ pos, int32_t* row_start,
-                                                             int32_t* sorted_id, int32_t* sorted_pos) {
-    extern __shared__ int32_t at[];  // 2^shift counters, then starts
-    __shared__ int32_t sums[256];
-    const int rows = 1 << shift;
+// Each wavefront takes a stretch of the tokens; at: a counter per wavefront and row.
+__global__ __launch_bounds__(1024) void embed_bin_sort_kernel(const int32_t* __restrict__ bin_start, int shift,
+                                                              int64_t V, const int32_t* __restrict__ key,
+                                                              const int32_t* __restrict__ pos, int32_t* row_start,
+                                                              int32_t* sorted_id, int32_t* sorted_pos) {
+    extern __shared__ int32_t at[];
+    __shared__ int sums[16];
+    const int rows = 1 << shift, nt = blockDim.x, nw = nt >> 6;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int from = gld(bin_start + blockIdx.x), to = gld(bin_start + blockIdx.x + 1);
     const int64_t first = (int64_t)blockIdx.x << shift;
-    for (int r = threadIdx.x; r < rows; r += 256) at[r] = 0;
+    for (int i = threadIdx.x; i < nw * rows; i += nt) at[i] = 0;
     __syncthreads();
-    for (int i = from + threadIdx.x; i < to; i += 256) atomicAdd(&at[gld(key + i)], 1);
+    const int part = (to - from + nt - 1) / nt * 64;
+    const int wfrom = min(to, from + wave * part), wto = min(to, wfrom + part);
+    int32_t* mine = at + wave * rows;
+    for (int i = wfrom + lane; i < wto; i += 64) atomicAdd(&mine[gld(key + i)], 1);
     __syncthreads();
-    // exclusive scan: a thread's stretch of rows, then the threads' sums
-    const int per = (rows + 255) / 256, r0 = min(rows, (int)threadIdx.x * per), r1 = min(rows, r0 + per);
-    int mine = 0;
-    for (int r = r0; r < r1; ++r) mine += at[r];
-    sums[threadIdx.x] = mine;
-    __syncthreads();
-    for (int o = 1; o < 256; o <<= 1) {
-        const int x = (int)threadIdx.x >= o ? sums[threadIdx.x - o] : 0;
-        __syncthreads();
-        sums[threadIdx.x] += x;
-        __syncthreads();
-    }
-    int run = from + sums[threadIdx.x] - mine;
+    // a thread's stretch of rows; its rows' counts over the wavefronts
+    const int per = (rows + nt - 1) / nt, r0 = min(rows, (int)threadIdx.x * per), r1 = min(rows, r0 + per);
+    int n = 0;
+    for (int r = r0; r < r1; ++r)
+        for (int w = 0; w < nw; ++w) n += at[w * rows + r];
+    int run = from + scan_exclusive(n, nw, sums);
     for (int r = r0; r < r1; ++r) {
-        const int c = at[r];
-        at[r] = run;
         if (first + r < V) gst(row_start + first + r, run);
-        run += c;
+        for (int w = 0; w < nw; ++w) {
+            const int c = at[w * rows + r];
+            at[w * rows + r] = run;
+            run += c;
+        }
     }
     if (first + rows >= V && threadIdx.x == 0) gst(row_start + V, to);  // the last bin
     __syncthreads();
-    if (threadIdx.x >= 64) return;
-    const int lane = threadIdx.x;
     const uint64_t below = (1ull << lane) - 1;
-    int nk = from + lane < to ? gld(key + from + lane) : 0, np = from + lane < to ? gld(pos + from + lane) : 0;
-    for (int i0 = from; i0 < to; i0 += 64) {
+    int nk = wfrom + lane < wto ? gld(key + wfrom + lane) : 0, np = wfrom + lane < wto ? gld(pos + wfrom + lane) : 0;
+    for (int i0 = wfrom; i0 < wto; i0 += 64) {
         const int i = i0 + lane, k = nk, p = np;
-        if (i + 64 < to) {
+        if (i + 64 < wto) {
             nk = gld(key + i + 64);
             np = gld(pos + i + 64);
         }
-        const bool valid = i < to;
+        const bool valid = i < wto;
         const uint64_t m = same_key((uint32_t)k, valid, shift);
         if (valid) {
-            const int o = at[k] + __popcll(m & below);
+            const int o = mine[k] + __popcll(m & below);
             gst(sorted_id + o, (int32_t)(first + k));
             gst(sorted_pos + o, p);
         }
-        __builtin_amdgcn_wave_barrier();
-        if (valid && (m & below) == 0) at[k] += __popcll(m);
-        __builtin_amdgcn_wave_barrier();
+        wave_fence();
+        if (valid && (m & below) == 0) mine[k] += __popcll(m);
+        wave_fence();
     }
 }
 
-// A wavefront sums one stretch's rows over kSlab columns.
-template <typename E>
+// The first `sums` tasks: a wavefront sums one stretch's rows over kSlab columns.  The others:
+// the zeros of eight table rows without a token, over kSlab columns.
+template <typename E, int ENDS>
 __global__ __launch_bounds__(256) void embed_sum_kernel(const E* __restrict__ dy, int H, int64_t V, float scale,
-                                                        const int32_t* __restrict__ row_start,
+                                                        int len, const int32_t* __restrict__ row_start,
                                                         const int32_t* __restrict__ sorted_id,
-                                                        const int32_t* __restrict__ sorted_pos, int64_t tasks, int slabs,
-                                                        E* dW, float* partial) {
-    const int64_t task = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+                                                        const int32_t* __restrict__ sorted_pos, int64_t sums,
+                                                        int64_t tasks, int slabs, E* dW, float* partial) {
+    int64_t task = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     if (task >= tasks) return;
     const int lane = threadIdx.x & 63;
+    const bool zeros = task >= sums;
+    if (zeros) task -= sums;
     const int64_t run = task / slabs;
     const int c = (int)(task - run * slabs) * kSlab + lane * 8, left = H - c;
+    if (zeros) {
+        const int64_t v0 = run * 8;
+        const int my_start = gld(row_start + (v0 + lane < V ? v0 + lane : V));
+        const float none[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            if (v0 + r >= V) break;
+            if (__builtin_amdgcn_readlane(my_start, r) == __builtin_amdgcn_readlane(my_start, r + 1) && left > 0)
+                store8(dW + (v0 + r) * H + c, left, none);
+        }
+        return;
+    }
     const int total = gld(row_start + V);
-    const int from = (int)run * kRun, to = min(total, from + kRun);
+    const int from = (int)run * len, to = min(total, from + len);
     if (from >= to) return;
     // one token a lane; ids and rows are broadcast from there
     const int mine = min(from + lane, to - 1);
@@ -217,18 +272,20 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(const E* __restrict__ dy
     for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
     constexpr int U = 8;  // rows in flight
     for (int k0 = 0; k0 < to - from; k0 += U) {
-        float v[U][8];
+        Group8<E, ENDS> w[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {  // past the end: the last token's row again, not summed
             const int64_t p = __builtin_amdgcn_readlane(my_pos, min(k0 + u, to - from - 1));
-            load8(dy + p * H + c, left, v[u]);
+            w[u].load(dy + p * H, c, H);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int k = k0 + u;
             if (k >= to - from) break;
+            float v[8];
+            value8(w[u], c, H, v);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i] += v[u][i];
+            for (int i = 0; i < 8; ++i) acc[i] += v[i];
             const int end = __builtin_amdgcn_readlane(my_end, k);
             if (from + k + 1 == end || from + k + 1 == to) {  // the row's last token here
                 const int start = __builtin_amdgcn_readlane(my_start, k);
@@ -249,56 +306,58 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(const E* __restrict__ dy
     }
 }
 
-// Eight table rows a wavefront, over kSlab columns.
-template <typename E>
-__global__ __launch_bounds__(256) void embed_finish_kernel(int H, int64_t V, float scale,
-                                                           const int32_t* __restrict__ row_start,
-                                                           const float* __restrict__ partial, int64_t tasks, int slabs,
-                                                           E* dW) {
-    const int64_t task = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (task >= tasks) return;
-    const int lane = threadIdx.x & 63;
-    const int64_t v0 = task / slabs * 8;
-    const int c = (int)(task % slabs) * kSlab + lane * 8, left = H - c;
-    const int64_t at = v0 + (lane & 15) < V ? v0 + (lane & 15) : V;
-    const int my_start = gld(row_start + at);
+// The row, if any, that crosses into stretch k = blockIdx.x / slabs + 1 from the stretch where
+// it begins: the sum of its partials, a quarter of them a wavefront.
+template <typename E, int ENDS>
+__global__ __launch_bounds__(256) void embed_cross_kernel(int H, int64_t V, float scale, int len,
+                                                          const int32_t* __restrict__ row_start,
+                                                          const int32_t* __restrict__ sorted_id,
+                                                          const float* __restrict__ partial, int slabs, E* dW) {
+    __shared__ float red[3][kSlab];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int k = (int)(blockIdx.x / slabs) + 1;
+    const int c = (int)(blockIdx.x % slabs) * kSlab + lane * 8, left = H - c;
+    if (k * len >= gld(row_start + V)) return;
+    const int64_t id = gld(sorted_id + k * len);
+    const int s = gld(row_start + id), e = gld(row_start + id + 1);
+    if (s >= k * len || s < (k - 1) * len) return;
+    const int last = (e - 1) / len, n = last - k + 2;  // partials: the first stretch's second one, then first ones
+    const int per = (n + 3) / 4, p0 = min(n, wave * per), p1 = min(n, p0 + per);
+    float acc[8];
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-        if (v0 + r >= V) break;
-        const int s = __builtin_amdgcn_readlane(my_start, r), e = __builtin_amdgcn_readlane(my_start, r + 1);
-        float acc[8];
+    for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+#pragma unroll 4
+    for (int p = p0; p < p1; ++p) {
+        float v[8];
+        load8<ENDS>(partial + (2ll * (k - 1 + p) + (p == 0 ? 1 : 0)) * H, c, H, v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
-        if (s < e) {
-            const int first = s / kRun, last = (e - 1) / kRun;
-            if (first == last) continue;
-            if (left > 0) {
-                load8(partial + (2ll * first + 1) * H + c, left, acc);
-                for (int k = first + 1; k <= last; ++k) {
-                    float p[8];
-                    load8(partial + 2ll * k * H + c, left, p);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) acc[i] += p[i];
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i] *= scale;
-        }
-        if (left > 0) store8(dW + (v0 + r) * H + c, left, acc);
+        for (int i = 0; i < 8; ++i) acc[i] += v[i];
     }
+    if (wave > 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) red[wave - 1][i * 64 + lane] = acc[i];
+    }
+    __syncthreads();
+    if (wave > 0 || left <= 0) return;
+#pragma unroll
+    for (int w = 0; w < 3; ++w)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] += red[w][i * 64 + lane];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] *= scale;
+    store8(dW + id * H + c, left, acc);
 }
 
 hipError_t launch_embed(bool bf16, const void* table, const int64_t* ids, int64_t T, int64_t V, int H, float scale,
                         void* out, hipStream_t st) {
     if (T <= 0) return hipSuccess;
-    const int64_t blocks = (T * ((H + 7) / 8) + 255) / 256;
+    const int64_t blocks = (T * ((H + 7) / 8) + 256 * kGroups - 1) / (256 * kGroups);
     const dim3 grid((unsigned)(blocks < 65536 ? blocks : 65536));
-    if (bf16)
-        hipLaunchKernelGGL(embed_kernel<uint16_t>, grid, dim3(256), 0, st, (const uint16_t*)table, ids, T, V, H,
-                           scale, (uint16_t*)out);
-    else
-        hipLaunchKernelGGL(embed_kernel<float>, grid, dim3(256), 0, st, (const float*)table, ids, T, V, H, scale,
-                           (float*)out);
+#define SC_EMBED(E_, ENDS_)                                                                              \
+    hipLaunchKernelGGL((embed_kernel<E_, ENDS_>), grid, dim3(256), 0, st, (const E_*)table, ids, T, V, H, \
+                       scale, (E_*)out);
+    SC_BY_ENDS(bf16, H, SC_EMBED)
+#undef SC_EMBED
     return hipGetLastError();
 }
 
@@ -312,7 +371,11 @@ EmbedGradPlan embed_grad_plan(int64_t T, int64_t V, int64_t H) {
     p.per_block = up(T > 0 ? (T + kBlocks - 1) / kBlocks : 1, 1024);
     p.blocks = (T + p.per_block - 1) / p.per_block;
     if (p.blocks < 1) p.blocks = 1;
-    p.runs = (T + kRun - 1) / kRun;
+    // the longest stretches that still give the chip 16 wavefronts a CU
+    const int64_t slabs = (H + kSlab - 1) / kSlab;
+    p.len = kMaxRun;
+    while (p.len > 8 && T / p.len * slabs < 4096) p.len /= 2;
+    p.runs = (T + p.len - 1) / p.len;
     int64_t o = 0;
     auto take = [&](int64_t bytes) {
         const int64_t at = o;
@@ -347,23 +410,21 @@ hipError_t launch_embed_grad(const EmbedGradPlan& p, bool bf16, const void* dy, 
     hipLaunchKernelGGL(embed_bin_scatter_kernel, dim3((unsigned)p.blocks), dim3(kBins), 0, st, ids, p.T, p.V,
                        p.per_block, p.shift, p.bins, bin_bits, counts, bin, key, pos);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    hipLaunchKernelGGL(embed_bin_sort_kernel, dim3((unsigned)p.bins), dim3(256), sizeof(int32_t) << p.shift, st, bin,
-                       p.shift, p.V, key, pos, start, sid, spos);
+    // a counter per wavefront and row of the bin in LDS: at most 32 KB
+    const int waves = 8192 >> p.shift < 16 ? (8192 >> p.shift < 1 ? 1 : 8192 >> p.shift) : 16;
+    hipLaunchKernelGGL(embed_bin_sort_kernel, dim3((unsigned)p.bins), dim3(64 * waves),
+                       (waves * sizeof(int32_t)) << p.shift, st, bin, p.shift, p.V, key, pos, start, sid, spos);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    const int slabs = (int)((p.H + kSlab - 1) / kSlab);
-    const int64_t sums = p.runs * slabs, rows = (p.V + 7) / 8 * slabs;
-#define SC_EMBED(E_)                                                                                              \
-    if (sums > 0)                                                                                                 \
-        hipLaunchKernelGGL(embed_sum_kernel<E_>, dim3((unsigned)((sums + 3) / 4)), dim3(256), 0, st, (const E_*)dy, \
-                           (int)p.H, p.V, scale, start, sid, spos, sums, slabs, (E_*)dW, part);                   \
-    if ((e = hipGetLastError()) != hipSuccess) return e;                                                          \
-    hipLaunchKernelGGL(embed_finish_kernel<E_>, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, st, (int)p.H, p.V, \
-                       scale, start, part, rows, slabs, (E_*)dW)
-    if (bf16) {
-        SC_EMBED(uint16_t);
-    } else {
-        SC_EMBED(float);
-    }
+    const int H = (int)p.H, slabs = (H + kSlab - 1) / kSlab;
+    const int64_t sums = p.runs * slabs, tasks = sums + (p.V + 7) / 8 * slabs;
+#define SC_EMBED(E_, ENDS_)                                                                                        \
+    hipLaunchKernelGGL((embed_sum_kernel<E_, ENDS_>), dim3((unsigned)((tasks + 3) / 4)), dim3(256), 0, st,         \
+                       (const E_*)dy, H, p.V, scale, p.len, start, sid, spos, sums, tasks, slabs, (E_*)dW, part);  \
+    if ((e = hipGetLastError()) != hipSuccess) return e;                                                           \
+    if (p.runs > 1)                                                                                                \
+        hipLaunchKernelGGL((embed_cross_kernel<E_, ENDS_>), dim3((unsigned)((p.runs - 1) * slabs)), dim3(256), 0,  \
+                           st, H, p.V, scale, p.len, start, sid, part, slabs, (E_*)dW);
+    SC_BY_ENDS(bf16, p.H, SC_EMBED)
 #undef SC_EMBED
     return hipGetLastError();
 }

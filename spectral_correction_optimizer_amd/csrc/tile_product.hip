@@ -136,27 +136,43 @@ hipError_t launch_zero(void* p, int64_t bytes, hipStream_t st) {
     return hipGetLastError();
 }
 
-// planes[p][r][c]: eight columns a thread (ld is a multiple of 8)
-template <typename E>
-__global__ __launch_bounds__(256) void to_planes_kernel(const E* __restrict__ src, int64_t rows, int64_t cols,
+// planes[p][r][c]: kGroups groups of eight columns a thread (ld is a multiple of 8)
+template <typename E, int ENDS>
+__global__ __launch_bounds__(256) void to_planes_kernel(const E* __restrict__ src, int64_t rows, int cols,
                                                         uint16_t* __restrict__ dst, int64_t ld, int64_t plane,
                                                         const int64_t* __restrict__ targets, int64_t vocab) {
-    const int64_t per_row = ld / 8, n = rows * per_row;
-    for (int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x; g < n; g += (int64_t)gridDim.x * 256) {
-        const int64_t r = g / per_row, c = (g - r * per_row) * 8;
-        const E* p = src + r * cols + c;
-        uint16_t* o = dst + r * ld + c;
-        const bool live = !targets || tp_target(targets, vocab, r) >= 0;
-        const int left = live ? (int)(cols - c < 8 ? cols - c : 8) : 0;
-        float f[8];
-        load8(p, left, f);
-        if constexpr (sizeof(E) == 2) {
-            store8(o, 8, f);  // exact
-        } else {
-            const Split8 s = split8(f);
-            *(SC_GLOBAL v8bf*)o = s.h;
-            *(SC_GLOBAL v8bf*)(o + plane) = s.m;
-            *(SC_GLOBAL v8bf*)(o + 2 * plane) = s.l;
+    const int per_row = (int)(ld / 8);
+    const int64_t n = rows * per_row;
+    const bool small = n < (int64_t)1 << 31;
+    for (int64_t g0 = (int64_t)blockIdx.x * 256 * kGroups + threadIdx.x; g0 < n;
+         g0 += (int64_t)gridDim.x * 256 * kGroups) {
+        Group8<E, ENDS> w[kGroups];
+        int64_t r[kGroups], tgt[kGroups];
+        int in[kGroups];
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k) {
+            const int64_t g = g0 + k * 256;
+            split_group(g < n ? g : n - 1, per_row, small, r[k], in[k]);
+            w[k].load(src + r[k] * cols, in[k] * 8, cols);
+            tgt[k] = targets ? gld(targets + r[k]) : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k) {
+            if (g0 + k * 256 >= n) break;
+            uint16_t* o = dst + r[k] * ld + in[k] * 8;
+            const bool live = tgt[k] >= 0 && tgt[k] < vocab;
+            float f[8];
+            value8(w[k], in[k] * 8, cols, f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = live ? f[i] : 0.0f;
+            if constexpr (sizeof(E) == 2) {
+                store8(o, 8, f);  // exact
+            } else {
+                const Split8 s = split8(f);
+                *(SC_GLOBAL v8bf*)o = s.h;
+                *(SC_GLOBAL v8bf*)(o + plane) = s.m;
+                *(SC_GLOBAL v8bf*)(o + 2 * plane) = s.l;
+            }
         }
     }
 }
@@ -165,14 +181,14 @@ hipError_t launch_to_planes(bool bf16, const void* src, int64_t rows, int64_t co
                             int64_t plane, const int64_t* targets, int64_t vocab, hipStream_t st) {
     const int64_t n = rows * (ld / 8);
     if (n <= 0) return hipSuccess;
-    const int64_t blocks = (n + 255) / 256;
+    if (!targets) vocab = 1;  // every row counts
+    const int64_t blocks = (n + 256 * kGroups - 1) / (256 * kGroups);
     const dim3 grid((unsigned)(blocks < 65536 ? blocks : 65536));
-    if (bf16)
-        hipLaunchKernelGGL(to_planes_kernel<uint16_t>, grid, dim3(256), 0, st, (const uint16_t*)src, rows, cols, dst,
-                           ld, plane, targets, vocab);
-    else
-        hipLaunchKernelGGL(to_planes_kernel<float>, grid, dim3(256), 0, st, (const float*)src, rows, cols, dst, ld,
-                           plane, targets, vocab);
+#define SC_PLANES(E_, ENDS_)                                                                                         \
+    hipLaunchKernelGGL((to_planes_kernel<E_, ENDS_>), grid, dim3(256), 0, st, (const E_*)src, rows, (int)cols, dst, \
+                       ld, plane, targets, vocab);
+    SC_BY_ENDS(bf16, cols, SC_PLANES)
+#undef SC_PLANES
     return hipGetLastError();
 }
 

@@ -132,7 +132,8 @@ struct EmbedGradPlan {
     int64_t T, V, H;
     int shift, bins;     // ids of 2^shift rows share a bin
     int64_t per_block, blocks;  // tokens of a block, blocks
-    int64_t runs;               // stretches of sorted tokens
+    int len;                    // sorted tokens of a stretch
+    int64_t runs;               // stretches
     int64_t o_counts, o_bin, o_key, o_pos, o_id, o_spos, o_start, o_part, bytes;
 };
 EmbedGradPlan embed_grad_plan(int64_t T, int64_t V, int64_t H);

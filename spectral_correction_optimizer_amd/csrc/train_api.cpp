@@ -23,7 +23,7 @@ namespace {
         if (rc_) return rc_;  \
     } while (0)
 
-constexpr int64_t kMaxTokens = (int64_t)1 << 31;
+constexpr int64_t kMaxTokens = (int64_t)1 << 31;  // embedding gradient: half of it, its indexes are 32-bit
 constexpr int64_t kMaxVocab = (int64_t)1 << 22;
 constexpr int kMaxEmbedH = 1 << 24;
 constexpr int kNormMaxH = 16384;
@@ -56,6 +56,10 @@ int check_embed(int64_t T, int64_t V, int H) {
     SC_TRY(check_size("T", T, 0, kMaxTokens - 1));
     SC_TRY(check_size("V", V, 1, kMaxVocab));
     return check_size("H", H, 1, kMaxEmbedH);
+}
+int check_embed_grad(int64_t T, int64_t V, int H) {
+    SC_TRY(check_size("T", T, 0, kMaxTokens / 2 - 1));
+    return check_embed(T, V, H);
 }
 int check_rows(int64_t T, int H, int maxH) {
     SC_TRY(check_size("T", T, 0, kMaxTokens - 1));
@@ -93,7 +97,7 @@ int sc_embed(sc_dtype dtype, const void* table, const int64_t* ids, int64_t T, i
 }
 
 int sc_embed_grad_workspace(int64_t T, int64_t V, int H, int64_t* bytes) {
-    SC_TRY(check_embed(T, V, H));
+    SC_TRY(check_embed_grad(T, V, H));
     if (!bytes) return fail(SC_ERR_INVALID_ARG, "bytes is NULL");
     *bytes = embed_grad_plan(T, V, H).bytes;
     return SC_OK;
@@ -102,7 +106,7 @@ int sc_embed_grad_workspace(int64_t T, int64_t V, int H, int64_t* bytes) {
 int sc_embed_grad(sc_dtype dtype, const void* dy, const int64_t* ids, int64_t T, int64_t V, int H, float scale,
                   void* dW, void* workspace, int64_t workspace_bytes, void* stream) {
     SC_TRY(check_dtype(dtype));
-    SC_TRY(check_embed(T, V, H));
+    SC_TRY(check_embed_grad(T, V, H));
     const EmbedGradPlan p = embed_grad_plan(T, V, H);
     if (T > 0) {
         SC_TRY(check_ptr("dy", dy, elem(dtype)));
