@@ -492,12 +492,13 @@ def _at16(t):
 
 
 def _run(dev, fn, *args):
-    """Call with the device current and its stream last."""
+    """Call with the device current and its stream last (the raw handle: a Stream object costs a
+    small call 2 us of its 10)."""
     if dev.index == torch.cuda.current_device():
-        rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
     if rc:
         _check(rc)
 

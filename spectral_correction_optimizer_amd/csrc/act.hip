@@ -416,8 +416,8 @@ WgradPlan wgrad_plan(bool bf16, int64_t T, int64_t N, int64_t H) {
     p.N = N;
     p.H = H;
     p.planes = !bf16 || N % 8 != 0;
-    p.Np = p.planes ? up(N, 64) : N;
-    p.Hp = up(H, 64);
+    p.Np = p.planes ? tp_pad(up(N, 64)) : N;
+    p.Hp = tp_pad(up(H, 64));
     p.prod = tp_plan((int)N, (int)H, (int)T, bf16 ? 1 : 3, true);
     int64_t o = 0;
     auto take = [&](int64_t bytes) {

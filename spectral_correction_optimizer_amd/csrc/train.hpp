@@ -68,6 +68,8 @@ struct TpPlan {
     int splits = 1;
     int64_t part_bytes = 0;  // float32 partial sums (splits > 1)
 };
+// Row stride of an operand that the library lays out itself
+inline int64_t tp_pad(int64_t cols) { return cols % 512 == 0 ? cols + 64 : cols; }
 TpPlan tp_plan(int M, int N, int K, int nseg, bool may_split);
 // A product whose sums join others (TPK_STATES, TPK_WEIGHTS): acc is added before the store;
 // with out_acc the float32 sum goes there and C is not written.  Either asks for args.part
@@ -89,7 +91,7 @@ hipError_t launch_to_planes(bool bf16, const void* src, int64_t rows, int64_t co
 // ---- cross entropy (xent.hip) --------------------------------------------------------
 struct XentPlan {
     bool bf16, planes;         // planes: W is copied into planes (float32, or H % 8), as h always is
-    int64_t T, V, H, Hp;       // Hp: columns of the operands (padded when planes)
+    int64_t T, V, H, Hp, Hh;   // columns of W's operand (H, or padded when planes) and of h's
     int64_t piece;             // vocabulary rows of a piece
     int pieces;
     bool keep;                 // one piece whose probabilities are kept between the passes

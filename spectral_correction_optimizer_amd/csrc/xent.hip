@@ -154,7 +154,8 @@ XentPlan xent_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit) {
     p.V = V;
     p.H = H;
     p.planes = !bf16 || H % 8 != 0;
-    p.Hp = p.planes ? up(H, 64) : H;
+    p.Hp = p.planes ? tp_pad(up(H, 64)) : H;
+    p.Hh = tp_pad(up(H, 64));
     const int nseg = bf16 ? 1 : 6;
     // bytes of a vocabulary column: the kept exponentials, or the logits and d's planes
     const int64_t col_kept = T * (bf16 ? 2 : 10), col_piece = T * (bf16 ? 2 : 6);
@@ -166,10 +167,10 @@ XentPlan xent_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit) {
         if (p.piece > V) p.piece = V;
     }
     p.pieces = (int)((V + p.piece - 1) / p.piece);
-    p.ldp = up(p.piece, 64);
+    p.ldp = tp_pad(up(p.piece, 64));
     const int64_t last = V - (int64_t)(p.pieces - 1) * p.piece;
-    p.logits = tp_plan((int)T, (int)p.piece, (int)p.Hp, nseg, false);
-    p.logits_last = tp_plan((int)T, (int)last, (int)p.Hp, nseg, false);
+    p.logits = tp_plan((int)T, (int)p.piece, (int)H, nseg, false);
+    p.logits_last = tp_plan((int)T, (int)last, (int)H, nseg, false);
     p.dh = tp_plan((int)T, (int)H, (int)p.piece, nseg, true);
     p.dw = tp_plan((int)p.piece, (int)H, (int)T, nseg, true);
     p.dw_last = tp_plan((int)last, (int)H, (int)T, nseg, true);
@@ -182,7 +183,7 @@ XentPlan xent_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit) {
     };
     const int np = bf16 ? 1 : 3;
     p.o_scalars = take(sizeof(XentScalars));
-    p.o_h = take(2 * np * T * p.Hp);
+    p.o_h = take(2 * np * T * p.Hh);
     p.o_w = p.planes ? take(2 * np * V * p.Hp) : 0;
     p.o_s = !bf16 && p.keep ? take(4 * T * p.ldp) : 0;
     p.o_p = take(2 * np * T * p.ldp);
@@ -204,7 +205,7 @@ XentPlan xent_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit) {
 hipError_t launch_xent(const XentPlan& p, const void* h, const void* W, const int64_t* targets, float* loss,
                        float* mean, void* dh, void* dW, void* workspace, hipStream_t st) {
     char* ws = (char*)workspace;
-    const int64_t T = p.T, V = p.V, H = p.H, Hp = p.Hp;
+    const int64_t T = p.T, V = p.V, H = p.H, Hp = p.Hp, Hh = p.Hh;
     const int np = p.bf16 ? 1 : 3;
     XentScalars* sc = (XentScalars*)(ws + p.o_scalars);
     uint16_t* P = (uint16_t*)(ws + p.o_p);
@@ -226,7 +227,7 @@ hipError_t launch_xent(const XentPlan& p, const void* h, const void* W, const in
     // (a NaN too) reaches no product
     uint16_t* hp = (uint16_t*)(ws + p.o_h);
     const uint16_t* wp = (const uint16_t*)W;
-    SC_RUN(launch_to_planes(p.bf16, h, T, H, hp, Hp, T * Hp, targets, V, st));
+    SC_RUN(launch_to_planes(p.bf16, h, T, H, hp, Hh, T * Hh, targets, V, st));
     if (p.planes) {
         wp = (uint16_t*)(ws + p.o_w);
         SC_RUN(launch_to_planes(p.bf16, W, V, H, (uint16_t*)wp, Hp, V * Hp, nullptr, 0, st));
@@ -239,14 +240,14 @@ hipError_t launch_xent(const XentPlan& p, const void* h, const void* W, const in
         TpArgs a;
         const int64_t v0 = (int64_t)i * p.piece;
         a.A = hp;
-        a.lda = Hp;
-        a.a_plane = T * Hp;
+        a.lda = Hh;
+        a.a_plane = T * Hh;
         a.B = wp + v0 * Hp;
         a.ldb = Hp;
         a.b_plane = V * Hp;
         a.M = (int)T;
         a.N = (int)(V - v0 < p.piece ? V - v0 : p.piece);
-        a.K = (int)Hp;
+        a.K = (int)up(H, 8);
         a.nseg = nseg;
         a.segs = segs;
         a.targets = targets;
@@ -325,8 +326,8 @@ hipError_t launch_xent(const XentPlan& p, const void* h, const void* W, const in
         b.lda = p.ldp;
         b.a_plane = T * p.ldp;
         b.B = hp;
-        b.ldb = Hp;
-        b.b_plane = T * Hp;
+        b.ldb = Hh;
+        b.b_plane = T * Hh;
         b.M = n;
         b.N = (int)H;
         b.K = (int)T;
