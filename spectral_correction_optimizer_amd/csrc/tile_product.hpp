@@ -103,29 +103,30 @@ struct TpLoader {
     }
 };
 
-// Fragment reader of NB 16-row blocks starting at row w0 of a tile.
+// Fragment reader of NB 16-row blocks starting at row w0 of a tile (w0 / 16 is a multiple of
+// NB, a power of two: a block's offset differs from the first one's by an exclusive or).
 template <int R, int NB, bool KC>
 struct TpReader {
-    int off[KC ? 2 : NB];
+    int off;
     __device__ __forceinline__ void init(int w0) {
         const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
         if constexpr (KC) {
             const int f = (j & 7) ^ ((j >> 3) & 1);
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk) off[kk] = (w0 + j) * 64 + (((kk * 4 + g) ^ f) << 3);
+            off = (w0 + j) * 64 + ((g ^ f) << 3);
         } else {
             const int k = g * 8 + (j >> 2);
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-                off[b] = k * R + (((w0 / 16 + b) ^ TpLoader<R, 64, false>::swz(k)) << 4) + (j & 3) * 4;
+            off = k * R + (((w0 / 16) ^ TpLoader<R, 64, false>::swz(k)) << 4) + (j & 3) * 4;
         }
     }
+    // The offsets are formed anew where this is called: kept in registers over the loop they
+    // would not fit beside the sums.
+    __device__ __forceinline__ void renew() { asm volatile("" : "+v"(off)); }
     // the 8 k values (kk * 32 + 8 * (lane / 16) ..) of row w0 + 16 b + lane % 16
     __device__ __forceinline__ v8bf read(const uint16_t* lds, int kk, int b) const {
         if constexpr (KC) {
-            return *(const v8bf*)(lds + off[kk] + b * 16 * 64);
+            return *(const v8bf*)(lds + (off ^ kk << 5) + b * 16 * 64);
         } else {
-            const uint16_t* p = lds + off[b] + kk * 32 * R;
+            const uint16_t* p = lds + (off ^ b << 4) + kk * 32 * R;
             const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((SC_LDS v4s*)p);
             const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((SC_LDS v4s*)(p + 4 * R));
             return __builtin_bit_cast(v8bf, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -270,51 +271,77 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
             ++seg;
         }
     };
-    auto multiply = [&](const uint16_t* as, const uint16_t* bs) SC_INLINE {
+    // fragments of one 32-deep half of a step, and their products
+    struct Frags {
+        v8bf a[MI], b[NI];
+    };
+    auto read = [&](const uint16_t* as, const uint16_t* bs, int kk, Frags& f) SC_INLINE {
+        ra.renew();
+        rb.renew();
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            v8bf af[MI], bf[NI];
+        for (int j = 0; j < NI; ++j) f.b[j] = rb.read(bs, kk, j);
 #pragma unroll
-            for (int j = 0; j < NI; ++j) bf[j] = rb.read(bs, kk, j);
+        for (int i = 0; i < MI; ++i) f.a[i] = ra.read(as, kk, i);
+    };
+    auto multiply = [&](const Frags& f) SC_INLINE {
 #pragma unroll
-            for (int i = 0; i < MI; ++i) af[i] = ra.read(as, kk, i);
+        for (int i = 0; i < MI; ++i)
 #pragma unroll
-            for (int i = 0; i < MI; ++i)
+            for (int j = 0; j < NI; ++j)  // transposed: a lane's four sums are consecutive n
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.b[j], f.a[i], acc[i][j], 0, 0, 0);
+    };
+    // one half's products with the next half's reads spread between them
+    auto interleave = [&]() SC_INLINE {
+        constexpr int READS = (AKC ? MI : 2 * MI) + (BKC ? NI : 2 * NI), PRODS = MI * NI;
 #pragma unroll
-                for (int j = 0; j < NI; ++j)  // transposed: a lane's four sums are consecutive n
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[j], af[i], acc[i][j], 0, 0, 0);
+        for (int r = 0; r < READS; ++r) {
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // an LDS read
+            __builtin_amdgcn_sched_group_barrier(0x008, PRODS / READS, 0);
         }
+        if constexpr (PRODS % READS) __builtin_amdgcn_sched_group_barrier(0x008, PRODS % READS, 0);
     };
     // every step issues the same number of loads (the ones past the end fetch nothing)
     constexpr int PER = LA::NL + LB::NL;
-    auto step = [&](const uint16_t* as, const uint16_t* bs, uint16_t* an, uint16_t* bn) SC_INLINE {
-        // this wave's loads of the step have landed and its reads of the buffer that is
-        // filled next are done; after the barrier that holds for every wave
-        if constexpr (NST == 2) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-        else asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(PER * (NST - 2)) : "memory");
+    Frags f0, f1;
+    // On entry the first half of this step's fragments is in f0 (or on its way).
+    auto step = [&](uint16_t* as, uint16_t* bs, const uint16_t* an, const uint16_t* bn) SC_INLINE {
+        read(as, bs, 1, f1);
+        multiply(f0);
+        interleave();
+        // this wave's loads of the next step have landed and its reads of this step's buffer
+        // are done; after the barrier that holds for every wave
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(PER * (NST - 2)) : "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        fetch(an, bn);
+        fetch(as, bs);
         __builtin_amdgcn_sched_barrier(0);  // the loads go out before the products
-        multiply(as, bs);
+        read(an, bn, 0, f0);
+        multiply(f1);
+        interleave();
+        __builtin_amdgcn_sched_barrier(0);
     };
     fetch(a0, b0);
-    if constexpr (NST > 2) fetch(a1, b1);
-    if constexpr (NST > 3) fetch(a2, b2);
+    fetch(a1, b1);
+    if constexpr (NST > 2) fetch(a2, b2);
+    if constexpr (NST > 3) fetch(a3, b3);
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(PER * (NST - 1)) : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    read(a0, b0, 0, f0);
     // whole turns of the buffers: the steps past the end multiply zeros
     for (int s = first; s < last; s += NST) {
         if constexpr (NST == 2) {
             step(a0, b0, a1, b1);
             step(a1, b1, a0, b0);
         } else if constexpr (NST == 3) {
-            step(a0, b0, a2, b2);
-            step(a1, b1, a0, b0);
-            step(a2, b2, a1, b1);
+            step(a0, b0, a1, b1);
+            step(a1, b1, a2, b2);
+            step(a2, b2, a0, b0);
         } else {
-            step(a0, b0, a3, b3);
-            step(a1, b1, a0, b0);
-            step(a2, b2, a1, b1);
-            step(a3, b3, a2, b2);
+            step(a0, b0, a1, b1);
+            step(a1, b1, a2, b2);
+            step(a2, b2, a3, b3);
+            step(a3, b3, a0, b0);
         }
     }
     // loads past the end may still be on their way into LDS
