@@ -7,10 +7,17 @@
 namespace scopt {
 
 namespace {
+constexpr int kCus = 256;
 using Big = TpShape<256, 256, 2, 4, 2, 1>;    // 128 KB of LDS: one workgroup of 8 waves per CU
 using Mid = TpShape<128, 128, 2, 2, 2, 2>;    // 64 KB: two workgroups of 4 waves per CU
 using Small = TpShape<64, 128, 1, 4, 3, 2>;   // 72 KB: two workgroups of 4 waves per CU
 }  // namespace
+
+// a column's factor
+__device__ __forceinline__ float tp_gain(const TpArgs& P, int n) {
+    if (!P.gain) return 1.0f;
+    return P.gain_bf16 ? Elem<uint16_t>::load((const uint16_t*)P.gain, n) : gld((const float*)P.gain + n);
+}
 
 // Sum of the splits' partial products, in split order, with the store's factors.
 // acc: an earlier sum that is added (NULL: none); out_acc: the sum is kept there in float32
@@ -18,7 +25,6 @@ using Small = TpShape<64, 128, 1, 4, 3, 2>;   // 72 KB: two workgroups of 4 wave
 __global__ __launch_bounds__(256) void tp_reduce_kernel(const TpArgs P, const float* acc, float* out_acc) {
     const int64_t groups = (int64_t)P.M * ((P.N + 3) / 4);
     const float alpha = P.alpha ? gld(P.alpha) : 1.0f;
-    const bool vec = (P.N & 3) == 0;
     for (int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x; g < groups; g += (int64_t)gridDim.x * 256) {
         const int64_t m = g / ((P.N + 3) / 4);
         const int n = (int)(g - m * ((P.N + 3) / 4)) * 4;
@@ -26,8 +32,8 @@ __global__ __launch_bounds__(256) void tp_reduce_kernel(const TpArgs P, const fl
         const int64_t at = m * P.N + n, stride = (int64_t)P.M * P.N;
         float v[4] = {0.f, 0.f, 0.f, 0.f};
         auto add = [&](const float* p) {
-            if (vec) {
-                const v4f x = gld4(p);
+            if (left >= 4) {
+                const v4f_any x = *(const SC_GLOBAL v4f_any*)p;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) v[r] += x[r];
             } else {
@@ -39,11 +45,11 @@ __global__ __launch_bounds__(256) void tp_reduce_kernel(const TpArgs P, const fl
         if (acc) add(acc + at);
         for (int s = 0; s < P.splits; ++s) add(P.part + s * stride + at);
         if (out_acc) {
-            tp_store(out_acc, 0, at, v, left, vec);
+            tp_store(out_acc, 0, at, v, left);
         } else {
 #pragma unroll
             for (int r = 0; r < 4; ++r) v[r] *= alpha * tp_gain(P, min(n + r, P.N - 1));
-            tp_store(P.C, P.c_bf16, m * P.ldc + n, v, left, P.c_vec);
+            tp_store(P.C, P.c_bf16, m * P.ldc + n, v, left);
         }
     }
 }
@@ -85,7 +91,8 @@ TpPlan tp_plan(int M, int N, int K, int nseg, bool may_split) {
 namespace {
 template <class S>
 hipError_t launch_shape(TpKind kind, const TpArgs& P, bool part, hipStream_t st) {
-    const dim3 grid((unsigned)(P.tiles_m * P.tiles_n * P.splits)), blk(S::NT);
+    const int all = P.tiles_m * P.tiles_n * P.splits, most = kCus * S::PER_CU;
+    const dim3 grid((unsigned)(all < most ? all : most)), blk(S::NT);
     switch (kind) {
         case TPK_LOGIT_STATS: hipLaunchKernelGGL((tile_product_kernel<S, true, true, TP_STATS>), grid, blk, 0, st, P); break;
         case TPK_LOGIT_GRAD: hipLaunchKernelGGL((tile_product_kernel<S, true, true, TP_GRAD>), grid, blk, 0, st, P); break;
@@ -114,7 +121,6 @@ hipError_t launch_tile_product(TpKind kind, const TpPlan& plan, TpArgs P, const 
     P.tiles_m = plan.tiles_m;
     P.tiles_n = plan.tiles_n;
     P.splits = plan.splits;
-    P.c_vec = P.C && (P.ldc & 3) == 0 && (P.N & 3) == 0 && ((uintptr_t)P.C & (P.c_bf16 ? 7 : 15)) == 0;
     const bool part = (kind == TPK_STATES || kind == TPK_WEIGHTS) && (plan.splits > 1 || sum.acc || sum.out_acc);
     hipError_t e = plan.shape == 0   ? launch_shape<Big>(kind, P, part, st)
                    : plan.shape == 1 ? launch_shape<Mid>(kind, P, part, st)

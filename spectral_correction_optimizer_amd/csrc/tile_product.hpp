@@ -25,15 +25,20 @@
 //                    a fragment is two transposing reads (ds_read_b64_tr_b16: 16 lanes
 //                    read four k rows of 16 elements, each lane receives the four k of
 //                    one row).
-// Bounds: every load goes through a buffer resource that ends at the operand's end, and a
-// lane whose chunk lies beyond the operand's rows (or k) gets an offset beyond it: such
-// lanes deliver zeros.
+// Bounds: every load goes through a buffer resource that ends at the operand's end, so rows
+// (k contiguous) or k (rows contiguous) past it deliver zeros.  A chunk past K of a row with k
+// contiguous gets an offset beyond the end.  Columns past the rows of a k row deliver that
+// row's padding or the next k row: they only reach sums that are not stored.
+//
+// A workgroup takes tiles in turn, as many workgroups as run at once, and the loads of its
+// next tile are under way while the sums of this one are stored.
 #pragma once
 
 #include <type_traits>
 
 #include "common.hpp"
 #include "internal.hpp"
+#include "rows.hpp"
 #include "train.hpp"
 
 namespace scopt {
@@ -48,41 +53,40 @@ typedef short v8s __attribute__((ext_vector_type(8)));
 constexpr uint32_t kTpMaxBytes = 0x7fffffffu;  // largest buffer range (offsets stay below 2^31)
 constexpr uint32_t kTpBeyond = 0x80000000u;    // an offset beyond every range
 
+// Rows contiguous: the permutation of row k's 32-byte blocks
+template <int R>
+__device__ __forceinline__ int tp_swz(int k) {
+    constexpr int MASK = R >= 128 ? 7 : R / 16 - 1;
+    return ((k & 3) | (((k >> 3) & 1) << 2)) & MASK;
+}
+
 // Loader of one operand's R x 64 tile: offsets are set up once, the base advances.
 template <int R, int NT, bool KC>
 struct TpLoader {
     static constexpr int NL = R * 8 / NT;  // 16-byte loads per thread and tile
-    uint32_t voff[NL];
-    int kchunk;  // KC: the k of this lane's chunk within a tile
-    __device__ __forceinline__ void init(int64_t ld, int rows, int r0) {
+    static constexpr int STEP = KC ? NT / 8 : NT / (R / 8);  // rows (or k) between them
+    static_assert(STEP % 16 == 0, "the permutation of a row's slots repeats every 16 rows");
+    uint32_t voff;  // of the first load
+    int kchunk;     // KC: the k of this lane's chunk within a tile
+    __device__ __forceinline__ void init(int64_t ld) {
         const int t = threadIdx.x;
         if constexpr (KC) {
             const int r = t >> 3, slot = t & 7;
             const int c = slot ^ (r & 7) ^ ((r >> 3) & 1);
             kchunk = c * 8;
-#pragma unroll
-            for (int i = 0; i < NL; ++i) {
-                const int row = r + i * (NT / 8);
-                voff[i] = r0 + row < rows ? (uint32_t)(row * ld + c * 8) * 2u : kTpBeyond;
-            }
+            voff = (uint32_t)(r * ld + c * 8) * 2u;
         } else {
             constexpr int CR = R / 8;  // chunks per k row
+            const int k = t / CR, slot = t % CR;
+            const int c = slot ^ tp_swz<R>(k) * 2;
             kchunk = 0;
-#pragma unroll
-            for (int i = 0; i < NL; ++i) {
-                const int k = t / CR + i * (NT / CR), slot = t % CR;
-                const int c = slot ^ swz(k) * 2;
-                voff[i] = r0 + c * 8 < rows ? (uint32_t)(k * ld + c * 8) * 2u : kTpBeyond;
-            }
+            voff = (uint32_t)(k * ld + c * 8) * 2u;
         }
-    }
-    static __device__ __forceinline__ int swz(int k) {
-        constexpr int MASK = R >= 128 ? 7 : R / 16 - 1;
-        return ((k & 3) | (((k >> 3) & 1) << 2)) & MASK;
     }
     // fetch the tile at k0 of a plane into lds; live = false fetches nothing (zeros)
     __device__ __forceinline__ void fetch(const uint16_t* p, int64_t ld, int rows, int K, int r0, int k0,
-                                          bool live, uint16_t* lds) const {
+                                          bool live, uint16_t* lds) {
+        asm volatile("" : "+v"(voff));  // the loads' offsets are formed here, not kept
         // a row of k ends at a whole chunk (what lies between is zero or meets zeros), and so
         // does a row of rows (the sums of what lies beyond are not stored)
         if (KC) K = (K + 7) & ~7;
@@ -95,7 +99,7 @@ struct TpLoader {
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
-            uint32_t v = voff[i];
+            uint32_t v = voff + (uint32_t)(i * STEP * ld) * 2u;
             if (KC) v = k0 + kchunk < K ? v : kTpBeyond;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (SC_LDS void*)(lds + i * NT * 8 + wave * 512), 16, v, 0,
                                                      0, 0);
@@ -115,7 +119,7 @@ struct TpReader {
             off = (w0 + j) * 64 + ((g ^ f) << 3);
         } else {
             const int k = g * 8 + (j >> 2);
-            off = k * R + (((w0 / 16) ^ TpLoader<R, 64, false>::swz(k)) << 4) + (j & 3) * 4;
+            off = k * R + (((w0 / 16) ^ tp_swz<R>(k)) << 4) + (j & 3) * 4;
         }
     }
     // The offsets are formed anew where this is called: kept in registers over the loop they
@@ -136,31 +140,58 @@ struct TpReader {
 
 // ---- epilogue pieces -------------------------------------------------------------------
 
-__device__ __forceinline__ float tp_gain(const TpArgs& P, int n) {
-    if (!P.gain) return 1.0f;
-    return P.gain_bf16 ? Elem<uint16_t>::load((const uint16_t*)P.gain, n) : gld((const float*)P.gain + n);
-}
 // four consecutive elements at `at`, the first `left` of them inside the row
-__device__ __forceinline__ void tp_store(void* base, int bf16, int64_t at, const float (&v)[4], int left, bool vec) {
+__device__ __forceinline__ void tp_store(void* base, int bf16, int64_t at, const float (&v)[4], int left) {
     if (bf16) {
         uint16_t* p = (uint16_t*)base + at;
-        if (vec) {
-            *(SC_GLOBAL v2u*)p = v2u{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-        } else {
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                if (r < left) gst(p + r, f32_to_bf16(v[r]));
-        }
+        for (int r = 0; r < 4; ++r)
+            if (r < left) gst(p + r, f32_to_bf16(v[r]));
     } else {
         float* p = (float*)base + at;
-        if (vec) {
-            gst4(p, v4f{v[0], v[1], v[2], v[3]});
+        if (left >= 4) {
+            *(SC_GLOBAL v4f_any*)p = v4f_any{v[0], v[1], v[2], v[3]};
         } else {
 #pragma unroll
             for (int r = 0; r < 4; ++r)
                 if (r < left) gst(p + r, v[r]);
         }
     }
+}
+// Bfloat16 pairs of one row of NI blocks of 16 columns: in, lane group g = lane / 16 holds
+// columns 4 g .. 4 g + 3 of every block; out, 4 NI consecutive columns, and the first of them.
+// (Rows of 16 lanes change places between registers; the stores then write whole 16 bytes,
+// and with NI = 4 a row's 128 bytes are four lanes'.)
+template <int NI>
+__device__ __forceinline__ int tp_gather_row(uint32_t (&d)[NI][2]) {
+    static_assert(NI == 2 || NI == 4, "blocks of a wave");
+    const int g = (threadIdx.x & 63) >> 4;
+    auto swap16 = [](uint32_t& x, uint32_t& y) SC_INLINE {
+        const auto r = __builtin_amdgcn_permlane16_swap(x, y, false, false);
+        x = r[0];
+        y = r[1];
+    };
+    auto swap32 = [](uint32_t& x, uint32_t& y) SC_INLINE {
+        const auto r = __builtin_amdgcn_permlane32_swap(x, y, false, false);
+        x = r[0];
+        y = r[1];
+    };
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+#pragma unroll
+        for (int j = 0; j < NI; j += 2) swap16(d[j][w], d[j + 1][w]);
+        if constexpr (NI == 4) {
+            swap32(d[0][w], d[2][w]);
+            swap32(d[1][w], d[3][w]);
+        }
+    }
+    return NI == 4 ? 16 * g : 16 * (g & 1) + 4 * (g & 2);
+}
+template <int NI>
+__device__ __forceinline__ void tp_store_row(uint16_t* p, const uint32_t (&d)[NI][2]) {
+#pragma unroll
+    for (int j = 0; j < NI; j += 2)
+        *(SC_GLOBAL v4u_any*)(p + 4 * j) = v4u_any{d[j][0], d[j][1], d[j + 1][0], d[j + 1][1]};
 }
 // four dlogits as one bfloat16 plane, or as the three planes of their float32 values
 __device__ __forceinline__ void tp_store_planes(uint16_t* base, int planes, int64_t plane, int64_t at,
@@ -219,6 +250,13 @@ __device__ __forceinline__ void tp_tile(int id, int tiles_m, int tiles_n, int& t
     tn = in / gm;
 }
 
+// LDS written before is read after, by every wave; loads into LDS may stay under way
+__device__ __forceinline__ void tp_lds_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 template <class S, bool AKC, bool BKC, int EPI>
 __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpArgs P) {
     constexpr int BM = S::BM, BN = S::BN, NT = S::NT, NST = S::NST;
@@ -229,85 +267,101 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
     __shared__ __align__(1024) uint16_t a0[ASZ], b0[BSZ], a1[ASZ], b1[BSZ];
     __shared__ __align__(1024) uint16_t a2[NST > 2 ? ASZ : 8], b2[NST > 2 ? BSZ : 8];
     __shared__ __align__(1024) uint16_t a3[NST > 3 ? ASZ : 8], b3[NST > 3 ? BSZ : 8];
+    __shared__ float red[EPI == TP_STATS ? 2 * S::WVN * BM : 1];  // row maxima, then sums
 
-    const int tiles = P.tiles_m * P.tiles_n;
-    const int id = xcd_remap(blockIdx.x, gridDim.x);
-    const int split = id / tiles;
-    int tm, tn;
-    tp_tile(id - split * tiles, P.tiles_m, P.tiles_n, tm, tn);
-    const int m0 = tm * BM, n0 = tn * BN;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = (wave / S::WVN) * WM, wn = (wave % S::WVN) * WN;
 
     LA la;
     LB lb;
-    la.init(P.lda, P.M, m0);
-    lb.init(P.ldb, P.N, n0);
+    la.init(P.lda);
+    lb.init(P.ldb);
     TpReader<BM, MI, AKC> ra;
     TpReader<BN, NI, BKC> rb;
     ra.init(wm);
     rb.init(wn);
 
     v4f acc[MI][NI];
-#pragma unroll
-    for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int j = 0; j < NI; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
 
     const int ksteps = (P.K + 63) / 64, total = ksteps * P.nseg;
     const int per = (total + P.splits - 1) / P.splits;
-    const int first = split * per, last = min(total, first + per);
+    const int tiles = P.tiles_m * P.tiles_n, all = tiles * P.splits;
 
-    // the step that is fetched next: its segment and k
-    int seg = first / ksteps, kst = first - seg * ksteps, fetched = first;
+    // the step that is fetched next: its tile, segment and k
+    struct Ahead {
+        int m0, n0, seg, kst, left;
+    } ah;
+    auto begin_tile = [&](int turn) SC_INLINE {
+        const int id = turn < all ? xcd_remap(turn, all) : 0;
+        const int split = id / tiles;
+        int tm, tn;
+        tp_tile(id - split * tiles, P.tiles_m, P.tiles_n, tm, tn);
+        ah.m0 = tm * BM;
+        ah.n0 = tn * BN;
+        const int step = split * per;
+        ah.left = turn < all ? min(total, step + per) - step : 0;
+        ah.seg = step / ksteps;
+        ah.kst = step - ah.seg * ksteps;
+    };
     auto fetch = [&](uint16_t* as, uint16_t* bs) SC_INLINE {
-        const bool live = fetched < last;
-        const uint32_t planes = live ? (uint32_t)(P.segs >> (4 * seg)) : 0;
-        la.fetch(P.A + (planes & 3) * P.a_plane, P.lda, P.M, P.K, m0, kst * 64, live, as);
-        lb.fetch(P.B + ((planes >> 2) & 3) * P.b_plane, P.ldb, P.N, P.K, n0, kst * 64, live, bs);
-        ++fetched;
-        if (++kst == ksteps) {
-            kst = 0;
-            ++seg;
-        }
+        const bool live = ah.left > 0;
+        const uint32_t planes = live ? (uint32_t)(P.segs >> (4 * ah.seg)) : 0;
+        la.fetch(P.A + (planes & 3) * P.a_plane, P.lda, P.M, P.K, ah.m0, ah.kst * 64, live, as);
+        lb.fetch(P.B + ((planes >> 2) & 3) * P.b_plane, P.ldb, P.N, P.K, ah.n0, ah.kst * 64, live, bs);
+        --ah.left;
+        const bool wrap = ++ah.kst == ksteps;
+        ah.kst = wrap ? 0 : ah.kst;
+        ah.seg += wrap;
     };
-    // fragments of one 32-deep half of a step, and their products
-    struct Frags {
-        v8bf a[MI], b[NI];
-    };
-    auto read = [&](const uint16_t* as, const uint16_t* bs, int kk, Frags& f) SC_INLINE {
+    // A step's products go in four phases: each 32-deep half of k, in two groups of MI / 2 row
+    // blocks.  A phase reads the fragments of the next one while it multiplies.
+    constexpr int MG = MI / 2;
+    v8bf fa[2][MG], fb[2][NI];
+    auto read_a = [&](const uint16_t* as, int kk, int grp) SC_INLINE {
         ra.renew();
+#pragma unroll
+        for (int i = 0; i < MG; ++i) fa[grp][i] = ra.read(as, kk, grp * MG + i);
+    };
+    auto read_b = [&](const uint16_t* bs, int kk) SC_INLINE {
         rb.renew();
 #pragma unroll
-        for (int j = 0; j < NI; ++j) f.b[j] = rb.read(bs, kk, j);
-#pragma unroll
-        for (int i = 0; i < MI; ++i) f.a[i] = ra.read(as, kk, i);
+        for (int j = 0; j < NI; ++j) fb[kk][j] = rb.read(bs, kk, j);
     };
-    auto multiply = [&](const Frags& f) SC_INLINE {
+    auto multiply = [&](int kk, int grp) SC_INLINE {
 #pragma unroll
-        for (int i = 0; i < MI; ++i)
+        for (int i = 0; i < MG; ++i)
 #pragma unroll
             for (int j = 0; j < NI; ++j)  // transposed: a lane's four sums are consecutive n
-                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.b[j], f.a[i], acc[i][j], 0, 0, 0);
+                acc[grp * MG + i][j] =
+                    __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[kk][j], fa[grp][i], acc[grp * MG + i][j], 0, 0, 0);
     };
-    // one half's products with the next half's reads spread between them
-    auto interleave = [&]() SC_INLINE {
-        constexpr int READS = (AKC ? MI : 2 * MI) + (BKC ? NI : 2 * NI), PRODS = MI * NI;
+    // one phase's products with the reads spread between them
+    auto spread = [&](auto reads) SC_INLINE {
+        constexpr int READS = decltype(reads)::value, PRODS = MG * NI;
+        constexpr int EVERY = PRODS / READS > 0 ? PRODS / READS : 1, AT_ONCE = (READS + PRODS - 1) / PRODS;
 #pragma unroll
-        for (int r = 0; r < READS; ++r) {
-            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // an LDS read
-            __builtin_amdgcn_sched_group_barrier(0x008, PRODS / READS, 0);
+        for (int r = 0; r < READS / AT_ONCE; ++r) {
+            __builtin_amdgcn_sched_group_barrier(0x100, AT_ONCE, 0);  // LDS reads
+            __builtin_amdgcn_sched_group_barrier(0x008, EVERY, 0);    // products
         }
-        if constexpr (PRODS % READS) __builtin_amdgcn_sched_group_barrier(0x008, PRODS % READS, 0);
+        __builtin_amdgcn_sched_barrier(0);
     };
+    using ReadsA = std::integral_constant<int, (AKC ? 1 : 2) * MG>;
+    using ReadsAB = std::integral_constant<int, (AKC ? 1 : 2) * MG + (BKC ? 1 : 2) * NI>;
     // every step issues the same number of loads (the ones past the end fetch nothing)
     constexpr int PER = LA::NL + LB::NL;
-    Frags f0, f1;
-    // On entry the first half of this step's fragments is in f0 (or on its way).
+    // On entry the fragments of this step's first phase are read or on their way.
     auto step = [&](uint16_t* as, uint16_t* bs, const uint16_t* an, const uint16_t* bn) SC_INLINE {
-        read(as, bs, 1, f1);
-        multiply(f0);
-        interleave();
+        read_a(as, 0, 1);
+        multiply(0, 0);
+        spread(ReadsA{});
+        read_a(as, 1, 0);
+        read_b(bs, 1);
+        multiply(0, 1);
+        spread(ReadsAB{});
+        read_a(as, 1, 1);
+        multiply(1, 0);
+        spread(ReadsA{});
         // this wave's loads of the next step have landed and its reads of this step's buffer
         // are done; after the barrier that holds for every wave
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(PER * (NST - 2)) : "memory");
@@ -315,11 +369,12 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
         asm volatile("" ::: "memory");
         fetch(as, bs);
         __builtin_amdgcn_sched_barrier(0);  // the loads go out before the products
-        read(an, bn, 0, f0);
-        multiply(f1);
-        interleave();
-        __builtin_amdgcn_sched_barrier(0);
+        read_a(an, 0, 0);
+        read_b(bn, 0);
+        multiply(1, 1);
+        spread(ReadsAB{});
     };
+    begin_tile(blockIdx.x);
     fetch(a0, b0);
     fetch(a1, b1);
     if constexpr (NST > 2) fetch(a2, b2);
@@ -327,9 +382,23 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(PER * (NST - 1)) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    read(a0, b0, 0, f0);
-    // whole turns of the buffers: the steps past the end multiply zeros
-    for (int s = first; s < last; s += NST) {
+
+    for (int turn = blockIdx.x; turn < all; turn += gridDim.x) {
+    const int id = xcd_remap(turn, all), split = id / tiles;
+    int tm, tn;
+    tp_tile(id - split * tiles, P.tiles_m, P.tiles_n, tm, tn);
+    const int m0 = tm * BM, n0 = tn * BN;
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NI; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+    // (the last step of the tile before has read these too, or they are the first)
+    read_a(a0, 0, 0);
+    read_b(b0, 0);
+    // whole turns of the buffers, one at least: the steps past the end multiply zeros
+    int left = max(1, min(total, split * per + per) - split * per);
+    for (; left > 0; left -= NST) {
+        if (left <= NST) begin_tile(turn + gridDim.x);  // the last turn fetches the next tile's first steps
         if constexpr (NST == 2) {
             step(a0, b0, a1, b1);
             step(a1, b1, a0, b0);
@@ -344,40 +413,60 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
             step(a3, b3, a0, b0);
         }
     }
-    // loads past the end may still be on their way into LDS
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
 
     // Lane l holds, of block (i, j): row m = wm + 16 i + l % 16, columns
     // n = wn + 16 j + 4 (l / 16) + 0..3.
+    // (formed anew for every tile: the registers are the main loop's)
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
     const int lm = m0 + wm + (lane & 15), ln = n0 + wn + 4 * (lane >> 4);
     const int M = P.M, N = P.N;
+    const bool whole = n0 + BN <= N;  // all columns of the tile exist
     if constexpr (EPI == TP_STORE) {
         const float alpha = P.alpha ? gld(P.alpha) : 1.0f;
-        auto store = [&](auto bf16, auto vec) SC_INLINE {
+        float g[NI][4];
 #pragma unroll
-            for (int j = 0; j < NI; ++j) {
-                const int n = ln + 16 * j;
-                float g[4];
+        for (int j = 0; j < NI; ++j)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) g[r] = alpha * tp_gain(P, min(n + r, N - 1));
+            for (int r = 0; r < 4; ++r) g[j][r] = alpha;
+        if (P.gain) {
+            auto scale = [&](auto* gain) SC_INLINE {
+                using G = std::remove_const_t<std::remove_pointer_t<decltype(gain)>>;
 #pragma unroll
-                for (int i = 0; i < MI; ++i) {
-                    const int m = lm + 16 * i;
-                    const float v[4] = {acc[i][j][0] * g[0], acc[i][j][1] * g[1], acc[i][j][2] * g[2],
-                                        acc[i][j][3] * g[3]};
-                    if (m < M && n < N)
-                        tp_store(P.C, decltype(bf16)::value, (int64_t)m * P.ldc + n, v, N - n, decltype(vec)::value);
-                }
+                for (int j = 0; j < NI; ++j)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) g[j][r] *= Elem<G>::load(gain, min(ln + 16 * j + r, N - 1));
+            };
+            if (P.gain_bf16) scale((const uint16_t*)P.gain);
+            else scale((const float*)P.gain);
+        }
+        if (P.c_bf16 && whole) {
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                const int m = lm + 16 * i;
+                uint32_t d[NI][2];
+#pragma unroll
+                for (int j = 0; j < NI; ++j)
+#pragma unroll
+                    for (int w = 0; w < 2; ++w)
+                        d[j][w] = pack_bf16x2(acc[i][j][2 * w] * g[j][2 * w], acc[i][j][2 * w + 1] * g[j][2 * w + 1]);
+                const int c = tp_gather_row<NI>(d);
+                if (m < M) tp_store_row<NI>((uint16_t*)P.C + (int64_t)m * P.ldc + n0 + wn + c, d);
             }
-        };
-        using T = std::true_type;
-        using F = std::false_type;
-        if (P.c_bf16) {
-            if (P.c_vec) store(T{}, T{});
-            else store(T{}, F{});
         } else {
-            if (P.c_vec) store(F{}, T{});
-            else store(F{}, F{});
+            auto store = [&](auto bf16) SC_INLINE {
+#pragma unroll
+                for (int i = 0; i < MI; ++i)
+#pragma unroll
+                    for (int j = 0; j < NI; ++j) {
+                        const int m = lm + 16 * i, n = ln + 16 * j;
+                        const float v[4] = {acc[i][j][0] * g[j][0], acc[i][j][1] * g[j][1], acc[i][j][2] * g[j][2],
+                                            acc[i][j][3] * g[j][3]};
+                        if (m < M) tp_store(P.C, decltype(bf16)::value, (int64_t)m * P.ldc + n, v, N - n);
+                    }
+            };
+            if (P.c_bf16) store(std::true_type{});
+            else store(std::false_type{});
         }
     } else if constexpr (EPI == TP_PART) {
 #pragma unroll
@@ -385,82 +474,101 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
 #pragma unroll
             for (int j = 0; j < NI; ++j) {
                 const int m = lm + 16 * i, n = ln + 16 * j;
-                if (m >= M || n >= N) continue;
                 const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-                tp_store(P.part, 0, ((int64_t)split * M + m) * N + n, v, N - n, (N & 3) == 0);
+                if (m < M) tp_store(P.part, 0, ((int64_t)split * M + m) * N + n, v, N - n);
             }
     } else if constexpr (EPI == TP_STATS) {
         // row maximum over the tile's columns: registers, the four lanes of a row, the
         // waves beside each other
-        float* red = (float*)a0;  // [WVN][BM]
-        __syncthreads();
-        float mx[MI], sum[MI];
+        int hit[MI];  // the target's column in this wave's part, or -1
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            const int64_t t = gld(P.targets + min(lm + 16 * i, M - 1)) - P.n_first;
+            const int64_t c = t - (n0 + wn);
+            hit[i] = lm + 16 * i < M && t < N && c >= 0 && c < WN ? (int)c : -1;
+        }
+        if (!whole) {
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int j = 0; j < NI; ++j)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (ln + 16 * j + r >= N) acc[i][j][r] = -__builtin_huge_valf();
+        }
         const bool pow2 = P.keep == TP_KEEP_EXP;
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
-            float v = -__builtin_huge_valf();
+            float v = acc[i][0][0];
 #pragma unroll
             for (int j = 0; j < NI; ++j)
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (ln + 16 * j + r < N) v = fmaxf(v, acc[i][j][r]);
+                for (int r = 0; r < 4; ++r) v = fmaxf(v, acc[i][j][r]);
             v = fmaxf(v, __shfl_xor(v, 16));
             v = fmaxf(v, __shfl_xor(v, 32));
             if (lane < 16) red[(wave % S::WVN) * BM + wm + 16 * i + lane] = v;
-        }
-        __syncthreads();
+            if (__ballot(hit[i] >= 0)) {
 #pragma unroll
-        for (int i = 0; i < MI; ++i) {
-            float v = red[wm + 16 * i + (lane & 15)];
+                for (int j = 0; j < NI; ++j)
 #pragma unroll
-            for (int w = 1; w < S::WVN; ++w) v = fmaxf(v, red[w * BM + wm + 16 * i + (lane & 15)]);
-            mx[i] = v;
+                    for (int r = 0; r < 4; ++r)
+                        if (hit[i] == 16 * j + 4 * (lane >> 4) + r) gst(P.target_logit + lm + 16 * i, acc[i][j][r]);
+            }
         }
-        __syncthreads();
+        tp_lds_barrier();
+        float* sums = red + S::WVN * BM;
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
             const int m = lm + 16 * i;
-            const int64_t tgt = m < M ? tp_target(P.targets, P.vocab, m) - P.n_first : -1;
-            const float ref = tp_reference(mx[i], pow2);
+            float mx = red[wm + 16 * i + (lane & 15)];
+#pragma unroll
+            for (int w = 1; w < S::WVN; ++w) mx = fmaxf(mx, red[w * BM + wm + 16 * i + (lane & 15)]);
+            const float ref = tp_reference(mx, pow2);
             float z = 0.0f;
+            uint32_t d[NI][2];
+            if (pow2) {
 #pragma unroll
-            for (int j = 0; j < NI; ++j) {
-                const int n = ln + 16 * j;
-                float e[4];
+                for (int j = 0; j < NI; ++j) {
+                    float e[4];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float s = acc[i][j][r];
-                    e[r] = n + r < N ? (pow2 ? __builtin_amdgcn_exp2f(fmaf(s, kLog2e, -ref)) : expf(s - ref)) : 0.0f;
-                    z += e[r];
-                    if (m < M && n + r < N && n + r == tgt) gst(P.target_logit + m, s);
-                }
-                if (m < M && n < P.ldp) {
-                    if (P.keep == TP_KEEP_EXP)
-                        tp_store(P.P, 1, (int64_t)m * P.ldp + n, e, 4, true);
-                    else if (P.keep == TP_KEEP_LOGIT) {
-                        const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-                        tp_store(P.P, 0, (int64_t)m * P.ldp + n, v, 4, true);
+                    for (int r = 0; r < 4; ++r) {
+                        e[r] = __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], kLog2e, -ref));
+                        z += e[r];
                     }
+                    d[j][0] = pack_bf16x2(e[0], e[1]);
+                    d[j][1] = pack_bf16x2(e[2], e[3]);
+                }
+                uint16_t* p = (uint16_t*)P.P + (int64_t)m * P.ldp;
+                if (whole) {
+                    const int c = tp_gather_row<NI>(d);
+                    if (m < M) tp_store_row<NI>(p + n0 + wn + c, d);
+                } else if (m < M) {
+#pragma unroll
+                    for (int j = 0; j < NI; ++j)
+                        if (ln + 16 * j < P.ldp) *(SC_GLOBAL v2u*)(p + ln + 16 * j) = v2u{d[j][0], d[j][1]};
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < NI; ++j) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) z += __builtin_amdgcn_exp2f((acc[i][j][r] - ref) * kLog2e);
+                    if (P.keep == TP_KEEP_LOGIT && m < M && ln + 16 * j < P.ldp)
+                        gst4((float*)P.P + (int64_t)m * P.ldp + ln + 16 * j, acc[i][j]);
                 }
             }
             z += __shfl_xor(z, 16);
             z += __shfl_xor(z, 32);
-            sum[i] = z;
-            if (lane < 16) red[(wave % S::WVN) * BM + wm + 16 * i + lane] = z;
+            if (lane < 16) sums[(wave % S::WVN) * BM + wm + 16 * i + lane] = z;
+            if (wave % S::WVN == 0 && lane < 16 && m < M)
+                gst(P.stat_max + (int64_t)(P.stat_first + tn) * M + m,
+                    mx == -__builtin_huge_valf() ? mx : ref);
         }
-        __syncthreads();
-        if (wave % S::WVN == 0 && lane < 16) {
+        tp_lds_barrier();
+        for (int r = threadIdx.x; r < BM; r += NT) {
+            float z = sums[r];
 #pragma unroll
-            for (int i = 0; i < MI; ++i) {
-                const int m = lm + 16 * i;
-                float z = sum[i];
-                for (int w = 1; w < S::WVN; ++w) z += red[w * BM + wm + 16 * i + lane];
-                if (m < M) {
-                    const int64_t at = (int64_t)m * P.stat_ld + P.stat_first + tn;
-                    gst(P.stat_max + at, mx[i] == -__builtin_huge_valf() ? mx[i] : tp_reference(mx[i], pow2));
-                    gst(P.stat_sum + at, z);
-                }
-            }
+            for (int w = 1; w < S::WVN; ++w) z += sums[w * BM + r];
+            if (m0 + r < M) gst(P.stat_sum + (int64_t)(P.stat_first + tn) * M + m0 + r, z);
         }
     } else {
 #pragma unroll
@@ -476,12 +584,16 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
                 float v[4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    v[r] = tgt >= 0 && n + r < N ? expf(acc[i][j][r] - lse) - (P.n_first + n + r == tgt ? 1.0f : 0.0f)
+                    v[r] = tgt >= 0 && n + r < N ? __builtin_amdgcn_exp2f((acc[i][j][r] - lse) * kLog2e) -
+                                                       (P.n_first + n + r == tgt ? 1.0f : 0.0f)
                                                  : 0.0f;
                 tp_store_planes((uint16_t*)P.P, P.p_planes, P.p_plane, (int64_t)m * P.ldp + n, v);
             }
         }
     }
+    }
+    // loads past the end may still be on their way into LDS
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
 }
 
 }  // namespace scopt

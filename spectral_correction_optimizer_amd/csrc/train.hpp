@@ -31,7 +31,7 @@ struct TpArgs {
     // TP_STORE, and the reduction of TP_PART's splits
     void* C = nullptr;
     int64_t ldc = 0;
-    int c_bf16 = 0, c_vec = 0;     // c_vec: groups of four columns are aligned and whole
+    int c_bf16 = 0;
     const float* alpha = nullptr;  // device scalar (NULL: 1)
     const void* gain = nullptr;    // column factors (NULL: 1)
     int gain_bf16 = 0;
@@ -46,9 +46,9 @@ struct TpArgs {
     int64_t p_plane = 0;     // TP_GRAD: elements between planes
     int p_planes = 1;        // TP_GRAD: 1 or 3
     float* target_logit = nullptr;
-    float* stat_max = nullptr;
+    float* stat_max = nullptr;  // [tile of columns][M]
     float* stat_sum = nullptr;
-    int64_t stat_ld = 0, stat_first = 0;
+    int64_t stat_first = 0;
     const float* lse = nullptr;
 };
 
@@ -96,7 +96,7 @@ struct XentPlan {
     int pieces;
     bool keep;                 // one piece whose probabilities are kept between the passes
     int64_t ldp;               // columns of P
-    int64_t stat_ld;
+    int64_t stat_tiles;        // tiles of a row
     TpPlan logits, logits_last, dh, dw, dw_last;
     // offsets into the workspace
     int64_t o_scalars, o_h, o_w, o_s, o_p, o_tl, o_lse, o_smax, o_ssum, o_part, o_dh, bytes;

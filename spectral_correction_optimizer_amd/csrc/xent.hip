@@ -55,36 +55,45 @@ __global__ __launch_bounds__(1024) void xent_count_kernel(const int64_t* __restr
     }
 }
 
-// One wavefront per token: the row's log-sum-exp from its tiles' references and sums, and
-// its loss.  pow2: the references are powers of two.  A row of -infinity only has no finite
-// log-sum-exp; like a row with NaN or +infinity it gives NaN.
-__global__ __launch_bounds__(256) void xent_lse_kernel(const float* __restrict__ smax, const float* __restrict__ ssum,
-                                                       int tiles, int64_t ld, int pow2,
-                                                       const float* __restrict__ target_logit,
-                                                       const int64_t* __restrict__ targets, int64_t T, int64_t V,
-                                                       float* __restrict__ lse, float* __restrict__ loss) {
-    const int lane = threadIdx.x & 63;
-    const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (t >= T) return;
+// 64 tokens a workgroup, one a lane, the tiles dealt to 16 wavefronts: a row's log-sum-exp from
+// its tiles' references and sums [tile][T], and its loss.  pow2: the references are powers of
+// two.  A row of -infinity only has no finite log-sum-exp; like a row with NaN or +infinity
+// it gives NaN.
+__global__ __launch_bounds__(1024) void xent_lse_kernel(const float* __restrict__ smax, const float* __restrict__ ssum,
+                                                        int tiles, int pow2, const float* __restrict__ target_logit,
+                                                        const int64_t* __restrict__ targets, int64_t T, int64_t V,
+                                                        float* __restrict__ lse, float* __restrict__ loss) {
+    __shared__ float red[16][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t t = (int64_t)blockIdx.x * 64 + lane, at = t < T ? t : T - 1;
     const float none = -__builtin_huge_valf();
     float m = none;
-    for (int i = lane; i < tiles; i += 64) m = fmaxf(m, gld(smax + t * ld + i));
-    for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+#pragma unroll 8
+    for (int i = wave; i < tiles; i += 16) m = fmaxf(m, gld(smax + i * T + at));
+    red[wave][lane] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 16; ++w) m = fmaxf(m, red[w][lane]);
     float z = 0.0f;
-    for (int i = lane; i < tiles; i += 64) {
-        const float r = gld(smax + t * ld + i), s = gld(ssum + t * ld + i);
+#pragma unroll 8
+    for (int i = wave; i < tiles; i += 16) {
+        const float r = gld(smax + i * T + at), s = gld(ssum + i * T + at);
         // a tile of -infinity has sum 0 (or NaN)
         z += r == none ? s : s * (pow2 ? exp2f(r - m) : expf(r - m));
     }
-    for (int o = 32; o > 0; o >>= 1) z += __shfl_xor(z, o);
-    if (lane == 0) {
-        // a power of two's logarithm in two parts: m * ln2 is off by less than 2^-40 of m
-        const float base = pow2 ? m * 0.693145751953125f : m, rest = pow2 ? m * 1.42860682030941723e-6f : 0.0f;
-        const float logz = m == none ? __builtin_nanf("") : logf(z) + rest;
-        const bool counted = tp_target(targets, V, t) >= 0;
-        gst(lse + t, base + logz);
-        gst(loss + t, counted ? (base - gld(target_logit + t)) + logz : 0.0f);
-    }
+    __syncthreads();
+    red[wave][lane] = z;
+    __syncthreads();
+    if (wave > 0 || t >= T) return;
+    z = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) z += red[w][lane];
+    // a power of two's logarithm in two parts: m * ln2 is off by less than 2^-40 of m
+    const float base = pow2 ? m * 0.693145751953125f : m, rest = pow2 ? m * 1.42860682030941723e-6f : 0.0f;
+    const float logz = m == none ? __builtin_nanf("") : logf(z) + rest;
+    const bool counted = tp_target(targets, V, t) >= 0;
+    gst(lse + t, base + logz);
+    gst(loss + t, counted ? (base - gld(target_logit + t)) + logz : 0.0f);
 }
 
 // d from what the logits product kept: bfloat16 exponentials (in place) or float32 logits
@@ -92,7 +101,7 @@ __global__ __launch_bounds__(256) void xent_lse_kernel(const float* __restrict__
 template <bool EXP>
 __global__ __launch_bounds__(256) void xent_dlogits_kernel(const float* __restrict__ logits, uint16_t* P, int64_t plane,
                                                            int64_t ldp, int N, int bn, int64_t chunk, int chunks,
-                                                           const float* __restrict__ smax, int64_t stat_ld,
+                                                           const float* __restrict__ smax, int64_t T,
                                                            const float* __restrict__ lse,
                                                            const float* __restrict__ target_logit,
                                                            const int64_t* __restrict__ targets, int64_t V) {
@@ -107,7 +116,7 @@ __global__ __launch_bounds__(256) void xent_dlogits_kernel(const float* __restri
         float v[8];
         if constexpr (EXP) {
             const v4u w = *(const SC_GLOBAL v4u*)p;
-            const float f = __builtin_amdgcn_exp2f(gld(smax + t * stat_ld + c / bn) - ls2);
+            const float f = __builtin_amdgcn_exp2f(gld(smax + (int64_t)(c / bn) * T + t) - ls2);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 v[2 * i] = bf16_lo(w[i]) * f;
@@ -174,7 +183,7 @@ XentPlan xent_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit) {
     p.dh = tp_plan((int)T, (int)H, (int)p.piece, nseg, true);
     p.dw = tp_plan((int)p.piece, (int)H, (int)T, nseg, true);
     p.dw_last = tp_plan((int)last, (int)H, (int)T, nseg, true);
-    p.stat_ld = (int64_t)(p.pieces - 1) * p.logits.tiles_n + p.logits_last.tiles_n;
+    p.stat_tiles = (int64_t)(p.pieces - 1) * p.logits.tiles_n + p.logits_last.tiles_n;
     int64_t o = 0;
     auto take = [&](int64_t bytes) {
         const int64_t at = o;
@@ -189,8 +198,8 @@ XentPlan xent_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit) {
     p.o_p = take(2 * np * T * p.ldp);
     p.o_tl = take(4 * T);
     p.o_lse = take(4 * T);
-    p.o_smax = take(4 * T * p.stat_ld);
-    p.o_ssum = take(4 * T * p.stat_ld);
+    p.o_smax = take(4 * T * p.stat_tiles);
+    p.o_ssum = take(4 * T * p.stat_tiles);
     const bool join = p.pieces > 1;
     int64_t part = p.dh.part_bytes;
     if (join && part == 0) part = 4 * T * H;
@@ -259,7 +268,6 @@ hipError_t launch_xent(const XentPlan& p, const void* h, const void* W, const in
         a.target_logit = tl;
         a.stat_max = smax;
         a.stat_sum = ssum;
-        a.stat_ld = p.stat_ld;
         a.stat_first = (int64_t)i * p.logits.tiles_n;
         a.lse = lse;
         return a;
@@ -272,8 +280,8 @@ hipError_t launch_xent(const XentPlan& p, const void* h, const void* W, const in
         SC_RUN(launch_tile_product(TPK_LOGIT_STATS, logits_plan(i), a, TpSum{}, st));
     }
     const int pow2 = p.keep && p.bf16;
-    hipLaunchKernelGGL(xent_lse_kernel, dim3((unsigned)((T + 3) / 4)), dim3(256), 0, st, smax, ssum, (int)p.stat_ld,
-                       p.stat_ld, pow2, tl, targets, T, V, lse, loss);
+    hipLaunchKernelGGL(xent_lse_kernel, dim3((unsigned)((T + 63) / 64)), dim3(1024), 0, st, smax, ssum,
+                       (int)p.stat_tiles, pow2, tl, targets, T, V, lse, loss);
     SC_RUN(hipGetLastError());
     hipLaunchKernelGGL(xent_mean_kernel, dim3(1), dim3(1024), 0, st, loss, T, sc, mean);
     SC_RUN(hipGetLastError());
@@ -288,10 +296,10 @@ hipError_t launch_xent(const XentPlan& p, const void* h, const void* W, const in
             const dim3 grid((unsigned)(chunks * T));
             if (p.bf16)
                 hipLaunchKernelGGL(xent_dlogits_kernel<true>, grid, dim3(256), 0, st, nullptr, P, T * p.ldp, p.ldp, n,
-                                   p.logits.bn, chunk, chunks, smax, p.stat_ld, lse, tl, targets, V);
+                                   p.logits.bn, chunk, chunks, smax, T, lse, tl, targets, V);
             else
                 hipLaunchKernelGGL(xent_dlogits_kernel<false>, grid, dim3(256), 0, st, S, P, T * p.ldp, p.ldp, n,
-                                   p.logits.bn, chunk, chunks, smax, p.stat_ld, lse, tl, targets, V);
+                                   p.logits.bn, chunk, chunks, smax, T, lse, tl, targets, V);
             SC_RUN(hipGetLastError());
         } else {
             TpArgs a = logits(i);
