@@ -8,9 +8,9 @@ namespace scopt {
 
 namespace {
 constexpr int kCus = 256;
-using Big = TpShape<256, 256, 2, 4, 2, 1>;    // 128 KB of LDS: one workgroup of 8 waves per CU
-using Mid = TpShape<128, 128, 2, 2, 2, 2>;    // 64 KB: two workgroups of 4 waves per CU
-using Small = TpShape<64, 128, 1, 4, 3, 2>;   // 72 KB: two workgroups of 4 waves per CU
+using Big = TpShape<256, 256, 2, 4, 2, 1>;   // 128 KB of LDS: one workgroup of 8 waves per CU
+using Mid = TpShape<128, 128, 2, 2, 2, 2>;   // 64 KB: two workgroups of 4 waves per CU
+using Small = TpShape<64, 128, 1, 4, 3, 2>;  // 72 KB: two workgroups of 4 waves per CU
 }  // namespace
 
 // a column's factor

@@ -11,16 +11,28 @@
 // run through the same loop, smallest first, into the same accumulators: the parts left
 // out are below 2^-23 of |a b|.
 //
-// A workgroup owns a BM x BN tile and advances 64 k at a time.  Both operand tiles go
-// from memory straight into LDS (16 bytes per lane, no registers), NST buffers deep; each
-// wave multiplies a (BM / WVM) x (BN / WVN) part in 16 x 16 x 32 blocks.  Each buffer is
-// an array of its own and the loop is unrolled over them, so the reads of one buffer do
-// not wait for the loads that fill another.
+// A workgroup owns a BM x BN tile; buffers in LDS hold 64 k of it.  Both operand tiles go
+// from memory straight into LDS (16 bytes per lane, no registers); each wave multiplies a
+// (BM / WVM) x (BN / WVN) part in 16 x 16 x 32 blocks, 32 k a step.  A step's fragments are
+// read from LDS during the products of the step before it, so a buffer is free, and being
+// filled again, one step before its products end.  Each buffer is an array of its own and the
+// loop is unrolled over them, so the reads of one buffer do not wait for the loads that fill
+// another.
+//
+// At 256 x 256, 8 waves and two buffers: 1340 TFLOP/s at 8192 x 2048 x 131072 (A with k
+// contiguous, B with rows), 1205 at 131072 x 2048 x 8192 (both with rows), where the matrix
+// cores are busy for 65% of the cycles, LDS for a quarter of them without a bank conflict,
+// and the clock has fallen to 1.75 GHz: fewer wasted cycles no longer make it faster.  Tried
+// and not kept: four buffers of 32 k (64-byte rows where k is contiguous: 10% slower there),
+// fragments that are read in the step that multiplies them (1040), addresses formed in
+// every step instead of every turn of the buffers (8% slower), and sums that the register
+// allocator places (it moves them about and spills).
 //
 // LDS layouts (16-byte slots permuted within a row by choosing which global chunk each
 // lane fetches, so that the matrix operand reads touch every bank once):
-//   k contiguous:    [row][64 k], slot = chunk ^ (row & 7) ^ ((row >> 3) & 1); a
-//                    fragment is one 16-byte read per lane.
+//   k contiguous:    [row][64 k], slot = chunk ^ (row >> 1 & 7); a fragment is one 16-byte
+//                    read per lane.  (The hardware takes 16 lanes at a time, in quads that
+//                    are not all consecutive; this order has no conflict, row & 7 had.)
 //   rows contiguous: [k][rows], 32-byte blocks, block ^= (k & 3) | ((k >> 3) & 1) << 2;
 //                    a fragment is two transposing reads (ds_read_b64_tr_b16: 16 lanes
 //                    read four k rows of 16 elements, each lane receives the four k of
@@ -72,7 +84,7 @@ struct TpLoader {
         const int t = threadIdx.x;
         if constexpr (KC) {
             const int r = t >> 3, slot = t & 7;
-            const int c = slot ^ (r & 7) ^ ((r >> 3) & 1);
+            const int c = slot ^ ((r >> 1) & 7);
             kchunk = c * 8;
             voff = (uint32_t)(r * ld + c * 8) * 2u;
         } else {
@@ -83,10 +95,12 @@ struct TpLoader {
             voff = (uint32_t)(k * ld + c * 8) * 2u;
         }
     }
-    // fetch the tile at k0 of a plane into lds; live = false fetches nothing (zeros)
-    __device__ __forceinline__ void fetch(const uint16_t* p, int64_t ld, int rows, int K, int r0, int k0,
-                                          bool live, uint16_t* lds) {
-        asm volatile("" : "+v"(voff));  // the loads' offsets are formed here, not kept
+    __amdgpu_buffer_rsrc_t rs;
+    int k_left;      // of this turn
+    uint32_t ahead;  // bytes from one tile to the next one's
+    // the tiles of a turn from k0 of a plane; live = false: zeros
+    __device__ __forceinline__ void prepare(const uint16_t* p, int64_t ld, int rows, int K, int r0, int k0,
+                                            bool live) {
         // a row of k ends at a whole chunk (what lies between is zero or meets zeros), and so
         // does a row of rows (the sums of what lies beyond are not stored)
         if (KC) K = (K + 7) & ~7;
@@ -95,15 +109,21 @@ struct TpLoader {
         const int64_t total = KC ? (int64_t)(rows - 1) * ld + K : (int64_t)(K - 1) * ld + rows;
         int64_t bytes = (total - first) * 2;
         bytes = bytes < (int64_t)kTpMaxBytes ? bytes : (int64_t)kTpMaxBytes;
-        const __amdgpu_buffer_rsrc_t rs = buf_rsrc(p + first, live && bytes > 0 ? (uint32_t)bytes : 0u);
+        rs = buf_rsrc(p + first, live && bytes > 0 ? (uint32_t)bytes : 0u);
+        k_left = K - k0;
+        ahead = (KC ? 1u : (uint32_t)ld) * 128u;
+    }
+    // fetch tile u of the turn into lds (offsets beyond the end stay there: the tiles of a turn span less
+    // than 2 GiB)
+    __device__ __forceinline__ void issue(int64_t ld, int u, uint16_t* lds) {
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        asm volatile("" : "+v"(voff));  // the loads' offsets are formed here, not kept
+        uint32_t v = voff + u * ahead;
+        if (KC) v = u * 64 + kchunk < k_left ? v : kTpBeyond;
 #pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            uint32_t v = voff + (uint32_t)(i * STEP * ld) * 2u;
-            if (KC) v = k0 + kchunk < K ? v : kTpBeyond;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (SC_LDS void*)(lds + i * NT * 8 + wave * 512), 16, v, 0,
-                                                     0, 0);
-        }
+        for (int i = 0; i < NL; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (SC_LDS void*)(lds + i * NT * 8 + wave * 512), 16,
+                                                     v + (uint32_t)(i * STEP * ld) * 2u, 0, 0, 0);
     }
 };
 
@@ -115,8 +135,7 @@ struct TpReader {
     __device__ __forceinline__ void init(int w0) {
         const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
         if constexpr (KC) {
-            const int f = (j & 7) ^ ((j >> 3) & 1);
-            off = (w0 + j) * 64 + ((g ^ f) << 3);
+            off = (w0 + j) * 64 + ((g ^ (j >> 1)) << 3);
         } else {
             const int k = g * 8 + (j >> 2);
             off = k * R + (((w0 / 16) ^ tp_swz<R>(k)) << 4) + (j & 3) * 4;
@@ -125,7 +144,7 @@ struct TpReader {
     // The offsets are formed anew where this is called: kept in registers over the loop they
     // would not fit beside the sums.
     __device__ __forceinline__ void renew() { asm volatile("" : "+v"(off)); }
-    // the 8 k values (kk * 32 + 8 * (lane / 16) ..) of row w0 + 16 b + lane % 16
+    // the 8 k values (32 kk + 8 * (lane / 16) ..) of row w0 + 16 b + lane % 16
     __device__ __forceinline__ v8bf read(const uint16_t* lds, int kk, int b) const {
         if constexpr (KC) {
             return *(const v8bf*)(lds + (off ^ kk << 5) + b * 16 * 64);
@@ -230,9 +249,9 @@ enum TpEpi {
     TP_GRAD = 3,    // exp(acc - lse[m]) - [n is m's target], as bfloat16 planes
 };
 
-template <int BM_, int BN_, int WVM_, int WVN_, int NST_, int PER_CU_>
+template <int BM_, int BN_, int WVM_, int WVN_, int NBUF_, int PER_CU_>
 struct TpShape {
-    static constexpr int BM = BM_, BN = BN_, WVM = WVM_, WVN = WVN_, NST = NST_, PER_CU = PER_CU_;
+    static constexpr int BM = BM_, BN = BN_, WVM = WVM_, WVN = WVN_, NBUF = NBUF_, PER_CU = PER_CU_;
     static constexpr int NT = 64 * WVM * WVN;
     static constexpr int WAVES = WVM * WVN * PER_CU / 4;  // per SIMD
 };
@@ -259,14 +278,15 @@ __device__ __forceinline__ void tp_lds_barrier() {
 
 template <class S, bool AKC, bool BKC, int EPI>
 __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpArgs P) {
-    constexpr int BM = S::BM, BN = S::BN, NT = S::NT, NST = S::NST;
+    constexpr int BM = S::BM, BN = S::BN, NT = S::NT;
+    constexpr int NBUF = S::NBUF;
     constexpr int WM = BM / S::WVM, WN = BN / S::WVN, MI = WM / 16, NI = WN / 16;
     using LA = TpLoader<BM, NT, AKC>;
     using LB = TpLoader<BN, NT, BKC>;
     constexpr int ASZ = BM * 64, BSZ = BN * 64;
+    static_assert(NBUF == 2 || NBUF == 3, "buffers");
     __shared__ __align__(1024) uint16_t a0[ASZ], b0[BSZ], a1[ASZ], b1[BSZ];
-    __shared__ __align__(1024) uint16_t a2[NST > 2 ? ASZ : 8], b2[NST > 2 ? BSZ : 8];
-    __shared__ __align__(1024) uint16_t a3[NST > 3 ? ASZ : 8], b3[NST > 3 ? BSZ : 8];
+    __shared__ __align__(1024) uint16_t a2[NBUF > 2 ? ASZ : 8], b2[NBUF > 2 ? BSZ : 8];
     __shared__ float red[EPI == TP_STATS ? 2 * S::WVN * BM : 1];  // row maxima, then sums
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -283,13 +303,14 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
 
     v4f acc[MI][NI];
 
-    const int ksteps = (P.K + 63) / 64, total = ksteps * P.nseg;
+    // k goes in turns of the buffers; what lies past its end multiplies zeros.
+    const int kturns = (P.K + 64 * NBUF - 1) / (64 * NBUF), total = kturns * P.nseg;
     const int per = (total + P.splits - 1) / P.splits;
     const int tiles = P.tiles_m * P.tiles_n, all = tiles * P.splits;
 
-    // the step that is fetched next: its tile, segment and k
+    // the turn that is fetched next: its tile, segment and place in the segment
     struct Ahead {
-        int m0, n0, seg, kst, left;
+        int m0, n0, seg, kt, left;
     } ah;
     auto begin_tile = [&](int turn) SC_INLINE {
         const int id = turn < all ? xcd_remap(turn, all) : 0;
@@ -298,299 +319,306 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
         tp_tile(id - split * tiles, P.tiles_m, P.tiles_n, tm, tn);
         ah.m0 = tm * BM;
         ah.n0 = tn * BN;
-        const int step = split * per;
-        ah.left = turn < all ? min(total, step + per) - step : 0;
-        ah.seg = step / ksteps;
-        ah.kst = step - ah.seg * ksteps;
+        const int at = split * per;
+        ah.left = turn < all ? min(total, at + per) - at : 0;
+        ah.seg = at / kturns;
+        ah.kt = at - ah.seg * kturns;
     };
-    auto fetch = [&](uint16_t* as, uint16_t* bs) SC_INLINE {
+    auto prepare = [&]() SC_INLINE {
         const bool live = ah.left > 0;
         const uint32_t planes = live ? (uint32_t)(P.segs >> (4 * ah.seg)) : 0;
-        la.fetch(P.A + (planes & 3) * P.a_plane, P.lda, P.M, P.K, ah.m0, ah.kst * 64, live, as);
-        lb.fetch(P.B + ((planes >> 2) & 3) * P.b_plane, P.ldb, P.N, P.K, ah.n0, ah.kst * 64, live, bs);
+        const int k0 = ah.kt * 64 * NBUF;
+        la.prepare(P.A + (planes & 3) * P.a_plane, P.lda, P.M, P.K, ah.m0, k0, live);
+        lb.prepare(P.B + ((planes >> 2) & 3) * P.b_plane, P.ldb, P.N, P.K, ah.n0, k0, live);
         --ah.left;
-        const bool wrap = ++ah.kst == ksteps;
-        ah.kst = wrap ? 0 : ah.kst;
+        const bool wrap = ++ah.kt == kturns;
+        ah.kt = wrap ? 0 : ah.kt;
         ah.seg += wrap;
     };
-    // A step's products go in four phases: each 32-deep half of k, in two groups of MI / 2 row
-    // blocks.  A phase reads the fragments of the next one while it multiplies.
+    auto issue = [&](int u, uint16_t* as, uint16_t* bs) SC_INLINE {
+        la.issue(P.lda, u, as);
+        lb.issue(P.ldb, u, bs);
+    };
+    // A step's products go in two phases, of MI / 2 row blocks each; a phase reads fragments of
+    // the next step (half kk of a buffer) while it multiplies.
     constexpr int MG = MI / 2;
-    v8bf fa[2][MG], fb[2][NI];
-    auto read_a = [&](const uint16_t* as, int kk, int grp) SC_INLINE {
+    v8bf fa[2][2][MG], fb[2][NI];  // [step's parity]
+    // Products in place in the accumulation registers: left to itself the register allocator
+    // moves sums about and spills fragments.
+    auto product = [&](int cur, int grp, int p) SC_INLINE {
+        const int i = p / NI, j = p % NI;  // transposed: a lane's four sums are consecutive n
+        asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0"
+                     : "+a"(acc[grp * MG + i][j])
+                     : "v"(fb[cur][j]), "v"(fa[cur][grp][i]));
+    };
+    // The products of a group, and spread between them the next step's reads of A's group and,
+    // with the first group, of B.
+    auto phase = [&](auto parity, auto group, const uint16_t* as, const uint16_t* bs, int kk) SC_INLINE {
+        constexpr int cur = decltype(parity)::value, nxt = cur ^ 1, grp = decltype(group)::value;
+        constexpr int READS = MG + (grp == 0 ? NI : 0), PRODS = MG * NI;
         ra.renew();
+        if constexpr (grp == 0) rb.renew();
 #pragma unroll
-        for (int i = 0; i < MG; ++i) fa[grp][i] = ra.read(as, kk, grp * MG + i);
-    };
-    auto read_b = [&](const uint16_t* bs, int kk) SC_INLINE {
-        rb.renew();
+        for (int p = 0; p < PRODS; ++p) {
 #pragma unroll
-        for (int j = 0; j < NI; ++j) fb[kk][j] = rb.read(bs, kk, j);
-    };
-    auto multiply = [&](int kk, int grp) SC_INLINE {
-#pragma unroll
-        for (int i = 0; i < MG; ++i)
-#pragma unroll
-            for (int j = 0; j < NI; ++j)  // transposed: a lane's four sums are consecutive n
-                acc[grp * MG + i][j] =
-                    __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[kk][j], fa[grp][i], acc[grp * MG + i][j], 0, 0, 0);
-    };
-    // one phase's products with the reads spread between them
-    auto spread = [&](auto reads) SC_INLINE {
-        constexpr int READS = decltype(reads)::value, PRODS = MG * NI;
-        constexpr int EVERY = PRODS / READS > 0 ? PRODS / READS : 1, AT_ONCE = (READS + PRODS - 1) / PRODS;
-#pragma unroll
-        for (int r = 0; r < READS / AT_ONCE; ++r) {
-            __builtin_amdgcn_sched_group_barrier(0x100, AT_ONCE, 0);  // LDS reads
-            __builtin_amdgcn_sched_group_barrier(0x008, EVERY, 0);    // products
+            for (int r = (p * READS + PRODS - 1) / PRODS; r < ((p + 1) * READS + PRODS - 1) / PRODS; ++r) {
+                if (grp == 0 && r < NI) fb[nxt][r] = rb.read(bs, kk, r);
+                else fa[nxt][grp][r - (grp == 0 ? NI : 0)] = ra.read(as, kk, grp * MG + r - (grp == 0 ? NI : 0));
+            }
+            product(cur, grp, p);
+            __builtin_amdgcn_sched_barrier(0x6);  // scalar and vector arithmetic may pass
         }
-        __builtin_amdgcn_sched_barrier(0);
     };
-    using ReadsA = std::integral_constant<int, (AKC ? 1 : 2) * MG>;
-    using ReadsAB = std::integral_constant<int, (AKC ? 1 : 2) * MG + (BKC ? 1 : 2) * NI>;
-    // every step issues the same number of loads (the ones past the end fetch nothing)
+    using P0 = std::integral_constant<int, 0>;
+    using P1 = std::integral_constant<int, 1>;
+    using Yes = std::true_type;
+    using No = std::false_type;
+    // every tile of a turn takes the same number of loads (the ones past the end fetch nothing)
     constexpr int PER = LA::NL + LB::NL;
-    // On entry the fragments of this step's first phase are read or on their way.
-    auto step = [&](uint16_t* as, uint16_t* bs, const uint16_t* an, const uint16_t* bn) SC_INLINE {
-        read_a(as, 0, 1);
-        multiply(0, 0);
-        spread(ReadsA{});
-        read_a(as, 1, 0);
-        read_b(bs, 1);
-        multiply(0, 1);
-        spread(ReadsAB{});
-        read_a(as, 1, 1);
-        multiply(1, 0);
-        spread(ReadsA{});
-        // this wave's loads of the next step have landed and its reads of this step's buffer
-        // are done; after the barrier that holds for every wave
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(PER * (NST - 2)) : "memory");
+    // Buffer u of a turn: its halves' fragments are read during the products of the step before
+    // each.  Then it is free and filled with the tile NBUF further on.
+    auto buffer = [&](int u, uint16_t* as, uint16_t* bs) SC_INLINE {
+        phase(P1{}, P0{}, as, bs, 0);
+        phase(P1{}, P1{}, as, bs, 0);
+        phase(P0{}, P0{}, as, bs, 1);
+        phase(P0{}, P1{}, as, bs, 1);
+        // this wave's loads of the next buffer have landed and its reads of this one are done;
+        // after the barrier that holds for every wave
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(PER * (NBUF - 2)) : "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        fetch(as, bs);
-        __builtin_amdgcn_sched_barrier(0);  // the loads go out before the products
-        read_a(an, 0, 0);
-        read_b(bn, 0);
-        multiply(1, 1);
-        spread(ReadsAB{});
+        issue(u, as, bs);
+        __builtin_amdgcn_sched_barrier(0x6);  // the loads go out before the products
     };
     begin_tile(blockIdx.x);
-    fetch(a0, b0);
-    fetch(a1, b1);
-    if constexpr (NST > 2) fetch(a2, b2);
-    if constexpr (NST > 3) fetch(a3, b3);
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(PER * (NST - 1)) : "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
+    prepare();
+    issue(0, a0, b0);
+    issue(1, a1, b1);
+    if constexpr (NBUF > 2) issue(2, a2, b2);
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(PER * (NBUF - 1)) : "memory");
 
     for (int turn = blockIdx.x; turn < all; turn += gridDim.x) {
-    const int id = xcd_remap(turn, all), split = id / tiles;
-    int tm, tn;
-    tp_tile(id - split * tiles, P.tiles_m, P.tiles_n, tm, tn);
-    const int m0 = tm * BM, n0 = tn * BN;
+        const int id = xcd_remap(turn, all), split = id / tiles;
+        int tm, tn;
+        tp_tile(id - split * tiles, P.tiles_m, P.tiles_n, tm, tn);
+        const int m0 = tm * BM, n0 = tn * BN;
+        // (TP_STATS: a column past the last one starts at -infinity and, its operand being zero, stays)
 #pragma unroll
-    for (int i = 0; i < MI; ++i)
+        for (int j = 0; j < NI; ++j) {
+            v4f start = {0.f, 0.f, 0.f, 0.f};
+            if constexpr (EPI == TP_STATS) {
 #pragma unroll
-        for (int j = 0; j < NI; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-    // (the last step of the tile before has read these too, or they are the first)
-    read_a(a0, 0, 0);
-    read_b(b0, 0);
-    // whole turns of the buffers, one at least: the steps past the end multiply zeros
-    int left = max(1, min(total, split * per + per) - split * per);
-    for (; left > 0; left -= NST) {
-        if (left <= NST) begin_tile(turn + gridDim.x);  // the last turn fetches the next tile's first steps
-        if constexpr (NST == 2) {
-            step(a0, b0, a1, b1);
-            step(a1, b1, a0, b0);
-        } else if constexpr (NST == 3) {
-            step(a0, b0, a1, b1);
-            step(a1, b1, a2, b2);
-            step(a2, b2, a0, b0);
-        } else {
-            step(a0, b0, a1, b1);
-            step(a1, b1, a2, b2);
-            step(a2, b2, a3, b3);
-            step(a3, b3, a0, b0);
+                for (int r = 0; r < 4; ++r) {
+                    const int n = n0 + wn + 16 * j + 4 * ((threadIdx.x & 63) >> 4) + r;
+                    start[r] = n < P.N ? 0.0f : -__builtin_huge_valf();
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < MI; ++i) acc[i][j] = start;
         }
-    }
+        // Every step reads the next one's fragments: the first reads come with products of zeros.
+        const v8bf zeros = {};
+#pragma unroll
+        for (int j = 0; j < NI; ++j) fb[1][j] = zeros;
+#pragma unroll
+        for (int i = 0; i < MI; ++i) fa[1][i / MG][i % MG] = zeros;
+        __builtin_amdgcn_s_barrier();  // the first buffer has landed for every wave
+        asm volatile("s_nop 7" ::: "memory");  // and the zeros are written
+        for (int turns = max(1, min(total, split * per + per) - split * per); turns > 0; --turns) {
+            if (turns == 1) begin_tile(turn + gridDim.x);  // the last turn fetches the next tile's first one
+            prepare();
+            buffer(0, a0, b0);
+            buffer(1, a1, b1);
+            if constexpr (NBUF > 2) buffer(2, a2, b2);
+        }
+#pragma unroll
+        for (int grp = 0; grp < 2; ++grp)
+#pragma unroll
+            for (int p = 0; p < MG * NI; ++p) product(1, grp, p);  // the last step's
+        // The next tile's buffers land before the stores go out: its first steps would else wait
+        // for those too.
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
-    // Lane l holds, of block (i, j): row m = wm + 16 i + l % 16, columns
-    // n = wn + 16 j + 4 (l / 16) + 0..3.
-    // (formed anew for every tile: the registers are the main loop's)
-    int lane = threadIdx.x & 63;
-    asm volatile("" : "+v"(lane));
-    const int lm = m0 + wm + (lane & 15), ln = n0 + wn + 4 * (lane >> 4);
-    const int M = P.M, N = P.N;
-    const bool whole = n0 + BN <= N;  // all columns of the tile exist
-    if constexpr (EPI == TP_STORE) {
-        const float alpha = P.alpha ? gld(P.alpha) : 1.0f;
-        float g[NI][4];
+        // The last products are written before other instructions read them.  Row blocks leave the
+        // accumulation registers one at a time.
+        asm volatile("s_nop 15\n\ts_nop 3" ::: "memory");
+        auto row_block = [&](int i) SC_INLINE {
 #pragma unroll
-        for (int j = 0; j < NI; ++j)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) g[j][r] = alpha;
-        if (P.gain) {
-            auto scale = [&](auto* gain) SC_INLINE {
-                using G = std::remove_const_t<std::remove_pointer_t<decltype(gain)>>;
-#pragma unroll
-                for (int j = 0; j < NI; ++j)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) g[j][r] *= Elem<G>::load(gain, min(ln + 16 * j + r, N - 1));
-            };
-            if (P.gain_bf16) scale((const uint16_t*)P.gain);
-            else scale((const float*)P.gain);
-        }
-        if (P.c_bf16 && whole) {
-#pragma unroll
-            for (int i = 0; i < MI; ++i) {
-                const int m = lm + 16 * i;
-                uint32_t d[NI][2];
-#pragma unroll
-                for (int j = 0; j < NI; ++j)
-#pragma unroll
-                    for (int w = 0; w < 2; ++w)
-                        d[j][w] = pack_bf16x2(acc[i][j][2 * w] * g[j][2 * w], acc[i][j][2 * w + 1] * g[j][2 * w + 1]);
-                const int c = tp_gather_row<NI>(d);
-                if (m < M) tp_store_row<NI>((uint16_t*)P.C + (int64_t)m * P.ldc + n0 + wn + c, d);
-            }
-        } else {
-            auto store = [&](auto bf16) SC_INLINE {
-#pragma unroll
-                for (int i = 0; i < MI; ++i)
-#pragma unroll
-                    for (int j = 0; j < NI; ++j) {
-                        const int m = lm + 16 * i, n = ln + 16 * j;
-                        const float v[4] = {acc[i][j][0] * g[j][0], acc[i][j][1] * g[j][1], acc[i][j][2] * g[j][2],
-                                            acc[i][j][3] * g[j][3]};
-                        if (m < M) tp_store(P.C, decltype(bf16)::value, (int64_t)m * P.ldc + n, v, N - n);
-                    }
-            };
-            if (P.c_bf16) store(std::true_type{});
-            else store(std::false_type{});
-        }
-    } else if constexpr (EPI == TP_PART) {
-#pragma unroll
-        for (int i = 0; i < MI; ++i)
-#pragma unroll
-            for (int j = 0; j < NI; ++j) {
-                const int m = lm + 16 * i, n = ln + 16 * j;
-                const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-                if (m < M) tp_store(P.part, 0, ((int64_t)split * M + m) * N + n, v, N - n);
-            }
-    } else if constexpr (EPI == TP_STATS) {
-        // row maximum over the tile's columns: registers, the four lanes of a row, the
-        // waves beside each other
-        int hit[MI];  // the target's column in this wave's part, or -1
-#pragma unroll
-        for (int i = 0; i < MI; ++i) {
-            const int64_t t = gld(P.targets + min(lm + 16 * i, M - 1)) - P.n_first;
-            const int64_t c = t - (n0 + wn);
-            hit[i] = lm + 16 * i < M && t < N && c >= 0 && c < WN ? (int)c : -1;
-        }
-        if (!whole) {
-#pragma unroll
-            for (int i = 0; i < MI; ++i)
-#pragma unroll
-                for (int j = 0; j < NI; ++j)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (ln + 16 * j + r >= N) acc[i][j][r] = -__builtin_huge_valf();
-        }
-        const bool pow2 = P.keep == TP_KEEP_EXP;
-#pragma unroll
-        for (int i = 0; i < MI; ++i) {
-            float v = acc[i][0][0];
+            for (int j = 0; j < NI; ++j) asm volatile("" : "+a"(acc[i][j]));
+        };
+
+        // Lane l holds, of block (i, j): row m = wm + 16 i + l % 16, columns
+        // n = wn + 16 j + 4 (l / 16) + 0..3.
+        // (formed anew for every tile: the registers are the main loop's)
+        int lane = threadIdx.x & 63;
+        asm volatile("" : "+v"(lane));
+        const int lm = m0 + wm + (lane & 15), ln = n0 + wn + 4 * (lane >> 4);
+        const int M = P.M, N = P.N;
+        const bool whole = n0 + BN <= N;  // all columns of the tile exist
+        if constexpr (EPI == TP_STORE) {
+            const float alpha = P.alpha ? gld(P.alpha) : 1.0f;
+            float g[NI][4];
 #pragma unroll
             for (int j = 0; j < NI; ++j)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) v = fmaxf(v, acc[i][j][r]);
-            v = fmaxf(v, __shfl_xor(v, 16));
-            v = fmaxf(v, __shfl_xor(v, 32));
-            if (lane < 16) red[(wave % S::WVN) * BM + wm + 16 * i + lane] = v;
-            if (__ballot(hit[i] >= 0)) {
+                for (int r = 0; r < 4; ++r) g[j][r] = alpha;
+            if (P.gain) {
+                auto scale = [&](auto* gain) SC_INLINE {
+                    using G = std::remove_const_t<std::remove_pointer_t<decltype(gain)>>;
+#pragma unroll
+                    for (int j = 0; j < NI; ++j)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) g[j][r] *= Elem<G>::load(gain, min(ln + 16 * j + r, N - 1));
+                };
+                if (P.gain_bf16) scale((const uint16_t*)P.gain);
+                else scale((const float*)P.gain);
+            }
+            if (P.c_bf16 && whole) {
+#pragma unroll
+                for (int i = 0; i < MI; ++i) {
+                    row_block(i);
+                    const int m = lm + 16 * i;
+                    uint32_t d[NI][2];
+#pragma unroll
+                    for (int j = 0; j < NI; ++j)
+#pragma unroll
+                        for (int w = 0; w < 2; ++w)
+                            d[j][w] = pack_bf16x2(acc[i][j][2 * w] * g[j][2 * w],
+                                                  acc[i][j][2 * w + 1] * g[j][2 * w + 1]);
+                    const int c = tp_gather_row<NI>(d);
+                    if (m < M) tp_store_row<NI>((uint16_t*)P.C + (int64_t)m * P.ldc + n0 + wn + c, d);
+                }
+            } else {
+                auto store = [&](auto bf16) SC_INLINE {
+#pragma unroll
+                    for (int i = 0; i < MI; ++i) {
+                        row_block(i);
+#pragma unroll
+                        for (int j = 0; j < NI; ++j) {
+                            const int m = lm + 16 * i, n = ln + 16 * j;
+                            float v[4];
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) v[r] = acc[i][j][r] * g[j][r];
+                            if (m < M) tp_store(P.C, decltype(bf16)::value, (int64_t)m * P.ldc + n, v, N - n);
+                        }
+                    }
+                };
+                if (P.c_bf16) store(std::true_type{});
+                else store(std::false_type{});
+            }
+        } else if constexpr (EPI == TP_PART) {
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                row_block(i);
+#pragma unroll
+                for (int j = 0; j < NI; ++j) {
+                    const int m = lm + 16 * i, n = ln + 16 * j;
+                    const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+                    if (m < M) tp_store(P.part, 0, ((int64_t)split * M + m) * N + n, v, N - n);
+                }
+            }
+        } else if constexpr (EPI == TP_STATS) {
+            // row maximum over the tile's columns: registers, the four lanes of a row, the
+            // waves beside each other
+            int hit[MI];  // the target's column in this wave's part, or -1
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                const int64_t t = gld(P.targets + min(lm + 16 * i, M - 1)) - P.n_first;
+                const int64_t c = t - (n0 + wn);
+                hit[i] = lm + 16 * i < M && t < N && c >= 0 && c < WN ? (int)c : -1;
+            }
+            const bool pow2 = P.keep == TP_KEEP_EXP;
+            float* sums = red + S::WVN * BM;
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                row_block(i);
+                float v = -__builtin_huge_valf();
 #pragma unroll
                 for (int j = 0; j < NI; ++j)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (hit[i] == 16 * j + 4 * (lane >> 4) + r) gst(P.target_logit + lm + 16 * i, acc[i][j][r]);
-            }
-        }
-        tp_lds_barrier();
-        float* sums = red + S::WVN * BM;
-#pragma unroll
-        for (int i = 0; i < MI; ++i) {
-            const int m = lm + 16 * i;
-            float mx = red[wm + 16 * i + (lane & 15)];
-#pragma unroll
-            for (int w = 1; w < S::WVN; ++w) mx = fmaxf(mx, red[w * BM + wm + 16 * i + (lane & 15)]);
-            const float ref = tp_reference(mx, pow2);
-            float z = 0.0f;
-            uint32_t d[NI][2];
-            if (pow2) {
-#pragma unroll
-                for (int j = 0; j < NI; ++j) {
-                    float e[4];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        e[r] = __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], kLog2e, -ref));
-                        z += e[r];
-                    }
-                    d[j][0] = pack_bf16x2(e[0], e[1]);
-                    d[j][1] = pack_bf16x2(e[2], e[3]);
-                }
-                uint16_t* p = (uint16_t*)P.P + (int64_t)m * P.ldp;
-                if (whole) {
-                    const int c = tp_gather_row<NI>(d);
-                    if (m < M) tp_store_row<NI>(p + n0 + wn + c, d);
-                } else if (m < M) {
+                    for (int r = 0; r < 4; ++r) v = fmaxf(v, acc[i][j][r]);
+                v = fmaxf(v, __shfl_xor(v, 16));
+                v = fmaxf(v, __shfl_xor(v, 32));
+                if (lane < 16) red[(wave % S::WVN) * BM + wm + 16 * i + lane] = v;
+                if (__ballot(hit[i] >= 0)) {
 #pragma unroll
                     for (int j = 0; j < NI; ++j)
-                        if (ln + 16 * j < P.ldp) *(SC_GLOBAL v2u*)(p + ln + 16 * j) = v2u{d[j][0], d[j][1]};
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if (hit[i] == 16 * j + 4 * (lane >> 4) + r)
+                                gst(P.target_logit + lm + 16 * i, acc[i][j][r]);
                 }
-            } else {
+            }
+            tp_lds_barrier();
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                row_block(i);
+                const int m = lm + 16 * i;
+                float mx = red[wm + 16 * i + (lane & 15)];
+#pragma unroll
+                for (int w = 1; w < S::WVN; ++w) mx = fmaxf(mx, red[w * BM + wm + 16 * i + (lane & 15)]);
+                const float ref = tp_reference(mx, pow2);
+                float z = 0.0f;
+                uint32_t d[NI][2];
+                if (pow2) {
+#pragma unroll
+                    for (int j = 0; j < NI; ++j) {
+                        float e[4];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            e[r] = __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], kLog2e, -ref));
+                            z += e[r];
+                        }
+                        d[j][0] = pack_bf16x2(e[0], e[1]);
+                        d[j][1] = pack_bf16x2(e[2], e[3]);
+                    }
+                    uint16_t* p = (uint16_t*)P.P + (int64_t)m * P.ldp;
+                    const int c = tp_gather_row<NI>(d);
+                    if (m < M) tp_store_row<NI>(p + n0 + wn + c, d);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < NI; ++j) {
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) z += __builtin_amdgcn_exp2f((acc[i][j][r] - ref) * kLog2e);
+                        if (P.keep == TP_KEEP_LOGIT && m < M)
+                            gst4((float*)P.P + (int64_t)m * P.ldp + ln + 16 * j, acc[i][j]);
+                    }
+                }
+                z += __shfl_xor(z, 16);
+                z += __shfl_xor(z, 32);
+                if (lane < 16) sums[(wave % S::WVN) * BM + wm + 16 * i + lane] = z;
+                if (wave % S::WVN == 0 && lane < 16 && m < M)
+                    gst(P.stat_max + (int64_t)(P.stat_first + tn) * M + m,
+                        mx == -__builtin_huge_valf() ? mx : ref);
+            }
+            tp_lds_barrier();
+            for (int r = threadIdx.x; r < BM; r += NT) {
+                float z = sums[r];
+#pragma unroll
+                for (int w = 1; w < S::WVN; ++w) z += sums[w * BM + r];
+                if (m0 + r < M) gst(P.stat_sum + (int64_t)(P.stat_first + tn) * M + m0 + r, z);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                const int m = lm + 16 * i;
+                row_block(i);
+                if (m >= M) continue;
+                const int64_t tgt = tp_target(P.targets, P.vocab, m);
+                const float lse = gld(P.lse + m);
 #pragma unroll
                 for (int j = 0; j < NI; ++j) {
+                    const int n = ln + 16 * j;
+                    float v[4];
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) z += __builtin_amdgcn_exp2f((acc[i][j][r] - ref) * kLog2e);
-                    if (P.keep == TP_KEEP_LOGIT && m < M && ln + 16 * j < P.ldp)
-                        gst4((float*)P.P + (int64_t)m * P.ldp + ln + 16 * j, acc[i][j]);
+                    for (int r = 0; r < 4; ++r)
+                        v[r] = tgt >= 0 && n + r < N ? __builtin_amdgcn_exp2f((acc[i][j][r] - lse) * kLog2e) -
+                                                           (P.n_first + n + r == tgt ? 1.0f : 0.0f)
+                                                     : 0.0f;
+                    tp_store_planes((uint16_t*)P.P, P.p_planes, P.p_plane, (int64_t)m * P.ldp + n, v);
                 }
             }
-            z += __shfl_xor(z, 16);
-            z += __shfl_xor(z, 32);
-            if (lane < 16) sums[(wave % S::WVN) * BM + wm + 16 * i + lane] = z;
-            if (wave % S::WVN == 0 && lane < 16 && m < M)
-                gst(P.stat_max + (int64_t)(P.stat_first + tn) * M + m,
-                    mx == -__builtin_huge_valf() ? mx : ref);
         }
-        tp_lds_barrier();
-        for (int r = threadIdx.x; r < BM; r += NT) {
-            float z = sums[r];
-#pragma unroll
-            for (int w = 1; w < S::WVN; ++w) z += sums[w * BM + r];
-            if (m0 + r < M) gst(P.stat_sum + (int64_t)(P.stat_first + tn) * M + m0 + r, z);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < MI; ++i) {
-            const int m = lm + 16 * i;
-            if (m >= M) continue;
-            const int64_t tgt = tp_target(P.targets, P.vocab, m);
-            const float lse = gld(P.lse + m);
-#pragma unroll
-            for (int j = 0; j < NI; ++j) {
-                const int n = ln + 16 * j;
-                if (n >= P.ldp) continue;
-                float v[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    v[r] = tgt >= 0 && n + r < N ? __builtin_amdgcn_exp2f((acc[i][j][r] - lse) * kLog2e) -
-                                                       (P.n_first + n + r == tgt ? 1.0f : 0.0f)
-                                                 : 0.0f;
-                tp_store_planes((uint16_t*)P.P, P.p_planes, P.p_plane, (int64_t)m * P.ldp + n, v);
-            }
-        }
-    }
     }
     // loads past the end may still be on their way into LDS
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");

@@ -42,7 +42,7 @@ struct TpArgs {
     int64_t n_first = 0;  // the vocabulary row of column 0
     int keep = 0;
     void* P = nullptr;
-    int64_t ldp = 0;         // columns of P, written up to it
+    int64_t ldp = 0;         // row stride of P; its rows hold whole tiles
     int64_t p_plane = 0;     // TP_GRAD: elements between planes
     int p_planes = 1;        // TP_GRAD: 1 or 3
     float* target_logit = nullptr;

@@ -168,7 +168,7 @@ XentPlan xent_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit) {
     const int nseg = bf16 ? 1 : 6;
     // bytes of a vocabulary column: the kept exponentials, or the logits and d's planes
     const int64_t col_kept = T * (bf16 ? 2 : 10), col_piece = T * (bf16 ? 2 : 6);
-    p.keep = up(V, 64) * col_kept <= limit;
+    p.keep = up(V, 256) * col_kept <= limit;
     p.piece = V;
     if (!p.keep) {
         p.piece = limit / col_piece / 256 * 256;
@@ -176,7 +176,7 @@ XentPlan xent_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit) {
         if (p.piece > V) p.piece = V;
     }
     p.pieces = (int)((V + p.piece - 1) / p.piece);
-    p.ldp = tp_pad(up(p.piece, 64));
+    p.ldp = tp_pad(up(p.piece, 256));  // the logits' tiles are stored whole
     const int64_t last = V - (int64_t)(p.pieces - 1) * p.piece;
     p.logits = tp_plan((int)T, (int)p.piece, (int)H, nseg, false);
     p.logits_last = tp_plan((int)T, (int)last, (int)H, nseg, false);
