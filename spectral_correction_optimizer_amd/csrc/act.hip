@@ -24,8 +24,9 @@ int64_t up(int64_t n, int64_t a) { return (n + a - 1) / a * a; }
 
 }  // namespace
 
-// A thread converts kGroups groups of 8 elements.  The four threads of a block of 32 are neighbours in a wave, and whole blocks
-// leave the loop together (groups and strides are multiples of 4).
+// A thread converts kGroups groups of 8 elements.  The four threads of a block of 32 are
+// neighbours in a wave, and whole blocks leave the loop together (groups and strides are
+// multiples of 4).
 template <typename E, int ENDS>
 __global__ __launch_bounds__(256) void act_pack_kernel(const E* __restrict__ x, int64_t T, int H, int8_t* q,
                                                        uint8_t* e) {

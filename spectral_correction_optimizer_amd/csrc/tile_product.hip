@@ -31,19 +31,25 @@ __global__ __launch_bounds__(256) void tp_reduce_kernel(const TpArgs P, const fl
         const int left = P.N - n;
         const int64_t at = m * P.N + n, stride = (int64_t)P.M * P.N;
         float v[4] = {0.f, 0.f, 0.f, 0.f};
-        auto add = [&](const float* p) {
-            if (left >= 4) {
-                const v4f_any x = *(const SC_GLOBAL v4f_any*)p;
+        if (left >= 4) {
+            if (acc) {
+                const v4f_any x = *(const SC_GLOBAL v4f_any*)(acc + at);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v[r] = x[r];
+            }
+#pragma unroll 8
+            for (int s = 0; s < P.splits; ++s) {
+                const v4f_any x = *(const SC_GLOBAL v4f_any*)(P.part + s * stride + at);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) v[r] += x[r];
-            } else {
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (r < left) v[r] += gld(p + r);
             }
-        };
-        if (acc) add(acc + at);
-        for (int s = 0; s < P.splits; ++s) add(P.part + s * stride + at);
+        } else {
+            for (int r = 0; r < left; ++r) {
+                float sum = acc ? gld(acc + at + r) : 0.0f;
+                for (int s = 0; s < P.splits; ++s) sum += gld(P.part + s * stride + at + r);
+                v[r] = sum;
+            }
+        }
         if (out_acc) {
             tp_store(out_acc, 0, at, v, left);
         } else {
@@ -55,29 +61,36 @@ __global__ __launch_bounds__(256) void tp_reduce_kernel(const TpArgs P, const fl
 }
 
 // Choice of tile and split: the least estimated time.  A workgroup's 64-deep step takes
-// `step` us with the chip full; a split's partial sums are written and read once more.
+// `step` us with the chip full and a tile `tile` us beside its steps (its first reads, its
+// stores); steps come in whole turns of `turn` buffers for every segment.  Fitted to bf16
+// products with both operands' rows contiguous, N x H from T tokens; us of the three shapes:
+//   8192 x 2048, T 16384:  436, 614, 829    8192 x 8192, T 2048: 317, 336, 429
+//   16384 x 4096, T 512:   101, 106, 119    32768 x 2048, T 64:   54,  49,  63
+// A split's partial sums are written and read once more, at about 5 TB/s, by another kernel.
 TpPlan tp_plan(int M, int N, int K, int nseg, bool may_split) {
     struct Shape {
-        int bm, bn, per_cu;
-        double step;
+        int bm, bn, per_cu, turn;
+        double step, tile;
     };
-    static const Shape shapes[3] = {{256, 256, 1, 1.95}, {128, 128, 2, 1.30}, {64, 128, 2, 0.98}};
-    const int64_t steps = (int64_t)((K + 63) / 64) * nseg;
+    static const Shape shapes[3] = {
+        {256, 256, 1, 2, 1.70, 12.0}, {128, 128, 2, 2, 1.20, 3.7}, {64, 128, 2, 3, 0.81, 1.2}};
     TpPlan best;
     double best_us = 1e300;
     for (int s = 0; s < 3; ++s) {
-        const int64_t tm = (M + shapes[s].bm - 1) / shapes[s].bm, tn = (N + shapes[s].bn - 1) / shapes[s].bn;
+        const Shape& S = shapes[s];
+        const int64_t tm = (M + S.bm - 1) / S.bm, tn = (N + S.bn - 1) / S.bn;
+        const int64_t turns = (int64_t)((K + 64 * S.turn - 1) / (64 * S.turn)) * nseg;
         for (int sp = 1; sp <= (may_split ? 64 : 1); sp *= 2) {
-            if (sp > 1 && steps / sp < 4) break;
-            const int64_t wgs = tm * tn * sp, slots = 256 * shapes[s].per_cu;
+            if (sp > 1 && turns / sp < 2) break;
+            const int64_t wgs = tm * tn * sp, slots = kCus * S.per_cu;
             const int64_t rounds = (wgs + slots - 1) / slots;
-            double us = (double)rounds * ((double)((steps + sp - 1) / sp) + 3) * shapes[s].step;
+            double us = (double)rounds * ((double)((turns + sp - 1) / sp * S.turn) * S.step + S.tile);
             if (sp > 1) us += 4.0 + 8.0 * sp * (double)M * N / 5e6;
             if (us < best_us) {
                 best_us = us;
                 best.shape = s;
-                best.bm = shapes[s].bm;
-                best.bn = shapes[s].bn;
+                best.bm = S.bm;
+                best.bn = S.bn;
                 best.tiles_m = (int)tm;
                 best.tiles_n = (int)tn;
                 best.splits = sp;
@@ -94,8 +107,12 @@ hipError_t launch_shape(TpKind kind, const TpArgs& P, bool part, hipStream_t st)
     const int all = P.tiles_m * P.tiles_n * P.splits, most = kCus * S::PER_CU;
     const dim3 grid((unsigned)(all < most ? all : most)), blk(S::NT);
     switch (kind) {
-        case TPK_LOGIT_STATS: hipLaunchKernelGGL((tile_product_kernel<S, true, true, TP_STATS>), grid, blk, 0, st, P); break;
-        case TPK_LOGIT_GRAD: hipLaunchKernelGGL((tile_product_kernel<S, true, true, TP_GRAD>), grid, blk, 0, st, P); break;
+        case TPK_LOGIT_STATS:
+            hipLaunchKernelGGL((tile_product_kernel<S, true, true, TP_STATS>), grid, blk, 0, st, P);
+            break;
+        case TPK_LOGIT_GRAD:
+            hipLaunchKernelGGL((tile_product_kernel<S, true, true, TP_GRAD>), grid, blk, 0, st, P);
+            break;
         case TPK_STATES:
             if (part) hipLaunchKernelGGL((tile_product_kernel<S, true, false, TP_PART>), grid, blk, 0, st, P);
             else hipLaunchKernelGGL((tile_product_kernel<S, true, false, TP_STORE>), grid, blk, 0, st, P);

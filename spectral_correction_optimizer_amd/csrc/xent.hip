@@ -32,35 +32,14 @@ namespace {
 constexpr int64_t kAlign = 256;
 int64_t up(int64_t n, int64_t a) { return (n + a - 1) / a * a; }
 
-struct XentScalars {
-    float share;  // 1 / max(count, 1)
-    float count;
-};
 }  // namespace
-
-// count of the tokens with a target, and its inverse
-__global__ __launch_bounds__(1024) void xent_count_kernel(const int64_t* __restrict__ targets, int64_t T, int64_t V,
-                                                          XentScalars* out) {
-    __shared__ int part[16];
-    int n = 0;
-    for (int64_t t = threadIdx.x; t < T; t += 1024) n += tp_target(targets, V, t) >= 0;
-    for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o);
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = n;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        n = 0;
-        for (int w = 0; w < 16; ++w) n += part[w];
-        gst(&out->count, (float)n);
-        gst(&out->share, 1.0f / (float)(n > 0 ? n : 1));
-    }
-}
 
 // 64 tokens a workgroup, one a lane, the tiles dealt to 16 wavefronts: a row's log-sum-exp from
 // its tiles' references and sums [tile][T], and its loss.  pow2: the references are powers of
 // two.  A row of -infinity only has no finite log-sum-exp; like a row with NaN or +infinity
 // it gives NaN.
-__global__ __launch_bounds__(1024) void xent_lse_kernel(const float* __restrict__ smax, const float* __restrict__ ssum,
-                                                        int tiles, int pow2, const float* __restrict__ target_logit,
+__global__ __launch_bounds__(1024) void xent_lse_kernel(const float* __restrict__ smax,
+                                                        const float* __restrict__ ssum, int tiles, int pow2, const float* __restrict__ target_logit,
                                                         const int64_t* __restrict__ targets, int64_t T, int64_t V,
                                                         float* __restrict__ lse, float* __restrict__ loss) {
     __shared__ float red[16][64];
@@ -99,8 +78,8 @@ __global__ __launch_bounds__(1024) void xent_lse_kernel(const float* __restrict_
 // d from what the logits product kept: bfloat16 exponentials (in place) or float32 logits
 // (into three planes).  `chunks` workgroups a row; a thread takes 8 columns at a time.
 template <bool EXP>
-__global__ __launch_bounds__(256) void xent_dlogits_kernel(const float* __restrict__ logits, uint16_t* P, int64_t plane,
-                                                           int64_t ldp, int N, int bn, int64_t chunk, int chunks,
+__global__ __launch_bounds__(256) void xent_dlogits_kernel(const float* __restrict__ logits, uint16_t* P,
+                                                           int64_t plane, int64_t ldp, int N, int bn, int64_t chunk, int chunks,
                                                            const float* __restrict__ smax, int64_t T,
                                                            const float* __restrict__ lse,
                                                            const float* __restrict__ target_logit,
@@ -146,14 +125,24 @@ __global__ __launch_bounds__(256) void xent_dlogits_kernel(const float* __restri
     }
 }
 
-// the mean loss, summed in a fixed order
-__global__ __launch_bounds__(1024) void xent_mean_kernel(const float* __restrict__ loss, int64_t T,
-                                                         const XentScalars* sc, float* mean) {
+// the mean loss over the counted tokens, summed in a fixed order, and one token's share of it
+__global__ __launch_bounds__(1024) void xent_mean_kernel(const float* __restrict__ loss,
+                                                         const int64_t* __restrict__ targets, int64_t T, int64_t V,
+                                                         float* share, float* mean) {
     __shared__ double red[16];
-    double s = 0.0;
-    for (int64_t t = threadIdx.x; t < T; t += 1024) s += (double)gld(loss + t);
+    double s = 0.0, n = 0.0;
+#pragma unroll 4
+    for (int64_t t = threadIdx.x; t < T; t += 1024) {
+        s += (double)gld(loss + t);
+        n += tp_target(targets, V, t) >= 0 ? 1.0 : 0.0;
+    }
     s = block_sum_f64(s, red);
-    if (threadIdx.x == 0) gst(mean, (float)(s * (double)gld(&sc->share)));
+    n = block_sum_f64(n, red);
+    if (threadIdx.x == 0) {
+        n = n > 0.0 ? n : 1.0;
+        gst(share, (float)(1.0 / n));
+        gst(mean, (float)(s / n));
+    }
 }
 
 XentPlan xent_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit) {
@@ -191,7 +180,7 @@ XentPlan xent_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit) {
         return at;
     };
     const int np = bf16 ? 1 : 3;
-    p.o_scalars = take(sizeof(XentScalars));
+    p.o_share = take(4);
     p.o_h = take(2 * np * T * p.Hh);
     p.o_w = p.planes ? take(2 * np * V * p.Hp) : 0;
     p.o_s = !bf16 && p.keep ? take(4 * T * p.ldp) : 0;
@@ -216,7 +205,7 @@ hipError_t launch_xent(const XentPlan& p, const void* h, const void* W, const in
     char* ws = (char*)workspace;
     const int64_t T = p.T, V = p.V, H = p.H, Hp = p.Hp, Hh = p.Hh;
     const int np = p.bf16 ? 1 : 3;
-    XentScalars* sc = (XentScalars*)(ws + p.o_scalars);
+    float* share = (float*)(ws + p.o_share);
     uint16_t* P = (uint16_t*)(ws + p.o_p);
     float* S = (float*)(ws + p.o_s);
     float *tl = (float*)(ws + p.o_tl), *lse = (float*)(ws + p.o_lse);
@@ -230,8 +219,6 @@ hipError_t launch_xent(const XentPlan& p, const void* h, const void* W, const in
 #define SC_RUN(expr) \
     if ((e = (expr)) != hipSuccess) return e
 
-    hipLaunchKernelGGL(xent_count_kernel, dim3(1), dim3(1024), 0, st, targets, T, V, sc);
-    SC_RUN(hipGetLastError());
     // h is always copied, with zeros for the tokens that are not counted: whatever they hold
     // (a NaN too) reaches no product
     uint16_t* hp = (uint16_t*)(ws + p.o_h);
@@ -283,7 +270,7 @@ hipError_t launch_xent(const XentPlan& p, const void* h, const void* W, const in
     hipLaunchKernelGGL(xent_lse_kernel, dim3((unsigned)((T + 63) / 64)), dim3(1024), 0, st, smax, ssum,
                        (int)p.stat_tiles, pow2, tl, targets, T, V, lse, loss);
     SC_RUN(hipGetLastError());
-    hipLaunchKernelGGL(xent_mean_kernel, dim3(1), dim3(1024), 0, st, loss, T, sc, mean);
+    hipLaunchKernelGGL(xent_mean_kernel, dim3(1), dim3(1024), 0, st, loss, targets, T, V, share, mean);
     SC_RUN(hipGetLastError());
 
     for (int i = 0; i < p.pieces; ++i) {
@@ -321,7 +308,7 @@ hipError_t launch_xent(const XentPlan& p, const void* h, const void* W, const in
         a.C = dh;
         a.ldc = H;
         a.c_bf16 = p.bf16;
-        a.alpha = &sc->share;
+        a.alpha = share;
         a.part = part;
         TpSum sum;
         if (p.pieces > 1) {
@@ -344,7 +331,7 @@ hipError_t launch_xent(const XentPlan& p, const void* h, const void* W, const in
         b.C = (char*)dW + v0 * H * (p.bf16 ? 2 : 4);
         b.ldc = H;
         b.c_bf16 = p.bf16;
-        b.alpha = &sc->share;
+        b.alpha = share;
         b.part = part;
         SC_RUN(launch_tile_product(TPK_WEIGHTS, i + 1 < p.pieces ? p.dw : p.dw_last, b, TpSum{}, st));
     }
