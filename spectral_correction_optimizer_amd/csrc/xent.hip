@@ -79,7 +79,8 @@ __global__ __launch_bounds__(1024) void xent_lse_kernel(const float* __restrict_
 // (into three planes).  `chunks` workgroups a row; a thread takes 8 columns at a time.
 template <bool EXP>
 __global__ __launch_bounds__(256) void xent_dlogits_kernel(const float* __restrict__ logits, uint16_t* P,
-                                                           int64_t plane, int64_t ldp, int N, int bn, int64_t chunk, int chunks,
+                                                           int64_t plane, int64_t ldp, int N, int bn,
+                                                           int64_t chunk, int chunks,
                                                            const float* __restrict__ smax, int64_t T,
                                                            const float* __restrict__ lse,
                                                            const float* __restrict__ target_logit,
@@ -89,7 +90,8 @@ __global__ __launch_bounds__(256) void xent_dlogits_kernel(const float* __restri
     const float ls = gld(lse + t);
     const float ls2 = ls * kLog2e;
     const float at_target = tgt >= 0 ? expf(gld(target_logit + t) - ls) - 1.0f : 0.0f;
-    const int64_t from = (int64_t)(blockIdx.x % chunks) * chunk, to = from + chunk < ldp ? from + chunk : ldp;
+    const int64_t end = (N + 7) & ~7;  // the products read no further
+    const int64_t from = (int64_t)(blockIdx.x % chunks) * chunk, to = from + chunk < end ? from + chunk : end;
     for (int64_t c = from + 8 * threadIdx.x; c < to; c += 8 * 256) {
         uint16_t* p = P + t * ldp + c;
         float v[8];
@@ -278,8 +280,8 @@ hipError_t launch_xent(const XentPlan& p, const void* h, const void* W, const in
         const int n = (int)(V - v0 < p.piece ? V - v0 : p.piece);
         if (p.keep) {
             // enough workgroups for the chip, at least 2048 columns each
-            int64_t chunk = up((p.ldp * T + 4095) / 4096, 2048);
-            const int chunks = (int)((p.ldp + chunk - 1) / chunk);
+            const int64_t chunk = up((n * T + 4095) / 4096, 2048);
+            const int chunks = (int)((n + chunk - 1) / chunk);
             const dim3 grid((unsigned)(chunks * T));
             if (p.bf16)
                 hipLaunchKernelGGL(xent_dlogits_kernel<true>, grid, dim3(256), 0, st, nullptr, P, T * p.ldp, p.ldp, n,

@@ -525,3 +525,73 @@ def test_other_stream_and_graph_replays():
         torch.cuda.synchronize()
         for a, b in zip(want, out):
             assert torch.equal(a, b), k
+
+
+# ---- many tiles a workgroup ----------------------------------------------------------------
+
+# more output tiles than workgroups run at once, each way of storing them: whole 256 x 256 tiles and
+# cut ones (and in float32 the six plane products of each)
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("T,N,H", [(130, 4400, 4104), (200, 8192, 2304)])
+def test_act_wgrad_many_tiles(T, N, H, dtype):
+    say(f"case: act_wgrad many tiles T {T} N {N} H {H} {dtype}")
+    g = gen(18)
+    dy = randn(g, T, N, dtype=dtype)
+    kept = sco().act_pack(randn(g, T, H))
+    n = sco().act_unpack(kept, torch.float32).cpu().to(F64)
+    d64 = dy.cpu().to(F64)
+    ref, mag = (d64.t() @ n).cuda(), (d64.abs().t() @ n.abs()).cuda()
+    terms = T * (1 if dtype == torch.bfloat16 else 3) + 64
+    within("dW", sco().act_wgrad(dy, kept), ref, ref.abs() * (HALF[dtype] + U) + terms * 2 * U * mag)
+
+
+@pytest.mark.parametrize("dtype", DT)
+def test_xent_many_tiles(dtype):
+    T, V, H = 300, 70003, 72
+    say(f"case: xent many tiles T {T} V {V} H {H} {dtype}")
+    g = gen(19)
+    h, W, tgt = _xent_case(g, T, V, H, dtype)
+    tgt[5] = -1
+    tgt[6] = V - 1
+    ref, tol = _xent_ref(h, W, tgt, dtype)
+    _xent_check(sco().xent(h, W, tgt), ref, tol)
+
+
+# ---- the operators together ------------------------------------------------------------------
+
+def test_example_learns():
+    """The example's model, trained by its own loop: the loss starts at the uniform distribution's
+    and falls."""
+    from examples.training_step import Model, train
+    losses = train(steps=40)
+    assert all(math.isfinite(x) for x in losses)
+    assert abs(losses[0] - math.log(512)) < 0.5
+    assert sum(losses[-5:]) / 5 < 0.8 * losses[0]
+
+
+def test_example_gradients_against_differences():
+    """The loss falls along the negative gradients by their squared norm, to first order.  The
+    checkpoints' rounding (a 127th of a block's largest value) bounds what the gradients that
+    read them are off by."""
+    from examples.training_step import Model
+    g = gen(20)
+    m = Model(V=64, H=64, seed=3)
+    ids = torch.randint(0, 64, (400,), generator=g, device="cuda")
+    tgt = torch.randint(-1, 64, (400,), generator=g, device="cuda")
+    _, grads, dgains = m.step(ids, tgt)
+    params = m.matrices() + m.gain
+    every = grads + dgains
+    norm2 = sum((d.double() ** 2).sum() for d in every)
+    t = 1e-3 / float(norm2.sqrt())
+    losses = []
+    for sign in (1, -1):
+        for p, d in zip(params, every):
+            p.add_(sign * t * d)
+        losses.append(float(m.step(ids, tgt)[0]))
+        for p, d in zip(params, every):
+            p.sub_(sign * t * d)
+    slope = (losses[0] - losses[1]) / (2 * t)
+    # float32 losses: 2 roundings of about 40 U each over 2 t; checkpoints: half a step of 1/64 of
+    # a block's largest power of two, at most 1% of the largest value, twice
+    slack = 80 * U * losses[0] / t + 0.04 * float(norm2)
+    assert abs(slope - float(norm2)) <= slack

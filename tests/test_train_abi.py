@@ -36,6 +36,8 @@ def test_embed_grad_refusals(lib):
     n = ctypes.c_int64()
     assert lib.sc_embed_grad_workspace(4, (1 << 22) + 1, 8, ctypes.byref(n)) == SHAPE
     assert lib.sc_embed_grad_workspace(4, 8, 8, None) == INVALID
+    assert lib.sc_embed_grad_workspace(1 << 30, 8, 8, ctypes.byref(n)) == SHAPE  # 32-bit indexes
+    assert lib.sc_embed_grad_workspace((1 << 30) - 1, 8, 1, ctypes.byref(n)) == 0
     assert lib.sc_embed_grad_workspace(1000, 5000, 64, ctypes.byref(n)) == 0 and n.value > 0
     f = lib.sc_embed_grad
     assert f(0, P, P, 1000, 5000, 64, 1.0, P, P, n.value - 1, None) == INVALID
