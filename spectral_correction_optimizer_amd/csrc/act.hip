@@ -103,10 +103,10 @@ __device__ __forceinline__ float row_sum(float v, float (*red)[TPR / 64], int tu
     return v;
 }
 
-// Rows beyond the grid's are taken in turn.
+// Rows beyond the grid's are taken in turn.  h may be x or res: a row is loaded whole (a cut
+// row's last group overlaps another thread's) before row_sum, and stored after it.
 template <typename E, int ENDS, int TPR, int C>
-__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rmsnorm_kernel(const E* __restrict__ x,
-                                                                        const E* __restrict__ res,
+__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rmsnorm_kernel(const E* x, const E* res,
                                                                         const E* __restrict__ gain, float eps,
                                                                         int64_t T, int H, E* h, E* y, float* rstd,
                                                                         int8_t* q, uint8_t* e) {
@@ -180,9 +180,8 @@ template <typename E, int ENDS, int C> struct NormGradRow {
 };
 template <typename E, int ENDS, int TPR, int C>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rmsnorm_grad_kernel(
-    const E* __restrict__ dy, const E* __restrict__ gain, const float* __restrict__ rstd,
-    const int8_t* __restrict__ q, const uint8_t* __restrict__ e, const E* __restrict__ dh, int64_t T, int H, E* dx,
-    float* partial) {
+    const E* dy, const E* __restrict__ gain, const float* __restrict__ rstd, const int8_t* __restrict__ q,
+    const uint8_t* __restrict__ e, const E* dh, int64_t T, int H, E* dx, float* partial) {
     constexpr int ROWS = TPR > 256 ? 1 : 256 / TPR;
     __shared__ float red[2][TPR / 64];
     __shared__ float sums[ROWS > 1 ? TPR * 8 : 1];
@@ -231,6 +230,14 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rmsnorm_grad_kernel(
                 dg[j][i] = fmaf(a[j][i], n[j][i], dg[j][i]);
                 a[j][i] *= g[j][i];
                 dot = fmaf(a[j][i], n[j][i], dot);
+            }
+        }
+        // dx may be dy or dh: a cut row's last group overlaps another thread's, so dh has to have
+        // arrived before any thread passes the sum
+        if constexpr (ENDS == ROW_CUT) {
+            if (dh) {
+#pragma unroll
+                for (int j = 0; j < C; ++j) cur.dh[j].arrived();
             }
         }
         const float c1 = row_sum<TPR>(dot, red, turn) / (float)H;

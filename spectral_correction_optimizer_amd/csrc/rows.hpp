@@ -38,6 +38,7 @@ template <int ENDS> struct Group8<uint16_t, ENDS> {
             w = *(const SC_GLOBAL v4u_any*)(row + min(c, H - 8));
         }
     }
+    __device__ __forceinline__ void arrived() { asm volatile("" : "+v"(w) : : "memory"); }  // waits for the load
     __device__ __forceinline__ void raw(float (&v)[8]) const {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -61,6 +62,7 @@ template <int ENDS> struct Group8<float, ENDS> {
             b = *(const SC_GLOBAL v4f_any*)(p + 4);
         }
     }
+    __device__ __forceinline__ void arrived() { asm volatile("" : "+v"(a), "+v"(b) : : "memory"); }
     __device__ __forceinline__ void raw(float (&v)[8]) const {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {

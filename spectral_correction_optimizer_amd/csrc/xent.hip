@@ -31,7 +31,6 @@ namespace scopt {
 namespace {
 constexpr int64_t kAlign = 256;
 int64_t up(int64_t n, int64_t a) { return (n + a - 1) / a * a; }
-
 }  // namespace
 
 // 64 tokens a workgroup, one a lane, the tiles dealt to 16 wavefronts: a row's log-sum-exp from
@@ -39,27 +38,43 @@ int64_t up(int64_t n, int64_t a) { return (n + a - 1) / a * a; }
 // two.  A row of -infinity only has no finite log-sum-exp; like a row with NaN or +infinity
 // it gives NaN.
 __global__ __launch_bounds__(1024) void xent_lse_kernel(const float* __restrict__ smax,
-                                                        const float* __restrict__ ssum, int tiles, int pow2, const float* __restrict__ target_logit,
+                                                        const float* __restrict__ ssum, int tiles, int pow2,
+                                                        const float* __restrict__ target_logit,
                                                         const int64_t* __restrict__ targets, int64_t T, int64_t V,
                                                         float* __restrict__ lse, float* __restrict__ loss) {
     __shared__ float red[16][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t t = (int64_t)blockIdx.x * 64 + lane, at = t < T ? t : T - 1;
     const float none = -__builtin_huge_valf();
-    float m = none;
-#pragma unroll 8
-    for (int i = wave; i < tiles; i += 16) m = fmaxf(m, gld(smax + i * T + at));
+    // a difference of references as a factor; a tile of -infinity has sum 0 (or NaN)
+    auto scaled = [&](float s, float r, float to) {
+        return r == none ? s : s * (pow2 ? exp2f(r - to) : expf(r - to));
+    };
+    // sixteen tiles' values in flight, joined to the running reference and sum
+    float m = none, z = 0.0f;
+    constexpr int U = 16;
+    for (int i0 = wave; i0 < tiles; i0 += 16 * U) {
+        float r[U], s[U], top = m;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t i = i0 + 16 * u < tiles ? i0 + 16 * u : tiles - 1;
+            r[u] = gld(smax + i * T + at);
+            s[u] = gld(ssum + i * T + at);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) top = i0 + 16 * u < tiles ? fmaxf(top, r[u]) : top;
+        z = scaled(z, m, top);
+        m = top;
+#pragma unroll
+        for (int u = 0; u < U; ++u) z += i0 + 16 * u < tiles ? scaled(s[u], r[u], m) : 0.0f;
+    }
     red[wave][lane] = m;
     __syncthreads();
+    float top = none;
 #pragma unroll
-    for (int w = 0; w < 16; ++w) m = fmaxf(m, red[w][lane]);
-    float z = 0.0f;
-#pragma unroll 8
-    for (int i = wave; i < tiles; i += 16) {
-        const float r = gld(smax + i * T + at), s = gld(ssum + i * T + at);
-        // a tile of -infinity has sum 0 (or NaN)
-        z += r == none ? s : s * (pow2 ? exp2f(r - m) : expf(r - m));
-    }
+    for (int w = 0; w < 16; ++w) top = fmaxf(top, red[w][lane]);
+    z = scaled(z, m, top);
+    m = top;
     __syncthreads();
     red[wave][lane] = z;
     __syncthreads();

@@ -304,6 +304,34 @@ def test_rmsnorm_grad_against_differences():
     within("dx", dx, ref, 90 * U * mag)
 
 
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("T,H", [(40, 1000), (700, 4100), (300, 2049), (9, 8191), (5, 9001), (64, 7)])
+def test_norm_in_place(T, H, dtype):
+    """The C entries allow h = x, h = residual, dx = dy and dx = dh, also for rows that end inside a
+    group of eight."""
+    say(f"case: in place T {T} H {H} {dtype}")
+    m, g = sco(), gen(21)
+    lib, dt, st = m.load_library(), m._DT[dtype], torch.cuda.current_stream().cuda_stream
+    x, r, dy, dh = (randn(g, T, H, dtype=dtype) for _ in range(4))
+    gain = randn(g, H, dtype=dtype)
+    want = m.rmsnorm(x, gain, residual=r)
+    for i in range(2):
+        a = [x.clone(), r.clone()]
+        y, rstd = torch.empty_like(x), torch.empty(T, device="cuda")
+        assert lib.sc_rmsnorm(dt, a[0].data_ptr(), a[1].data_ptr(), gain.data_ptr(), 1e-5, T, H, a[i].data_ptr(),
+                              y.data_ptr(), rstd.data_ptr(), None, None, st) == 0
+        assert torch.equal(a[i], want.h) and torch.equal(y, want.y) and torch.equal(rstd, want.rstd)
+    dx, dgain = m.rmsnorm_grad(dy, gain, want.rstd, want.kept, dh=dh)
+    n = m._workspace_bytes("sc_rmsnorm_grad_workspace", T, H)
+    for i in range(2):
+        a = [dy.clone(), dh.clone()]
+        dg, ws = torch.empty(H, device="cuda"), torch.empty(n, dtype=torch.uint8, device="cuda")
+        assert lib.sc_rmsnorm_grad(dt, a[0].data_ptr(), gain.data_ptr(), want.rstd.data_ptr(), want.kept.q.data_ptr(),
+                                   want.kept.e.data_ptr(), a[1].data_ptr(), T, H, a[i].data_ptr(), dg.data_ptr(),
+                                   ws.data_ptr(), n, st) == 0
+        assert torch.equal(a[i], dx) and torch.equal(dg, dgain)
+
+
 # ---- weight gradient from the checkpoint -------------------------------------------------
 
 @pytest.mark.parametrize("dtype", DT)
