@@ -8,9 +8,8 @@
 //   weight gradient: dW[o][i] = g[i] sum over tokens of dy[t][o] n[t][i]
 //
 // The norm, its gradient and the conversions stream each element once and are bound by HBM.
-// A wavefront owns a row of up to 2048 elements, a workgroup a longer one; the row stays in
-// registers between the sum and the outputs.  Sums are float32 (the norm's over at most
-// 16384 squares, spread over 64 or 256 lanes).
+// A wavefront owns a row of up to 1024 elements, a workgroup a longer one; the row stays in
+// registers between the sum and the outputs.  The norm's sums are 64-bit, its gradient's float32.
 #include <cmath>
 
 #include "rows.hpp"
@@ -21,7 +20,6 @@ namespace scopt {
 
 namespace {
 int64_t up(int64_t n, int64_t a) { return (n + a - 1) / a * a; }
-
 }  // namespace
 
 // A thread converts kGroups groups of 8 elements.  The four threads of a block of 32 are
@@ -87,22 +85,26 @@ __global__ __launch_bounds__(256) void act_unpack_kernel(const int8_t* __restric
     }
 }
 
-// Sum over the TPR threads of a row: `red` holds a float per wave, twice, and is used in turn
+// Sum over the TPR threads of a row: `red` holds a value per wave, twice, and is used in turn
 // (`turn`), so that one barrier a row is enough.
-template <int TPR>
-__device__ __forceinline__ float row_sum(float v, float (*red)[TPR / 64], int turn) {
+template <int TPR, typename F>
+__device__ __forceinline__ F row_sum(F v, F (*red)[TPR / 64], int turn) {
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
     if constexpr (TPR > 64) {
         if ((threadIdx.x & 63) == 0) red[turn][threadIdx.x >> 6] = v;
         __syncthreads();
-        v = 0.0f;
+        v = F(0);
 #pragma unroll
         for (int w = 0; w < TPR / 64; ++w) v += red[turn][w];
     }
     return v;
 }
 
+// The rows are normalised in 64 bits (the vector unit's rate for them is float32's, and HBM stays
+// the bound): a value next to the border of two of the checkpoint's steps then falls to the
+// side that it belongs to, which float32's roundings decided before, a few in a million.
+//
 // Rows beyond the grid's are taken in turn.  h may be x or res: a row is loaded whole (a cut
 // row's last group overlaps another thread's) before row_sum, and stored after it.
 template <typename E, int ENDS, int TPR, int C>
@@ -111,7 +113,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rmsnorm_kernel(const E*
                                                                         int64_t T, int H, E* h, E* y, float* rstd,
                                                                         int8_t* q, uint8_t* e) {
     constexpr int ROWS = TPR > 256 ? 1 : 256 / TPR;
-    __shared__ float red[2][TPR / 64];
+    __shared__ double red[2][TPR / 64];
     const int in = threadIdx.x % TPR;
     const int nb = (H + kActBlock - 1) / kActBlock;
     int turn = 0;
@@ -126,41 +128,44 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rmsnorm_kernel(const E*
         }
 #pragma unroll
         for (int j = 0; j < C; ++j) gw[j].load(gain, (j * TPR + in) * 8, H);
-        float v[C][8], ss = 0.0f;
+        auto sums = [&](int j, double (&v)[8]) __attribute__((always_inline)) {
+            float a[8], r[8];
+            value8(xw[j], (j * TPR + in) * 8, H, a);
+            if (res) value8(rw[j], (j * TPR + in) * 8, H, r);
 #pragma unroll
-        for (int j = 0; j < C; ++j) value8(xw[j], (j * TPR + in) * 8, H, v[j]);
-        if (res) {
+            for (int i = 0; i < 8; ++i) v[i] = res ? (double)a[i] + (double)r[i] : (double)a[i];
+        };
+        double ss = 0.0;
 #pragma unroll
-            for (int j = 0; j < C; ++j) {
-                float r[8];
-                value8(rw[j], (j * TPR + in) * 8, H, r);
+        for (int j = 0; j < C; ++j) {
+            double v[8];
+            sums(j, v);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[j][i] += r[i];
-            }
+            for (int i = 0; i < 8; ++i) ss = fma(v[i], v[i], ss);
         }
-#pragma unroll
-        for (int j = 0; j < C; ++j)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(v[j][i], v[j][i], ss);
         ss = row_sum<TPR>(ss, red, turn);
-        const float rs = 1.0f / sqrtf(ss / (float)H + eps);
-        if (in == 0) gst(rstd + t, rs);
+        const double rs = 1.0 / sqrt(ss / (double)H + (double)eps);
+        if (in == 0) gst(rstd + t, (float)rs);
 #pragma unroll
         for (int j = 0; j < C; ++j) {
             const int c = (j * TPR + in) * 8, left = H - c;
-            if (h && left > 0) store8(h + t * H + c, left, v[j]);
-            float g[8], o[8];
+            double v[8];
+            float f[8], g[8];
+            sums(j, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = (float)v[i];
+            if (h && left > 0) store8(h + t * H + c, left, f);
             value8(gw[j], c, H, g);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                v[j][i] *= rs;  // the norm of the float32 sum, not of the rounded h
-                o[i] = v[j][i] * g[i];
+                v[i] *= rs;  // the norm of the sum, not of the rounded h
+                f[i] = (float)v[i] * g[i];
             }
-            if (left > 0) store8(y + t * H + c, left, o);
+            if (left > 0) store8(y + t * H + c, left, f);
             if (q) {
                 int8_t k[8];
                 uint8_t ex;
-                act_encode8(v[j], k, ex);
+                act_encode8(v, k, ex);
                 if (left > 0) {
                     store_q8(q + t * H + c, left, k);
                     if ((in & 3) == 0) gst(e + t * nb + c / kActBlock, ex);
@@ -338,7 +343,7 @@ hipError_t launch_act_unpack(bool bf16, const int8_t* q, const uint8_t* e, int64
     return unpack_rows(bf16, q, e, T, H, H, x, st);
 }
 
-// Threads and groups of 8 a row: a wave up to 2048 elements, a workgroup beyond.
+// Threads and groups of 8 a row: a wave up to 1024 elements, a workgroup beyond.
 template <typename E, int ENDS, int TPR, int C, typename... A>
 static void norm_rows(int64_t T, hipStream_t st, A... args) {
     constexpr int64_t rows = TPR > 256 ? 1 : 256 / TPR;
@@ -351,7 +356,7 @@ static void norm_ends(int64_t T, int H, hipStream_t st, A... args) {
     if (ENDS == ROW_SHORT || H <= 512) norm_rows<E, ENDS, 64, 1>(T, st, args...);
     else if constexpr (ENDS != ROW_SHORT) {
         if (H <= 1024) norm_rows<E, ENDS, 64, 2>(T, st, args...);
-        else if (H <= 2048) norm_rows<E, ENDS, 64, 4>(T, st, args...);
+        else if (H <= 2048) norm_rows<E, ENDS, 256, 1>(T, st, args...);
         else if (H <= 4096) norm_rows<E, ENDS, 256, 2>(T, st, args...);
         else if (H <= 6144) norm_rows<E, ENDS, 256, 3>(T, st, args...);
         else if (H <= 8192) norm_rows<E, ENDS, 256, 4>(T, st, args...);

@@ -172,6 +172,29 @@ __device__ __forceinline__ void act_encode8(const float (&v)[8], int8_t (&q)[8],
         q[i] = finite ? (int8_t)fminf(fmaxf(r, -127.0f), 127.0f) : (int8_t)0;
     }
 }
+// The same for values in 64 bits: the largest magnitude's exponent is that of its high words.
+__device__ __forceinline__ void act_encode8(const double (&v)[8], int8_t (&q)[8], uint8_t& e) {
+    uint32_t big = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t a = (uint32_t)(__double_as_longlong(v[i]) >> 32) & 0x7fffffffu;
+        big = a > big ? a : big;
+    }
+    uint32_t o = __shfl_xor(big, 1);
+    big = o > big ? o : big;
+    o = __shfl_xor(big, 2);
+    big = o > big ? o : big;
+    int E = (int)(big >> 20) - 1023;
+    const bool finite = E <= 127;
+    E = E > kActMinExp ? E : kActMinExp;
+    e = finite ? (uint8_t)(E + 127) : kActNonFinite;
+    const double inv = __longlong_as_double((long long)(6 - E + 1023) << 52);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const double r = rint(v[i] * inv);
+        q[i] = finite ? (int8_t)fminf(fmaxf((float)r, -127.0f), 127.0f) : (int8_t)0;
+    }
+}
 __device__ __forceinline__ void store_q8(int8_t* p, int left, const int8_t (&q)[8]) {
     if (left >= 8) {
         v2u_any w;
