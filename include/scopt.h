@@ -410,7 +410,7 @@ int sc_embed(sc_dtype dtype, const void* table, const int64_t* ids, int64_t T, i
              void* out, void* stream);
 
 /* dW[v] = scale * sum over t with ids[t] = v of dy[t], in float32, in an order that ids fix;
- * dW [V][H] is written whole.  T < 2^30, V <= 2^22. */
+ * dW [V][H] is written whole.  T < 2^30, V <= 2^22, (T / 32 + V / 8) * ceil(H / 512) < 2^26. */
 int sc_embed_grad_workspace(int64_t T, int64_t V, int H, int64_t* bytes);
 int sc_embed_grad(sc_dtype dtype, const void* dy, const int64_t* ids, int64_t T, int64_t V, int H, float scale,
                   void* dW, void* workspace, int64_t workspace_bytes, void* stream);

@@ -32,6 +32,7 @@ constexpr int kBins = 512;     // most bins; also the scatter's workgroup size
 constexpr int kBlocks = 64;    // most token blocks
 constexpr int kMaxRun = 32;    // most sorted tokens of a stretch
 constexpr int kSlab = 512;     // columns of a wavefront
+constexpr int64_t kMaxCross = 1 << 20;  // workgroups of embed_cross: a launch of 2^32 threads wraps, with no error
 
 int64_t up(int64_t n, int64_t a) { return (n + a - 1) / a * a; }
 
@@ -309,46 +310,53 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(const E* __restrict__ dy
     }
 }
 
-// The row, if any, that crosses into stretch k = blockIdx.x / slabs + 1 from the stretch where
-// it begins: the sum of its partials, a quarter of them a wavefront.
+// The row, if any, that crosses into stretch k + 1 from stretch k, where it begins: the sum of its
+// partials, a quarter of them a wavefront.  Crossings and slabs beyond the grid's are taken in turn;
+// which of them a workgroup skips is the same for all its threads.
 template <typename E, int ENDS>
 __global__ __launch_bounds__(256) void embed_cross_kernel(int H, int64_t V, float scale, int len,
                                                           const int32_t* __restrict__ row_start,
                                                           const int32_t* __restrict__ sorted_id,
-                                                          const float* __restrict__ partial, int slabs, E* dW) {
+                                                          const float* __restrict__ partial, int64_t items, int slabs,
+                                                          E* dW) {
     __shared__ float red[3][kSlab];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int k = (int)(blockIdx.x / slabs) + 1;
-    const int c = (int)(blockIdx.x % slabs) * kSlab + lane * 8, left = H - c;
-    if (k * len >= gld(row_start + V)) return;
-    const int64_t id = gld(sorted_id + k * len);
-    const int s = gld(row_start + id), e = gld(row_start + id + 1);
-    if (s >= k * len || s < (k - 1) * len) return;
-    const int last = (e - 1) / len, n = last - k + 2;  // partials: the first stretch's second one, then first ones
-    const int per = (n + 3) / 4, p0 = min(n, wave * per), p1 = min(n, p0 + per);
-    float acc[8];
+    const int total = gld(row_start + V);
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const int k = (int)(item / slabs) + 1;
+        const int c = (int)(item % slabs) * kSlab + lane * 8, left = H - c;
+        if (k * len >= total) break;
+        const int64_t id = gld(sorted_id + k * len);
+        const int s = gld(row_start + id), e = gld(row_start + id + 1);
+        if (s >= k * len || s < (k - 1) * len) continue;
+        const int last = (e - 1) / len, n = last - k + 2;  // partials: the first stretch's second one, then first ones
+        const int per = (n + 3) / 4, p0 = min(n, wave * per), p1 = min(n, p0 + per);
+        float acc[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+        for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
 #pragma unroll 4
-    for (int p = p0; p < p1; ++p) {
-        float v[8];
-        load8<ENDS>(partial + (2ll * (k - 1 + p) + (p == 0 ? 1 : 0)) * H, c, H, v);
+        for (int p = p0; p < p1; ++p) {
+            float v[8];
+            load8<ENDS>(partial + (2ll * (k - 1 + p) + (p == 0 ? 1 : 0)) * H, c, H, v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] += v[i];
+            for (int i = 0; i < 8; ++i) acc[i] += v[i];
+        }
+        if (wave > 0) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) red[wave - 1][i * 64 + lane] = acc[i];
+        }
+        __syncthreads();
+        if (wave == 0 && left > 0) {
+#pragma unroll
+            for (int w = 0; w < 3; ++w)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[i] += red[w][i * 64 + lane];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[i] *= scale;
+            store8(dW + id * H + c, left, acc);
+        }
+        __syncthreads();  // red is read
     }
-    if (wave > 0) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) red[wave - 1][i * 64 + lane] = acc[i];
-    }
-    __syncthreads();
-    if (wave > 0 || left <= 0) return;
-#pragma unroll
-    for (int w = 0; w < 3; ++w)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] += red[w][i * 64 + lane];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] *= scale;
-    store8(dW + id * H + c, left, acc);
 }
 
 hipError_t launch_embed(bool bf16, const void* table, const int64_t* ids, int64_t T, int64_t V, int H, float scale,
@@ -379,6 +387,8 @@ EmbedGradPlan embed_grad_plan(int64_t T, int64_t V, int64_t H) {
     p.len = kMaxRun;
     while (p.len > 8 && T / p.len * slabs < 4096) p.len /= 2;
     p.runs = (T + p.len - 1) / p.len;
+    p.slabs = slabs;
+    p.tasks = (p.runs + (V + 7) / 8) * slabs;
     int64_t o = 0;
     auto take = [&](int64_t bytes) {
         const int64_t at = o;
@@ -418,15 +428,15 @@ hipError_t launch_embed_grad(const EmbedGradPlan& p, bool bf16, const void* dy, 
     hipLaunchKernelGGL(embed_bin_sort_kernel, dim3((unsigned)p.bins), dim3(64 * waves),
                        (waves * sizeof(int32_t)) << p.shift, st, bin, p.shift, p.V, key, pos, start, sid, spos);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    const int H = (int)p.H, slabs = (H + kSlab - 1) / kSlab;
-    const int64_t sums = p.runs * slabs, tasks = sums + (p.V + 7) / 8 * slabs;
+    const int H = (int)p.H, slabs = (int)p.slabs;
+    const int64_t sums = p.runs * slabs, cross = (p.runs - 1) * slabs;
 #define SC_EMBED(E_, ENDS_)                                                                                        \
-    hipLaunchKernelGGL((embed_sum_kernel<E_, ENDS_>), dim3((unsigned)((tasks + 3) / 4)), dim3(256), 0, st,         \
-                       (const E_*)dy, H, p.V, scale, p.len, start, sid, spos, sums, tasks, slabs, (E_*)dW, part);  \
+    hipLaunchKernelGGL((embed_sum_kernel<E_, ENDS_>), dim3((unsigned)((p.tasks + 3) / 4)), dim3(256), 0, st,       \
+                       (const E_*)dy, H, p.V, scale, p.len, start, sid, spos, sums, p.tasks, slabs, (E_*)dW, part); \
     if ((e = hipGetLastError()) != hipSuccess) return e;                                                           \
-    if (p.runs > 1)                                                                                                \
-        hipLaunchKernelGGL((embed_cross_kernel<E_, ENDS_>), dim3((unsigned)((p.runs - 1) * slabs)), dim3(256), 0,  \
-                           st, H, p.V, scale, p.len, start, sid, part, slabs, (E_*)dW);
+    if (cross > 0)                                                                                                 \
+        hipLaunchKernelGGL((embed_cross_kernel<E_, ENDS_>), dim3((unsigned)(cross < kMaxCross ? cross : kMaxCross)), \
+                           dim3(256), 0, st, H, p.V, scale, p.len, start, sid, part, cross, slabs, (E_*)dW);
     SC_BY_ENDS(bf16, p.H, SC_EMBED)
 #undef SC_EMBED
     return hipGetLastError();

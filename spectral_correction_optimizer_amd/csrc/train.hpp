@@ -136,6 +136,8 @@ struct EmbedGradPlan {
     int64_t per_block, blocks;  // tokens of a block, blocks
     int len;                    // sorted tokens of a stretch
     int64_t runs;               // stretches
+    int64_t slabs;              // of 512 columns
+    int64_t tasks;              // wavefronts of embed_sum: stretches and eights of table rows, times slabs
     int64_t o_counts, o_bin, o_key, o_pos, o_id, o_spos, o_start, o_part, bytes;
 };
 EmbedGradPlan embed_grad_plan(int64_t T, int64_t V, int64_t H);

@@ -26,6 +26,7 @@ namespace {
 constexpr int64_t kMaxTokens = (int64_t)1 << 31;  // embedding gradient: half of it, its indexes are 32-bit
 constexpr int64_t kMaxVocab = (int64_t)1 << 22;
 constexpr int kMaxEmbedH = 1 << 24;
+constexpr int64_t kMaxEmbedTasks = ((int64_t)1 << 26) - 4;  // of 64 threads: a launch has fewer than 2^32
 constexpr int kNormMaxH = 16384;
 constexpr int64_t kMaxProduct = (int64_t)1 << 21;  // sizes of a product's operands
 constexpr int64_t kXentLimit = (int64_t)4 << 30;
@@ -59,7 +60,8 @@ int check_embed(int64_t T, int64_t V, int H) {
 }
 int check_embed_grad(int64_t T, int64_t V, int H) {
     SC_TRY(check_size("T", T, 0, kMaxTokens / 2 - 1));
-    return check_embed(T, V, H);
+    SC_TRY(check_embed(T, V, H));
+    return check_size("(T / 32 + V / 8) * ceil(H / 512)", embed_grad_plan(T, V, H).tasks, 0, kMaxEmbedTasks);
 }
 int check_rows(int64_t T, int H, int maxH) {
     SC_TRY(check_size("T", T, 0, kMaxTokens - 1));
