@@ -177,7 +177,7 @@ __device__ __forceinline__ void tp_store(void* base, int bf16, int64_t at, const
         }
     }
 }
-// Bfloat16 pairs of one row of NI blocks of 16 columns: in, lane group g = lane / 16 holds
+// Pairs of 16-bit values of one row of NI blocks of 16 columns: in, lane group g = lane / 16 holds
 // columns 4 g .. 4 g + 3 of every block; out, 4 NI consecutive columns, and the first of them.
 // (Rows of 16 lanes change places between registers; the stores then write whole 16 bytes,
 // and with NI = 4 a row's 128 bytes are four lanes'.)
@@ -238,8 +238,22 @@ constexpr float kLog2e = 1.44269504088896340736f;
 // that its exponentials are 0 and not NaN.
 __device__ __forceinline__ float tp_reference(float mx, bool pow2) {
     if (mx == -__builtin_huge_valf()) return 0.0f;
-    return pow2 ? ceilf(mx * kLog2e) : mx;
+    if (!pow2) return mx;
+    float ref = ceilf(mx * kLog2e);
+    // the product may have been rounded down to a whole number: no exponential is above 1
+    if (fmaf(mx, kLog2e, -ref) > 0.0f) ref += fmaxf(1.0f, fabsf(ref) * 0x1p-23f);
+    return ref;
 }
+// Two exponentials in [0, 1] as 16 bits each, the first one low: float32's bits without the sign
+// and the upper bit of the exponent, which are 0 below 2, and without the last 14, rounded to
+// nearest.  Nine bits of fraction are kept: half a step is 2^-10 of the value, where
+// bfloat16's would be 2^-8.
+__device__ __forceinline__ uint32_t tp_pack_unit(float a, float b) {
+    return __builtin_amdgcn_perm((__float_as_uint(b) << 2) + 0x8000u, (__float_as_uint(a) << 2) + 0x8000u,
+                                 0x07060302u);
+}
+__device__ __forceinline__ float tp_unit_lo(uint32_t w) { return __uint_as_float((w & 0xffffu) << 14); }
+__device__ __forceinline__ float tp_unit_hi(uint32_t w) { return __uint_as_float(w >> 16 << 14); }
 
 // What becomes of a tile's sums.
 enum TpEpi {
@@ -569,8 +583,8 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
                             e[r] = __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], kLog2e, -ref));
                             z += e[r];
                         }
-                        d[j][0] = pack_bf16x2(e[0], e[1]);
-                        d[j][1] = pack_bf16x2(e[2], e[3]);
+                        d[j][0] = tp_pack_unit(e[0], e[1]);
+                        d[j][1] = tp_pack_unit(e[2], e[3]);
                     }
                     uint16_t* p = (uint16_t*)P.P + (int64_t)m * P.ldp;
                     const int c = tp_gather_row<NI>(d);

@@ -10,9 +10,9 @@ namespace scopt {
 // What TP_STATS keeps of a piece's logits.
 enum TpKeep {
     TP_KEEP_NONE = 0,   // nothing
-    TP_KEEP_EXP = 1,    // 2^(s log2(e) - ref) in bfloat16, ref the tile's row maximum in
-                        // powers of two, rounded up: a later change of reference by a power
-                        // of two is exact
+    TP_KEEP_EXP = 1,    // 2^(s log2(e) - ref) in 16 bits (tp_pack_unit), ref the tile's row
+                        // maximum in powers of two, rounded up: a later change of reference
+                        // by a power of two is exact
     TP_KEEP_LOGIT = 2,  // the logits in float32
 };
 

@@ -12,7 +12,7 @@
 // (3 products of 2 T V H operations), reading W and writing dW at small T.  The vocabulary
 // goes by in pieces:
 //   - If one piece (the whole vocabulary) fits the limit, the logits product leaves
-//     exponentials relative to each tile's row maximum (bfloat16; float32 operands: the
+//     exponentials relative to each tile's row maximum (16 bits; float32 operands: the
 //     logits in float32), xent_dlogits_kernel turns them into d once every row's sum is
 //     known, and the two gradient products read d: three products.
 //   - Otherwise a first pass over the pieces takes only the row sums, and a second one
@@ -20,9 +20,12 @@
 //     piece only.
 // 8192 tokens, 131072 x 2048 in bfloat16: logits 3.8 ms (1150 TFLOP/s), d 0.85 ms (5.1 TB/s), dh
 // 3.2 ms (1350), dW 3.6 ms (1210).
-// d is kept without the factor 1 / count, which the gradients' stores apply.  In bfloat16 an
-// entry of d is off by at most half a step of its own value (2^-9 of exp(s - lse) when kept
-// between the passes, then 2^-9 of the result); the target's entry is formed from the float32
+// d is kept without the factor 1 / count, which the gradients' stores apply.  The matrix cores take
+// d in bfloat16, half a step of its own value off (2^-8): two planes would double the gradient
+// products.  An exponential kept between the passes adds 2^-10 (tp_pack_unit).  Errors of dW against 64
+// bits at 64 tokens, 32000 x 2048, its rows' norm 1: 0.0019 in the rows of targets, 0.0024 in the
+// others, where exponentials kept in bfloat16 made it 0.0029; the rounding of dW alone is 0.0017.  The
+// exponentials cost the logits product 0.3% more.  The target's entry is formed from the float32
 // logit, as there the subtraction cancels.  In float32 d is split exactly into three planes.
 #include <cmath>
 
@@ -92,7 +95,7 @@ __global__ __launch_bounds__(1024) void xent_lse_kernel(const float* __restrict_
     gst(loss + t, counted ? (base - gld(target_logit + t)) + logz : 0.0f);
 }
 
-// d from what the logits product kept: bfloat16 exponentials (in place) or float32 logits
+// d from what the logits product kept: exponentials in 16 bits (in place) or float32 logits
 // (into three planes).  `chunks` workgroups a row; a thread takes 8 columns at a time.
 template <bool EXP>
 __global__ __launch_bounds__(256) void xent_dlogits_kernel(const float* __restrict__ logits, uint16_t* P,
@@ -117,8 +120,8 @@ __global__ __launch_bounds__(256) void xent_dlogits_kernel(const float* __restri
             const float f = __builtin_amdgcn_exp2f(gld(smax + (int64_t)(c / bn) * T + t) - ls2);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                v[2 * i] = bf16_lo(w[i]) * f;
-                v[2 * i + 1] = bf16_hi(w[i]) * f;
+                v[2 * i] = tp_unit_lo(w[i]) * f;
+                v[2 * i + 1] = tp_unit_hi(w[i]) * f;
             }
         } else {
             const v4f a = gld4(logits + t * ldp + c), b = gld4(logits + t * ldp + c + 4);

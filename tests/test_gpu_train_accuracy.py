@@ -1,0 +1,88 @@
+"""GPU tests of how exact the training-step operators are: what is rounded to fewer bits, how often,
+and which values survive.
+
+U = 2^-24 is half a step of float32, H16 = 2^-8 of bfloat16, relative to the value."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests.gpu_harness import say
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+H16 = 2.0 ** -8
+F64 = torch.float64
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def sco():
+    import spectral_correction_optimizer_amd as m
+    return m
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+# ---- cross entropy: the logit gradients ----------------------------------------------------
+# With h the identity, the logits are W's columns and dW[v][t] is token t's gradient of logit v over
+# the count, a power of two: the gradient product adds nothing but zeros to it, so dW shows d itself.
+
+# kept: one piece; limit 1: in pieces, each recomputed; T of each tile shape
+@pytest.mark.parametrize("limit", [0, 1])
+@pytest.mark.parametrize("T,V", [(1, 5000), (64, 3001), (256, 2000)])
+def test_xent_rounds_each_logit_gradient_once(T, V, limit):
+    """Half a step of bfloat16, and at most a quarter of that again for the exponential that is kept
+    between the passes."""
+    say(f"case: xent logit gradients T {T} V {V} limit {limit}")
+    g = gen(1)
+    W = (torch.randn(V, T, generator=g, device="cuda") * 1.5).bfloat16()
+    tgt = torch.randint(0, V, (T,), generator=g, device="cuda")
+    out = sco().xent(torch.eye(T, dtype=torch.bfloat16, device="cuda"), W, tgt, limit=limit)
+    s = W.to(F64)
+    lse = torch.logsumexp(s, 0)
+    p = torch.exp(s - lse)
+    ref = p.clone()
+    at = torch.arange(T, device="cuda")
+    ref[tgt, at] -= 1
+    got = out.dW.to(F64) * T
+    # float32: log-sum-exp, difference, exponential
+    f32 = (8 * s.abs().amax(0) + 4 * lse.abs() + 400 + V / 64 + 32) * U
+    rel = H16 * (1 if limit else 1.25) + H16 ** 2 + 2 * f32
+    tol = p * rel
+    tol[tgt, at] = ref[tgt, at].abs() * H16 + 2 * f32 * p[tgt, at] + 4 * U
+    bad = (got - ref).abs() > tol
+    assert not bad.any(), (int(bad.sum()), float(((got - ref).abs() / tol).max()))
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_xent_kept_exponentials_of_far_logits(sign):
+    """All logits of a token alike and beyond 2^24, where a tile's reference in powers of two lies a
+    whole number below the largest exponent unless it is raised: the probabilities stay 1 / V within
+    what float32 resolves of such logits."""
+    V, T = 200, 64
+    log2e = np.float32(1.44269504088896340736)
+    x = torch.arange(129, 256, dtype=F64) * 2.0 ** 18  # bfloat16 values from 2^25 on
+    x = (sign * x).numpy().astype(np.float32)
+    ref = np.ceil((x * log2e).astype(np.float32)).astype(np.float64)
+    above = x.astype(np.float64) * np.float64(log2e) - ref
+    x = x[above >= 1]
+    assert x.size >= 16
+    x = torch.from_numpy(np.resize(x, T)).cuda()
+    W = x[None, :].expand(V, T).bfloat16().contiguous()
+    assert torch.equal(W[0].float(), x)
+    out = sco().xent(torch.eye(T, dtype=torch.bfloat16, device="cuda"), W, torch.zeros(T, dtype=torch.long, device="cuda"))
+    got = out.dW[1:].to(F64) * T
+    assert (got > 0).all()
+    off = (got * V).log().abs()
+    assert (off <= 8 * x.abs().to(F64) * U + H16 * 2).all(), float(off.max())
