@@ -260,7 +260,7 @@ enum TpEpi {
     TP_STORE = 0,   // C = acc * alpha * gain[n], bfloat16 or float32
     TP_PART = 1,    // float32 sums of one split of k, [split][M][N]
     TP_STATS = 2,   // row maxima and exp sums of the tile; logits kept as P.keep says
-    TP_GRAD = 3,    // exp(acc - lse[m]) - [n is m's target], as bfloat16 planes
+    TP_GRAD = 3,    // (exp(acc - lse[m]) - [n is m's target]) * alpha, as bfloat16 planes
 };
 
 template <int BM_, int BN_, int WVM_, int WVN_, int NBUF_, int PER_CU_>
@@ -613,6 +613,7 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
                 if (m0 + r < M) gst(P.stat_sum + (int64_t)(P.stat_first + tn) * M + m0 + r, z);
             }
         } else {
+            const float alpha = gld(P.alpha);
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
                 const int m = lm + 16 * i;
@@ -626,8 +627,9 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
                     float v[4];
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        v[r] = tgt >= 0 && n + r < N ? __builtin_amdgcn_exp2f((acc[i][j][r] - lse) * kLog2e) -
-                                                           (P.n_first + n + r == tgt ? 1.0f : 0.0f)
+                        v[r] = tgt >= 0 && n + r < N ? (__builtin_amdgcn_exp2f((acc[i][j][r] - lse) * kLog2e) -
+                                                        (P.n_first + n + r == tgt ? 1.0f : 0.0f)) *
+                                                           alpha
                                                      : 0.0f;
                     tp_store_planes((uint16_t*)P.P, P.p_planes, P.p_plane, (int64_t)m * P.ldp + n, v);
                 }

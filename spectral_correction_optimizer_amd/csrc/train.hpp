@@ -32,7 +32,7 @@ struct TpArgs {
     void* C = nullptr;
     int64_t ldc = 0;
     int c_bf16 = 0;
-    const float* alpha = nullptr;  // device scalar (NULL: 1)
+    const float* alpha = nullptr;  // device scalar (NULL: 1); TP_GRAD: a factor of the values
     const void* gain = nullptr;    // column factors (NULL: 1)
     int gain_bf16 = 0;
     float* part = nullptr;
@@ -99,7 +99,7 @@ struct XentPlan {
     int64_t stat_tiles;        // tiles of a row
     TpPlan logits, logits_last, dh, dw, dw_last;
     // offsets into the workspace
-    int64_t o_share, o_h, o_w, o_s, o_p, o_tl, o_lse, o_smax, o_ssum, o_part, o_dh, bytes;
+    int64_t o_factors, o_h, o_w, o_s, o_p, o_tl, o_lse, o_smax, o_ssum, o_part, o_dh, bytes;
 };
 // limit: bytes that the kept probabilities (or a piece's) may take
 XentPlan xent_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit);

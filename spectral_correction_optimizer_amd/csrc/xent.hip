@@ -20,13 +20,15 @@
 //     piece only.
 // 8192 tokens, 131072 x 2048 in bfloat16: logits 3.8 ms (1150 TFLOP/s), d 0.85 ms (5.1 TB/s), dh
 // 3.2 ms (1350), dW 3.6 ms (1210).
-// d is kept without the factor 1 / count, which the gradients' stores apply.  The matrix cores take
-// d in bfloat16, half a step of its own value off (2^-8): two planes would double the gradient
-// products.  An exponential kept between the passes adds 2^-10 (tp_pack_unit).  Errors of dW against 64
-// bits at 64 tokens, 32000 x 2048, its rows' norm 1: 0.0019 in the rows of targets, 0.0024 in the
-// others, where exponentials kept in bfloat16 made it 0.0029; the rounding of dW alone is 0.0017.  The
-// exponentials cost the logits product 0.3% more.  The target's entry is formed from the float32
-// logit, as there the subtraction cancels.  In float32 d is split exactly into three planes.
+// Of the factor 1 / count, d takes the power of two next below, which is exact: its products with the
+// largest states then stay within float32's range as their mean does (0.4% of the call's time); the
+// gradients' stores apply the rest.  The matrix cores take d in bfloat16, half a step of its own
+// value off (2^-8): two planes would double the gradient products.  An exponential kept between
+// the passes adds 2^-10 (tp_pack_unit; 0.4% of the call's time).  Errors of dW against 64 bits at 64
+// tokens, 32000 x 2048, relative to its norm: 0.0019 in the rows of targets, 0.0024 in the others,
+// where exponentials kept in bfloat16 made it 0.0029; the rounding of dW alone is 0.0017.  The
+// target's entry is formed from the float32 logit, as there the subtraction cancels.  In float32 d is
+// split exactly into three planes.
 #include <cmath>
 
 #include "tile_product.hpp"
@@ -104,12 +106,14 @@ __global__ __launch_bounds__(256) void xent_dlogits_kernel(const float* __restri
                                                            const float* __restrict__ smax, int64_t T,
                                                            const float* __restrict__ lse,
                                                            const float* __restrict__ target_logit,
-                                                           const int64_t* __restrict__ targets, int64_t V) {
+                                                           const int64_t* __restrict__ targets, int64_t V,
+                                                           const float* __restrict__ scale_at) {
     const int64_t t = blockIdx.x / chunks;
+    const float scale = gld(scale_at);
     const int64_t tgt = tp_target(targets, V, t);
     const float ls = gld(lse + t);
     const float ls2 = ls * kLog2e;
-    const float at_target = tgt >= 0 ? expf(gld(target_logit + t) - ls) - 1.0f : 0.0f;
+    const float at_target = tgt >= 0 ? (expf(gld(target_logit + t) - ls) - 1.0f) * scale : 0.0f;
     const int64_t end = (N + 7) & ~7;  // the products read no further
     const int64_t from = (int64_t)(blockIdx.x % chunks) * chunk, to = from + chunk < end ? from + chunk : end;
     for (int64_t c = from + 8 * threadIdx.x; c < to; c += 8 * 256) {
@@ -117,7 +121,7 @@ __global__ __launch_bounds__(256) void xent_dlogits_kernel(const float* __restri
         float v[8];
         if constexpr (EXP) {
             const v4u w = *(const SC_GLOBAL v4u*)p;
-            const float f = __builtin_amdgcn_exp2f(gld(smax + (int64_t)(c / bn) * T + t) - ls2);
+            const float f = __builtin_amdgcn_exp2f(gld(smax + (int64_t)(c / bn) * T + t) - ls2) * scale;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 v[2 * i] = tp_unit_lo(w[i]) * f;
@@ -127,8 +131,8 @@ __global__ __launch_bounds__(256) void xent_dlogits_kernel(const float* __restri
             const v4f a = gld4(logits + t * ldp + c), b = gld4(logits + t * ldp + c + 4);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                v[i] = expf(a[i] - ls);
-                v[4 + i] = expf(b[i] - ls);
+                v[i] = expf(a[i] - ls) * scale;
+                v[4 + i] = expf(b[i] - ls) * scale;
             }
         }
 #pragma unroll
@@ -147,10 +151,11 @@ __global__ __launch_bounds__(256) void xent_dlogits_kernel(const float* __restri
     }
 }
 
-// the mean loss over the counted tokens, summed in a fixed order, and one token's share of it
+// the mean loss over the counted tokens, summed in a fixed order, and one token's share of it as the
+// factor of the gradients' stores (at least 1, below 2) and d's, a power of two
 __global__ __launch_bounds__(1024) void xent_mean_kernel(const float* __restrict__ loss,
                                                          const int64_t* __restrict__ targets, int64_t T, int64_t V,
-                                                         float* share, float* mean) {
+                                                         float* factors, float* mean) {
     __shared__ double red[16];
     double s = 0.0, n = 0.0;
 #pragma unroll 4
@@ -162,7 +167,10 @@ __global__ __launch_bounds__(1024) void xent_mean_kernel(const float* __restrict
     n = block_sum_f64(n, red);
     if (threadIdx.x == 0) {
         n = n > 0.0 ? n : 1.0;
-        gst(share, (float)(1.0 / n));
+        double scale = 1.0;
+        while (scale * n > 1.0) scale *= 0.5;
+        gst(factors, (float)(1.0 / (n * scale)));
+        gst(factors + 1, (float)scale);
         gst(mean, (float)(s / n));
     }
 }
@@ -202,7 +210,7 @@ XentPlan xent_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit) {
         return at;
     };
     const int np = bf16 ? 1 : 3;
-    p.o_share = take(4);
+    p.o_factors = take(8);
     p.o_h = take(2 * np * T * p.Hh);
     p.o_w = p.planes ? take(2 * np * V * p.Hp) : 0;
     p.o_s = !bf16 && p.keep ? take(4 * T * p.ldp) : 0;
@@ -227,7 +235,7 @@ hipError_t launch_xent(const XentPlan& p, const void* h, const void* W, const in
     char* ws = (char*)workspace;
     const int64_t T = p.T, V = p.V, H = p.H, Hp = p.Hp, Hh = p.Hh;
     const int np = p.bf16 ? 1 : 3;
-    float* share = (float*)(ws + p.o_share);
+    float* factors = (float*)(ws + p.o_factors);
     uint16_t* P = (uint16_t*)(ws + p.o_p);
     float* S = (float*)(ws + p.o_s);
     float *tl = (float*)(ws + p.o_tl), *lse = (float*)(ws + p.o_lse);
@@ -292,7 +300,7 @@ hipError_t launch_xent(const XentPlan& p, const void* h, const void* W, const in
     hipLaunchKernelGGL(xent_lse_kernel, dim3((unsigned)((T + 63) / 64)), dim3(1024), 0, st, smax, ssum,
                        (int)p.stat_tiles, pow2, tl, targets, T, V, lse, loss);
     SC_RUN(hipGetLastError());
-    hipLaunchKernelGGL(xent_mean_kernel, dim3(1), dim3(1024), 0, st, loss, targets, T, V, share, mean);
+    hipLaunchKernelGGL(xent_mean_kernel, dim3(1), dim3(1024), 0, st, loss, targets, T, V, factors, mean);
     SC_RUN(hipGetLastError());
 
     for (int i = 0; i < p.pieces; ++i) {
@@ -305,14 +313,15 @@ hipError_t launch_xent(const XentPlan& p, const void* h, const void* W, const in
             const dim3 grid((unsigned)(chunks * T));
             if (p.bf16)
                 hipLaunchKernelGGL(xent_dlogits_kernel<true>, grid, dim3(256), 0, st, nullptr, P, T * p.ldp, p.ldp, n,
-                                   p.logits.bn, chunk, chunks, smax, T, lse, tl, targets, V);
+                                   p.logits.bn, chunk, chunks, smax, T, lse, tl, targets, V, factors + 1);
             else
                 hipLaunchKernelGGL(xent_dlogits_kernel<false>, grid, dim3(256), 0, st, S, P, T * p.ldp, p.ldp, n,
-                                   p.logits.bn, chunk, chunks, smax, T, lse, tl, targets, V);
+                                   p.logits.bn, chunk, chunks, smax, T, lse, tl, targets, V, factors + 1);
             SC_RUN(hipGetLastError());
         } else {
             TpArgs a = logits(i);
             a.P = P;
+            a.alpha = factors + 1;
             SC_RUN(launch_tile_product(TPK_LOGIT_GRAD, logits_plan(i), a, TpSum{}, st));
         }
         TpArgs a;  // dh (+)= d W: k runs over the piece
@@ -330,7 +339,7 @@ hipError_t launch_xent(const XentPlan& p, const void* h, const void* W, const in
         a.C = dh;
         a.ldc = H;
         a.c_bf16 = p.bf16;
-        a.alpha = share;
+        a.alpha = factors;
         a.part = part;
         TpSum sum;
         if (p.pieces > 1) {
@@ -353,7 +362,7 @@ hipError_t launch_xent(const XentPlan& p, const void* h, const void* W, const in
         b.C = (char*)dW + v0 * H * (p.bf16 ? 2 : 4);
         b.ldc = H;
         b.c_bf16 = p.bf16;
-        b.alpha = share;
+        b.alpha = factors;
         b.part = part;
         SC_RUN(launch_tile_product(TPK_WEIGHTS, i + 1 < p.pieces ? p.dw : p.dw_last, b, TpSum{}, st));
     }

@@ -86,3 +86,23 @@ def test_xent_kept_exponentials_of_far_logits(sign):
     assert (got > 0).all()
     off = (got * V).log().abs()
     assert (off <= 8 * x.abs().to(F64) * U + H16 * 2).all(), float(off.max())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("limit", [0, 1])
+def test_xent_sums_of_the_largest_states(limit, dtype):
+    """States of 2^127: the mean's gradients are within float32's range, the plain sums over the tokens
+    are not."""
+    from tests.test_gpu_train import _xent_check, _xent_ref
+    T, V, H = 30, 300, 8
+    say(f"case: xent sums of the largest states limit {limit} {dtype}")
+    g = gen(4)
+    h = torch.randn(T, H, generator=g, device="cuda")
+    W = torch.randn(V, H, generator=g, device="cuda")
+    h[:, 0] = 2.0 ** 127
+    W[:, 0] = torch.randint(-8, 9, (V,), generator=g, device="cuda") * 2.0 ** -125
+    h, W = h.to(dtype), W.to(dtype)
+    tgt = torch.randint(0, 5, (T,), generator=g, device="cuda")
+    ref, tol = _xent_ref(h, W, tgt, dtype)
+    assert ref[3].abs().max() * T > 2.0 ** 128 > ref[3].abs().max()
+    _xent_check(sco().xent(h, W, tgt, limit=limit), ref, tol)
