@@ -445,7 +445,9 @@ int sc_act_wgrad(sc_dtype dtype, const void* dy, const int8_t* q, const uint8_t*
  * (0 if none), and the gradients of the mean: dh [T][H], dW [V][H].  The vocabulary
  * goes by in pieces.  limit: bytes that a piece's intermediate values may take (0: 4 GiB);
  * if the whole vocabulary's fit, they are kept between the forward and the gradient
- * products, otherwise each piece's are computed again.  T, V < 2^21 and H < 2^16. */
+ * products, otherwise each piece's are computed again.  T, V < 2^21 and H < 2^16.
+ * A NaN or an infinity in a counted row of h makes that token's loss, its row of dh, the mean and
+ * dW NaN; one in W makes all of them NaN. */
 int sc_xent_workspace(sc_dtype dtype, int64_t T, int64_t V, int H, int64_t limit, int64_t* bytes);
 int sc_xent(sc_dtype dtype, const void* h, const void* W, const int64_t* targets, int64_t T, int64_t V, int H,
             int64_t limit, float* loss, float* mean, void* dh, void* dW, void* workspace, int64_t workspace_bytes,

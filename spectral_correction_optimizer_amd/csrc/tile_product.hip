@@ -159,6 +159,31 @@ hipError_t launch_zero(void* p, int64_t bytes, hipStream_t st) {
     return hipGetLastError();
 }
 
+// The exact split of any float32 values (split8 rounds the first part, which overflows from
+// 0x1.FFp127 on and leaves infinity - infinity): the first part stays at bfloat16's largest value, and
+// an infinity is its own first part, beside zeros.
+__device__ __forceinline__ Split8 split8_any(const float (&f)[8]) {
+    constexpr float most = 0x1.FEp127f;
+    v4u h, m, l;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float first[2], rest[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const float x = f[2 * i + u], a = fabsf(x);
+            first[u] = a >= 0x1.FFp127f && a < __builtin_huge_valf() ? copysignf(most, x) : x;
+        }
+        h[i] = pack_bf16x2(first[0], first[1]);
+        rest[0] = f[2 * i] - bf16_lo(h[i]);
+        rest[1] = f[2 * i + 1] - bf16_hi(h[i]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) rest[u] = fabsf(f[2 * i + u]) == __builtin_huge_valf() ? 0.0f : rest[u];
+        m[i] = pack_bf16x2(rest[0], rest[1]);
+        l[i] = pack_bf16x2(rest[0] - bf16_lo(m[i]), rest[1] - bf16_hi(m[i]));
+    }
+    return Split8{__builtin_bit_cast(v8bf, h), __builtin_bit_cast(v8bf, m), __builtin_bit_cast(v8bf, l)};
+}
+
 // planes[p][r][c]: kGroups groups of eight columns a thread (ld is a multiple of 8)
 template <typename E, int ENDS>
 __global__ __launch_bounds__(256) void to_planes_kernel(const E* __restrict__ src, int64_t rows, int cols,
@@ -191,7 +216,7 @@ __global__ __launch_bounds__(256) void to_planes_kernel(const E* __restrict__ sr
             if constexpr (sizeof(E) == 2) {
                 store8(o, 8, f);  // exact
             } else {
-                const Split8 s = split8(f);
+                const Split8 s = split8_any(f);
                 *(SC_GLOBAL v8bf*)o = s.h;
                 *(SC_GLOBAL v8bf*)(o + plane) = s.m;
                 *(SC_GLOBAL v8bf*)(o + 2 * plane) = s.l;

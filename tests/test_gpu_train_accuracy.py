@@ -106,3 +106,51 @@ def test_xent_sums_of_the_largest_states(limit, dtype):
     ref, tol = _xent_ref(h, W, tgt, dtype)
     assert ref[3].abs().max() * T > 2.0 ** 128 > ref[3].abs().max()
     _xent_check(sco().xent(h, W, tgt, limit=limit), ref, tol)
+
+
+# ---- float32 operands that bfloat16 cannot hold ---------------------------------------------
+
+MOST = float(np.finfo(np.float32).max)
+FAR = [math.inf, -math.inf, math.nan, MOST, -MOST, float.fromhex("0x1.ffp127"), -float.fromhex("0x1.ff0002p127"),
+       float.fromhex("0x1.fefffep127"), float.fromhex("0x1.fep127")]
+
+
+def test_act_wgrad_keeps_infinities_and_the_largest_values():
+    """float32's largest values round to infinity in bfloat16, where the operand's planes begin: the
+    gradient of each output holds what the definition gives, and an infinity stays one."""
+    T, H = 40, 72
+    N = len(FAR) + 3
+    say(f"case: act_wgrad far values T {T} N {N} H {H}")
+    g = gen(2)
+    dy = torch.randn(T, N, generator=g, device="cuda")
+    for i, x in enumerate(FAR):
+        dy[7 * i % T, i] = x
+    kept = sco().act_pack(torch.randn(T, H, generator=g, device="cuda") * 2.0 ** -12)
+    n = sco().act_unpack(kept, torch.float32).cpu().to(F64)
+    d64 = dy.cpu().to(F64)
+    ref, mag = d64.t() @ n, d64.abs().t() @ n.abs()
+    got = sco().act_wgrad(dy, kept).cpu().to(F64)
+    assert torch.equal(got.isnan(), ref.isnan())
+    assert torch.equal(got.isinf(), ref.isinf()) and torch.equal(got[ref.isinf()], ref[ref.isinf()])
+    fin = ref.isfinite()
+    assert fin[3:].all()
+    # three products of T terms, two half steps a term, and the store
+    tol = ref.abs() * 2 * U + (3 * T + 64) * 2 * U * mag
+    assert ((got - ref).abs() <= tol)[fin].all()
+
+
+@pytest.mark.parametrize("limit", [0, 1])
+def test_xent_with_the_largest_states(limit):
+    """Float32 states next to the largest number, against weights that bring the logits back."""
+    from tests.test_gpu_train import _xent_check, _xent_ref
+    T, V, H = 30, 300, 8
+    say(f"case: xent largest states limit {limit}")
+    g = gen(3)
+    h = torch.randn(T, H, generator=g, device="cuda")
+    W = torch.randn(V, H, generator=g, device="cuda")
+    big = [x for x in FAR if math.isfinite(x)]
+    h[:, 0] = torch.tensor([big[t % len(big)] for t in range(T)], device="cuda")
+    W[:, 0] = torch.randint(-8, 9, (V,), generator=g, device="cuda") * 2.0 ** -125
+    tgt = torch.randint(0, V, (T,), generator=g, device="cuda")
+    ref, tol = _xent_ref(h, W, tgt, torch.float32)
+    _xent_check(sco().xent(h, W, tgt, limit=limit), ref, tol)
