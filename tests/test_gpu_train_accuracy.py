@@ -9,6 +9,7 @@ import pytest
 import torch
 
 from tests.gpu_harness import say
+from tests.test_train_bounds import rms, rms_bound
 
 pytestmark = pytest.mark.gpu
 
@@ -154,3 +155,53 @@ def test_xent_with_the_largest_states(limit):
     tgt = torch.randint(0, V, (T,), generator=g, device="cuda")
     ref, tol = _xent_ref(h, W, tgt, torch.float32)
     _xent_check(sco().xent(h, W, tgt, limit=limit), ref, tol)
+
+
+# ---- float32 products: the error's norm -----------------------------------------------------
+# (what a missing plane would do to it: tests/test_train_bounds.py)
+
+@pytest.mark.parametrize("T,N,H", [(2, 96, 200), (63, 65, 33), (1999, 96, 200)])
+def test_act_wgrad_has_the_accuracy_of_float32(T, N, H):
+    say(f"case: act_wgrad error T {T} N {N} H {H}")
+    g = gen(5)
+    dy = torch.randn(T, N, generator=g, device="cuda")
+    kept = sco().act_pack(torch.randn(T, H, generator=g, device="cuda"))
+    n = sco().act_unpack(kept, torch.float32).cpu().to(F64)
+    off = rms(sco().act_wgrad(dy, kept).cpu(), dy.cpu().to(F64).t() @ n)
+    assert off <= rms_bound(3, T), off / U
+
+
+@pytest.mark.parametrize("limit", [0, 1])
+def test_xent_logits_have_the_accuracy_of_float32(limit):
+    """Two words, one of them all zeros, and targets on the lesser logit: the loss is the other
+    logit's magnitude."""
+    T, H = 300, 520
+    g = gen(6)
+    h = torch.randn(T, H, generator=g, device="cuda") * 20
+    W = torch.randn(2, H, generator=g, device="cuda") * 20
+    W[1] = 0
+    x = h.cpu().to(F64) @ W[0].cpu().to(F64)
+    out = sco().xent(h, W, (x > 0).long().cuda(), limit=limit)
+    ref = x.abs() + torch.log1p(torch.exp(-x.abs()))
+    off = rms(out.loss.cpu(), ref)
+    assert off <= rms_bound(6, H), off / U
+
+
+@pytest.mark.parametrize("limit", [0, 1])
+def test_xent_gradients_have_the_accuracy_of_float32(limit):
+    """Logits and log-sum-exp below 8: they and their difference are off by at most 14 U in the mean."""
+    T, V, H = 300, 700, 520
+    g = gen(7)
+    h = torch.randn(T, H, generator=g, device="cuda") / math.sqrt(H)
+    W = torch.randn(V, H, generator=g, device="cuda") * 0.5
+    tgt = torch.randint(0, V, (T,), generator=g, device="cuda")
+    out = sco().xent(h, W, tgt, limit=limit)
+    h, W, at = h.cpu().to(F64), W.cpu().to(F64), torch.arange(T)
+    s = h @ W.t()
+    lse = torch.logsumexp(s, 1, keepdim=True)
+    assert s.abs().max() < 8 and lse.abs().max() < 8
+    d = torch.exp(s - lse)
+    d[at, tgt.cpu()] -= 1
+    for name, got, ref, K in (("dh", out.dh, d @ W / T, V), ("dW", out.dW, d.t() @ h / T, T)):
+        off = rms(got.cpu(), ref)
+        assert off <= rms_bound(6, K, 14), (name, off / U)
