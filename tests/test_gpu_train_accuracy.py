@@ -205,3 +205,43 @@ def test_xent_gradients_have_the_accuracy_of_float32(limit):
     for name, got, ref, K in (("dh", out.dh, d @ W / T, V), ("dW", out.dW, d.t() @ h / T, T)):
         off = rms(got.cpu(), ref)
         assert off <= rms_bound(6, K, 14), (name, off / U)
+
+
+# ---- residual norm: the 8-bit values are those of the rows in 64 bits -------------------------
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,H", [(4096, 1000), (2048, 2048), (300, 8191), (100, 16384)])
+def test_rmsnorm_picks_the_steps_of_64_bits(T, H, dtype):
+    """Every element of millions, but for those within 1e-10 of the border of two steps (of which
+    float32 rows missed a few in a million), and the statistics to a float32's rounding."""
+    from tests.test_gpu_train import pow2
+    say(f"case: rmsnorm steps T {T} H {H} {dtype}")
+    g = gen(8)
+    x = (torch.randn(T, H, generator=g, device="cuda") * 0.5).to(dtype)
+    r = torch.randn(T, H, generator=g, device="cuda").to(dtype)
+    gain = torch.randn(H, generator=g, device="cuda").to(dtype)
+    eps = 2.0 ** -17
+    out = sco().rmsnorm(x, gain, residual=r, eps=eps)
+    h = x.to(F64) + r.to(F64)
+    rstd = 1 / (h.square().mean(1) + eps).sqrt()
+    assert ((out.rstd.to(F64) - rstd).abs() <= U * (1 + 1e-6) * rstd).all()
+    n = h * rstd[:, None]
+    half = U if dtype == torch.float32 else H16
+    y = n * gain.to(F64)
+    assert ((out.y.to(F64) - y).abs() <= (half + 2 * U) * (1 + 1e-6) * y.abs()).all()
+    nb = -(-H // 32)
+    p = torch.zeros(T, nb * 32, dtype=F64, device="cuda")
+    p[:, :H] = n
+    p = p.reshape(T, nb, 32)
+    amax = p.abs().amax(2)
+    m, E = torch.frexp(amax)  # amax = m 2^E, m in [0.5, 1)
+    clear = ((m - 0.5).abs() > 1e-10) & ((1 - m).abs() > 1e-10)
+    assert clear.float().mean() > 0.999
+    assert torch.equal(out.kept.e[clear].int(), (E + 126)[clear].int())
+    steps = p * pow2(7 - E)[:, :, None]
+    border = (steps - steps.floor() - 0.5).abs() < 1e-10
+    want = steps.round().clamp(-127, 127)
+    q = torch.zeros(T, nb * 32, device="cuda", dtype=F64)
+    q[:, :H] = out.kept.q.to(F64)
+    same = (q.reshape(T, nb, 32) == want) | border | ~clear[:, :, None]
+    assert border.sum() < 100 and same.all(), int((~same).sum())
