@@ -245,3 +245,24 @@ def test_rmsnorm_picks_the_steps_of_64_bits(T, H, dtype):
     q[:, :H] = out.kept.q.to(F64)
     same = (q.reshape(T, nb, 32) == want) | border | ~clear[:, :, None]
     assert border.sum() < 100 and same.all(), int((~same).sum())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("limit", [0, 1])
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
+def test_xent_states_that_are_not_finite(value, limit, dtype):
+    """A counted token's: its loss, its row of dh, the mean and dW are NaN, the other rows are not.  A
+    token that is not counted: nothing is."""
+    T, V, H = 70, 300, 64
+    g = gen(9)
+    h = torch.randn(T, H, generator=g, device="cuda").to(dtype)
+    W = torch.randn(V, H, generator=g, device="cuda").to(dtype)
+    tgt = torch.randint(0, V, (T,), generator=g, device="cuda")
+    h[5, 7] = value
+    out = sco().xent(h, W, tgt, limit=limit)
+    rest = torch.arange(T, device="cuda") != 5
+    assert out.loss[5].isnan() and out.mean.isnan() and out.dh[5].isnan().all() and out.dW.isnan().all()
+    assert out.loss[rest].isfinite().all() and out.dh[rest].isfinite().all()
+    tgt[5] = V
+    out = sco().xent(h, W, tgt, limit=limit)
+    assert all(t.isfinite().all() for t in out)
