@@ -405,7 +405,7 @@ int sc_mask_unpack(sc_dtype dtype, const void* packed, const int32_t* idx, int64
  * stand for q * 2^(E - 6), q = round-to-even(x * 2^(6 - E)) clipped to +-127.  A
  * block that holds a NaN or an infinity has e = 255 and reads as NaN. */
 
-/* out[t] = scale * table[ids[t]]: table [V][H], out [T][H].  1 <= H <= 2^24. */
+/* out[t] = scale * table[ids[t]]: table [V][H], out [T][H].  T < 2^31, V <= 2^22, 1 <= H <= 2^24. */
 int sc_embed(sc_dtype dtype, const void* table, const int64_t* ids, int64_t T, int64_t V, int H, float scale,
              void* out, void* stream);
 
@@ -419,8 +419,8 @@ int sc_embed_grad(sc_dtype dtype, const void* dy, const int64_t* ids, int64_t T,
 int sc_act_pack(sc_dtype dtype, const void* x, int64_t T, int H, int8_t* q, uint8_t* e, void* stream);
 int sc_act_unpack(sc_dtype dtype, const int8_t* q, const uint8_t* e, int64_t T, int H, void* x, void* stream);
 
-/* h = x + residual, rstd = 1 / sqrt(mean(h^2) + eps), n = h * rstd, y = n * gain, all
- * from the float32 sum; q, e: the checkpoint of n.  residual may be NULL (h = x,
+/* h = x + residual, rstd = 1 / sqrt(mean(h^2) + eps), n = h * rstd, y = n * gain, summed and
+ * normalised in 64 bits from the unrounded sum; q, e: the checkpoint of n.  residual may be NULL (h = x,
  * then h may be NULL), h may be NULL, q and e may be NULL together.  gain [H], rstd
  * float32 [T].  h may be x or residual.  1 <= H <= 16384. */
 int sc_rmsnorm(sc_dtype dtype, const void* x, const void* residual, const void* gain, float eps, int64_t T, int H,
@@ -443,11 +443,14 @@ int sc_act_wgrad(sc_dtype dtype, const void* dy, const int8_t* q, const uint8_t*
 /* Softmax cross entropy of the logits h W^T (h [T][H], W [V][H]) against targets [T]:
  * loss float32 [T] (0 where not counted), mean float32 [1] over the counted tokens
  * (0 if none), and the gradients of the mean: dh [T][H], dW [V][H].  The vocabulary
- * goes by in pieces.  limit: bytes that a piece's intermediate values may take (0: 4 GiB);
- * if the whole vocabulary's fit, they are kept between the forward and the gradient
- * products, otherwise each piece's are computed again.  T, V < 2^21 and H < 2^16.
+ * goes by in pieces.  limit: bytes that a piece's intermediate values may take (0: 4 GiB).
+ * If the whole vocabulary's fit, a T x V matrix is kept between the forward and the gradient
+ * products (bfloat16: 2 bytes an entry; float32: the logits and the gradients' planes, 10 bytes);
+ * otherwise no such matrix exists, and each piece's logits are computed again (2 or 6 bytes an entry
+ * of a piece).  Beside the limit the workspace holds a copy of h, in float32 or when H % 8 != 0 one of W (6 or
+ * 2 bytes an element), and partial sums of the gradients.  T, V < 2^21 and H < 2^16.
  * A NaN or an infinity in a counted row of h makes that token's loss, its row of dh, the mean and
- * dW NaN; one in W makes all of them NaN. */
+ * dW NaN; one in W may make all of them NaN. */
 int sc_xent_workspace(sc_dtype dtype, int64_t T, int64_t V, int H, int64_t limit, int64_t* bytes);
 int sc_xent(sc_dtype dtype, const void* h, const void* W, const int64_t* targets, int64_t T, int64_t V, int H,
             int64_t limit, float* loss, float* mean, void* dh, void* dW, void* workspace, int64_t workspace_bytes,

@@ -451,7 +451,9 @@ def mask_unpack(packed: "torch.Tensor", idx: "torch.Tensor", H: int) -> "torch.T
 
 
 # ---- training-step operators: stateless calls --------------------------------------
-# Tensors are contiguous and on one device; work is queued on its current stream.
+# Tensors are contiguous and on one device; work is queued on its current stream.  These are plain
+# functions, not autograd ones: tensors that require gradients are taken as values, and the
+# results carry no graph.  The gradients are calls of their own (embed_grad, rmsnorm_grad, act_wgrad, xent).
 
 ActCheckpoint = collections.namedtuple("ActCheckpoint", "q e")
 ActCheckpoint.__doc__ = """An 8-bit checkpoint of a matrix [T, H]: int8 q [T, H] and uint8 e [T, ceil(H / 32)];
@@ -633,10 +635,12 @@ def act_wgrad(dy: "torch.Tensor", kept: ActCheckpoint, gain: "torch.Tensor" = No
 
 
 def xent(h: "torch.Tensor", W: "torch.Tensor", targets: "torch.Tensor", limit: int = 0) -> CrossEntropy:
-    """Softmax cross entropy of the logits h W^T (h [T, H], W [V, H]) against int64 targets [T],
-    without a matrix of logits, with the gradients of the mean over the counted tokens.  A
-    target outside [0, V) is not counted: its loss is 0.  limit: bytes for a vocabulary piece's
-    intermediate values (0: 4 GiB)."""
+    """Softmax cross entropy of the logits h W^T (h [T, H], W [V, H]) against int64 targets [T], with the
+    gradients of the mean over the counted tokens.  A target outside [0, V) is not counted: its loss
+    is 0.  limit: bytes for a vocabulary piece's intermediate values (0: 4 GiB).  Where the whole
+    vocabulary's fit (2 bytes for each of T x V entries, 10 in float32) they are kept between the
+    passes; otherwise there is no matrix of logits, and each piece's are computed again, about a
+    quarter slower."""
     T, H = _matrix("xent", "h", h)
     V = _matrix("xent", "W", W)[0]
     dev = h.device

@@ -20,7 +20,7 @@
 //   4. embed_cross: the sum of the partials of each row that crossed.
 // Bound by HBM: dy read once, dW written once (most rows of a large table are zeros).  65536
 // tokens x 2048 in bfloat16, 131072 rows: 5 + 8 + 11 us for steps 1 and 2, 162 us for step 3
-// (5.0 TB/s; zeros in a launch of their own: 114 + 119 us), 13 us for step 4.
+// (5.0 TB/s; zeros in a launch of their own: 114 + 119 us), 14 us for step 4.
 #include "internal.hpp"
 #include "rows.hpp"
 #include "train.hpp"

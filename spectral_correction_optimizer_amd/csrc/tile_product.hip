@@ -66,6 +66,8 @@ __global__ __launch_bounds__(256) void tp_reduce_kernel(const TpArgs P, const fl
 // products with both operands' rows contiguous, N x H from T tokens; us of the three shapes:
 //   8192 x 2048, T 16384:  436, 614, 829    8192 x 8192, T 2048: 317, 336, 429
 //   16384 x 4096, T 512:   101, 106, 119    32768 x 2048, T 64:   54,  49,  63
+// The same figures choose for the logits (k contiguous, row statistics behind every tile) and for the
+// segments of float32 products, which were not fitted.
 // A split's partial sums are written and read once more, at about 5 TB/s, by another kernel.
 TpPlan tp_plan(int M, int N, int K, int nseg, bool may_split) {
     struct Shape {

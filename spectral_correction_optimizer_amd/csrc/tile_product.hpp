@@ -19,10 +19,10 @@
 // loop is unrolled over them, so the reads of one buffer do not wait for the loads that fill
 // another.
 //
-// At 256 x 256, 8 waves and two buffers: 1340 TFLOP/s at 8192 x 2048 x 131072 (A with k
-// contiguous, B with rows), 1205 at 131072 x 2048 x 8192 (both with rows), where the matrix
-// cores are busy for 65% of the cycles, LDS for a quarter of them without a bank conflict,
-// and the clock has fallen to 1.75 GHz: fewer wasted cycles no longer make it faster.  Tried
+// At 256 x 256, 8 waves and two buffers: 1330 TFLOP/s at 8192 x 2048 x 131072 (A with k
+// contiguous, B with rows), 1190 at 131072 x 2048 x 8192 (both with rows).  The matrix cores are
+// busy for 66 and 61% of the cycles, LDS for a quarter of them without a bank conflict, at a clock
+// of 1.85 GHz (2.4 at most).  Tried
 // and not kept: four buffers of 32 k (64-byte rows where k is contiguous: 10% slower there),
 // fragments that are read in the step that multiplies them (1040), addresses formed in
 // every step instead of every turn of the buffers (8% slower), and sums that the register
@@ -385,8 +385,6 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
     };
     using P0 = std::integral_constant<int, 0>;
     using P1 = std::integral_constant<int, 1>;
-    using Yes = std::true_type;
-    using No = std::false_type;
     // every tile of a turn takes the same number of loads (the ones past the end fetch nothing)
     constexpr int PER = LA::NL + LB::NL;
     // Buffer u of a turn: its halves' fragments are read during the products of the step before

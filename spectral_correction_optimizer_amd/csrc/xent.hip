@@ -1,5 +1,4 @@
-// Softmax cross entropy over a large vocabulary with its gradients, without a matrix of
-// logits:
+// Softmax cross entropy over a large vocabulary with its gradients, the logits held in pieces:
 //
 //   s[t][v] = h[t] . W[v],  lse[t] = log sum_v exp(s[t][v]),  loss[t] = lse[t] - s[t][y_t]
 //   mean = sum of loss over the counted t / count
@@ -11,15 +10,17 @@
 // The products run on the matrix cores (tile_product.hpp); they are the cost at large T
 // (3 products of 2 T V H operations), reading W and writing dW at small T.  The vocabulary
 // goes by in pieces:
-//   - If one piece (the whole vocabulary) fits the limit, the logits product leaves
-//     exponentials relative to each tile's row maximum (16 bits; float32 operands: the
-//     logits in float32), xent_dlogits_kernel turns them into d once every row's sum is
-//     known, and the two gradient products read d: three products.
-//   - Otherwise a first pass over the pieces takes only the row sums, and a second one
-//     recomputes each piece's logits straight into d: four products, and memory for one
+//   - If one piece (the whole vocabulary) fits the limit, a T x V matrix is kept: the logits product
+//     leaves exponentials relative to each tile's row maximum (16 bits; float32 operands: the
+//     logits in float32, beside d's planes 10 bytes an entry), xent_dlogits_kernel turns them into d
+//     once every row's sum is known, and the two gradient products read d: three products.
+//   - Otherwise no matrix of logits exists: a first pass over the pieces takes only the row sums, and
+//     a second one recomputes each piece's logits straight into d: four products, and memory for one
 //     piece only.
-// 8192 tokens, 131072 x 2048 in bfloat16: logits 3.8 ms (1150 TFLOP/s), d 0.85 ms (5.1 TB/s), dh
-// 3.2 ms (1350), dW 3.6 ms (1210).
+// 8192 tokens, 131072 x 2048 in bfloat16, kept: logits 3.9 ms (1130 TFLOP/s), d 0.85 ms (5.1 TB/s), dh
+// 3.3 ms (1330), dW 3.7 ms (1190), the call 11.7 to 11.9 ms.  In pieces of 1 GiB or 256 MiB 15.0 ms, of 64 MiB
+// 16.4 ms (the gradients' sums over the pieces); 32768 tokens, in pieces by default, 59 ms.  Float32, 4096
+// tokens, 50021 x 1024: kept 7.2 ms, in pieces of 256 MiB 8.9 ms.
 // Of the factor 1 / count, d takes the power of two next below, which is exact: its products with the
 // largest states then stay within float32's range as their mean does (0.4% of the call's time); the
 // gradients' stores apply the rest.  The matrix cores take d in bfloat16, half a step of its own
