@@ -384,9 +384,11 @@ int sc_mask_unpack(sc_dtype dtype, const void* packed, const int32_t* idx, int64
 
 /* ---- Training-step operators ------------------------------------------------------
  * The two ends of a training step around the masked boundary: token embedding
- * with its gradient, the residual root-mean-square norm with an 8-bit
- * checkpoint of its output, the gradients that read the checkpoint, and softmax
- * cross entropy over a large vocabulary with its gradients.
+ * with its gradient, the residual root-mean-square and layer norms with an 8-bit
+ * checkpoint of their output, the gradients that read the checkpoint, and over a
+ * large vocabulary, with their gradients, softmax cross entropy, the clipped policy
+ * loss and the preference loss of paired answers; and the global gradient norm with
+ * clipping, before sc_step.
  *
  * These calls need no handle.  All pointers are device pointers on the current
  * device, matrices row-major and contiguous, `dtype` the type of every tensor
@@ -396,7 +398,7 @@ int sc_mask_unpack(sc_dtype dtype, const void* packed, const int32_t* idx, int64
  * allocate nothing; every call only enqueues.  Results do not depend on timing
  * (no floating-point atomics).  Token ids and targets are int64; one outside
  * [0, V) is no token: a zero row in sc_embed, no gradient in sc_embed_grad, not
- * counted in sc_xent.  T = 0 is allowed everywhere.
+ * counted in the losses.  T = 0 is allowed everywhere.
  * Errors: SC_ERR_INVALID_ARG (NULL or misaligned pointer, unknown dtype, too
  * small a workspace), SC_ERR_SHAPE (sizes out of range), before any GPU work.
  *
@@ -455,6 +457,74 @@ int sc_xent_workspace(sc_dtype dtype, int64_t T, int64_t V, int H, int64_t limit
 int sc_xent(sc_dtype dtype, const void* h, const void* W, const int64_t* targets, int64_t T, int64_t V, int H,
             int64_t limit, float* loss, float* mean, void* dh, void* dW, void* workspace, int64_t workspace_bytes,
             void* stream);
+
+/* The targets' log-probabilities under softmax(h W^T), float32 [T]; 0 where a token is not counted.  The rows
+ * of counted tokens are put together on the device, and only their logits are formed.  Sizes as sc_xent's. */
+int sc_token_logp_workspace(sc_dtype dtype, int64_t T, int64_t V, int H, int64_t* bytes);
+int sc_token_logp(sc_dtype dtype, const void* h, const void* W, const int64_t* targets, int64_t T, int64_t V, int H,
+                  float* logp, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* The clipped policy loss with a KL term.  For each counted token, with r = exp(logp - old_logp), A its
+ * advantage and x = ref_logp - logp:
+ *   loss = -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A) + kl (exp(x) - x - 1)
+ * and total = the sum of weights * loss (weights NULL: the mean over the counted tokens; weight 0: the token
+ * counts for nothing), with the gradients of total: dh [T][H], dW [V][H].  A token whose ratio is past the
+ * clip on its advantage's side has the KL term's gradient only.  old_logp, advantages, ref_logp (NULL: kl
+ * must be 0 and kl_mean NULL) and weights are float32 [T] and are not read where a token is not counted.
+ * Written: loss, logp float32 [T] (0 where not counted), total, kl_mean (NULL or the mean of
+ * exp(x) - x - 1), clipped (the share of tokens past the clip), float32 [1] each.  limit and workspace as
+ * sc_xent's, 20 bytes a token more.  0 <= clip_low <= 1, clip_high, kl >= 0.
+ *
+ * The gradients' products run over the counted tokens only; logit gradients are rounded as sc_xent's are. */
+int sc_token_loss_workspace(sc_dtype dtype, int64_t T, int64_t V, int H, int64_t limit, int64_t* bytes);
+int sc_policy_loss(sc_dtype dtype, const void* h, const void* W, const int64_t* targets, const float* old_logp,
+                   const float* advantages, const float* ref_logp, const float* weights, int64_t T, int64_t V, int H,
+                   float clip_low, float clip_high, float kl, int64_t limit, float* loss, float* total,
+                   float* kl_mean, float* clipped, float* logp, void* dh, void* dW, void* workspace,
+                   int64_t workspace_bytes, void* stream);
+
+/* The preference loss of pairs of sequences: sequence i is the tokens starts[i] .. starts[i + 1] - 1 (int64
+ * [2 pairs + 1] on the device, none smaller than the one before; starts outside [0, T] are taken as the
+ * nearest end), 2 p the preferred one of pair p and 2 p + 1 the other.  R_i = beta times the sum (average: the
+ * mean) of logp - ref_logp over the sequence's counted tokens, 0 where it has none, and
+ *   z = R_2p - R_2p+1 - margin,  loss_p = -(1 - smoothing) log sigmoid(z) - smoothing log sigmoid(-z).
+ * mean (float32 [1]) is over the pairs (0 if none); dh, dW are its gradients.  ref_logp float32 [T] or NULL (0).
+ * Written: loss float32 [pairs], rewards float32 [pairs][2] (R), logp as sc_policy_loss.  Tokens of no
+ * sequence have no gradient.  Workspace: sc_token_loss_workspace.  0 <= pairs <= 2^20, beta >= 0,
+ * 0 <= smoothing <= 1. */
+int sc_preference_loss(sc_dtype dtype, const void* h, const void* W, const int64_t* targets, const int64_t* starts,
+                       const float* ref_logp, int64_t pairs, int64_t T, int64_t V, int H, float beta, float margin,
+                       float smoothing, int average, int64_t limit, float* loss, float* mean, float* rewards,
+                       float* logp, void* dh, void* dW, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* h = x + residual, mean and rstd = 1 / sqrt(mean((h - mean)^2) + eps) of each row (float32 [T]),
+ * n = (h - mean) * rstd, y = n * gain + bias, summed and normalised in 64 bits from the unrounded sum; q, e:
+ * the checkpoint of n.  residual, bias, h, and q and e together may be NULL; h may be x or residual.
+ * 1 <= H <= 16384. */
+int sc_layernorm(sc_dtype dtype, const void* x, const void* residual, const void* gain, const void* bias, float eps,
+                 int64_t T, int H, void* h, void* y, float* mean, float* rstd, int8_t* q, uint8_t* e, void* stream);
+
+/* With a = dy * gain: dx = dh + rstd * (a - mean(a) - n * mean(a * n)), the gradient of x and of the
+ * residual; dgain, dbias [H] float32 = sums over tokens of dy * n and of dy.  n comes from the
+ * checkpoint (q, e; then h and mean are NULL), or is (h - mean) * rstd (then q and e are NULL).  dh and dbias may
+ * be NULL; dx may be dy or dh. */
+int sc_layernorm_grad_workspace(int64_t T, int H, int64_t* bytes);
+int sc_layernorm_grad(sc_dtype dtype, const void* dy, const void* gain, const float* rstd, const int8_t* q,
+                      const uint8_t* e, const void* h, const float* mean, const void* dh, int64_t T, int H, void* dx,
+                      float* dgain, float* dbias, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* The global norm of n gradients (host arrays of n types, sizes in elements and device pointers; an empty
+ * tensor's pointer is not looked at): sumsq = the sum of g^2 over all elements, in 64 bits on the device, in
+ * a fixed order.  Sharded gradients add their sumsq over the ranks before sc_clip_grads. */
+int sc_grad_sumsq_workspace(int n, const sc_dtype* dtypes, const int64_t* sizes, int64_t* bytes);
+int sc_grad_sumsq(int n, const sc_dtype* dtypes, const int64_t* sizes, const void* const* grads, double* sumsq,
+                  void* workspace, int64_t workspace_bytes, void* stream);
+
+/* norm = sqrt(sumsq), scale = min(1, max_norm / (norm + 1e-6)) (float32 [1] each) and out[i] = grads[i] * scale;
+ * out[i] may be grads[i], which then stays as it is where scale is 1.  An infinite norm gives scale 0,
+ * NaN gives NaN.  max_norm >= 0. */
+int sc_clip_grads(int n, const sc_dtype* dtypes, const int64_t* sizes, const void* const* grads, void* const* out,
+                  const double* sumsq, float max_norm, float* norm, float* scale, void* stream);
 
 #ifdef __cplusplus
 }

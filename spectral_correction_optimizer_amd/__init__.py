@@ -25,7 +25,8 @@ import torch  # loaded first: libscopt then binds to torch's HIP runtime
 __all__ = ["SpectralAdamW", "ScoptError", "library_path", "load_library", "EXPORTED_SYMBOLS",
            "mask_keep_count", "mask_seed", "mask_indices", "mask_pack", "mask_unpack",
            "ActCheckpoint", "RmsNorm", "CrossEntropy", "embed", "embed_grad", "act_pack", "act_unpack",
-           "rmsnorm", "rmsnorm_grad", "act_wgrad", "xent"]
+           "rmsnorm", "rmsnorm_grad", "act_wgrad", "xent", "LayerNorm", "layernorm", "layernorm_grad", "GradNorm",
+           "grad_sumsq", "clip_grads", "PolicyLoss", "PreferenceLoss", "token_logp", "policy_loss", "preference_loss"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libscopt.so")
@@ -40,7 +41,9 @@ EXPORTED_SYMBOLS = (
     "sc_mask_keep_count", "sc_mask_seed", "sc_mask_indices", "sc_mask_pack", "sc_mask_unpack",
     "sc_embed", "sc_embed_grad_workspace", "sc_embed_grad", "sc_act_pack", "sc_act_unpack", "sc_rmsnorm",
     "sc_rmsnorm_grad_workspace", "sc_rmsnorm_grad", "sc_act_wgrad_workspace", "sc_act_wgrad",
-    "sc_xent_workspace", "sc_xent",
+    "sc_xent_workspace", "sc_xent", "sc_token_logp_workspace", "sc_token_logp", "sc_token_loss_workspace",
+    "sc_policy_loss", "sc_preference_loss", "sc_layernorm", "sc_layernorm_grad_workspace", "sc_layernorm_grad",
+    "sc_grad_sumsq_workspace", "sc_grad_sumsq", "sc_clip_grads",
 )
 
 SC_F32, SC_BF16 = 0, 1
@@ -146,6 +149,18 @@ def load_library():
         "sc_act_wgrad": (i32, [dt, vp, vp, vp, vp, i64, i64, i32, vp, vp, i64, vp]),
         "sc_xent_workspace": (i32, [dt, i64, i64, i32, i64, i64p]),
         "sc_xent": (i32, [dt, vp, vp, vp, i64, i64, i32, i64, vp, vp, vp, vp, vp, i64, vp]),
+        "sc_token_logp_workspace": (i32, [dt, i64, i64, i32, i64p]),
+        "sc_token_logp": (i32, [dt, vp, vp, vp, i64, i64, i32, vp, vp, i64, vp]),
+        "sc_token_loss_workspace": (i32, [dt, i64, i64, i32, i64, i64p]),
+        "sc_policy_loss": (i32, [dt] + [vp] * 7 + [i64, i64, i32, f32, f32, f32, i64] + [vp] * 8 + [i64, vp]),
+        "sc_preference_loss": (i32, [dt] + [vp] * 5 + [i64, i64, i64, i32, f32, f32, f32, i32, i64] + [vp] * 7 +
+                               [i64, vp]),
+        "sc_layernorm": (i32, [dt, vp, vp, vp, vp, f32, i64, i32, vp, vp, vp, vp, vp, vp, vp]),
+        "sc_layernorm_grad_workspace": (i32, [i64, i32, i64p]),
+        "sc_layernorm_grad": (i32, [dt] + [vp] * 8 + [i64, i32, vp, vp, vp, vp, i64, vp]),
+        "sc_grad_sumsq_workspace": (i32, [i32, vp, vp, i64p]),
+        "sc_grad_sumsq": (i32, [i32, vp, vp, vp, vp, vp, i64, vp]),
+        "sc_clip_grads": (i32, [i32, vp, vp, vp, vp, vp, f32, vp, vp, vp]),
     })
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -453,7 +468,8 @@ def mask_unpack(packed: "torch.Tensor", idx: "torch.Tensor", H: int) -> "torch.T
 # ---- training-step operators: stateless calls --------------------------------------
 # Tensors are contiguous and on one device; work is queued on its current stream.  These are plain
 # functions, not autograd ones: tensors that require gradients are taken as values, and the
-# results carry no graph.  The gradients are calls of their own (embed_grad, rmsnorm_grad, act_wgrad, xent).
+# results carry no graph.  The gradients are calls of their own (embed_grad, rmsnorm_grad, layernorm_grad,
+# act_wgrad) or come with the loss (xent, policy_loss, preference_loss).
 
 ActCheckpoint = collections.namedtuple("ActCheckpoint", "q e")
 ActCheckpoint.__doc__ = """An 8-bit checkpoint of a matrix [T, H]: int8 q [T, H] and uint8 e [T, ceil(H / 32)];
@@ -655,3 +671,218 @@ def xent(h: "torch.Tensor", W: "torch.Tensor", targets: "torch.Tensor", limit: i
     _run(dev, lib.sc_xent, _DT[h.dtype], h.data_ptr(), W.data_ptr(), targets.data_ptr(), T, V, H, int(limit),
          loss.data_ptr(), mean.data_ptr(), dh.data_ptr(), dW.data_ptr(), ws.data_ptr(), n)
     return CrossEntropy(loss, mean, dh, dW)
+
+
+# ---- losses of given tokens ------------------------------------------------------------
+
+PolicyLoss = collections.namedtuple("PolicyLoss", "loss total kl clipped logp dh dW")
+PolicyLoss.__doc__ = """Of policy_loss: float32 losses and log-probabilities [T], their weighted sum, the mean KL
+term (None without ref_logp) and the share of tokens past the clip (0-dim), and the weighted sum's gradients."""
+
+PreferenceLoss = collections.namedtuple("PreferenceLoss", "loss mean rewards logp dh dW")
+PreferenceLoss.__doc__ = """Of preference_loss: float32 losses [pairs], their mean (0-dim), rewards [pairs, 2],
+log-probabilities [T], and the mean's gradients."""
+
+
+def _token_check(who, h, W, targets, *named):
+    """Sizes T, V, H of a loss's operands; named: (name, float32 tensor or None) of the tokens."""
+    T, H = _matrix(who, "h", h)
+    V = _matrix(who, "W", W)[0]
+    per_token = [(name, t, torch.float32, (T,)) for name, t in named if t is not None]
+    _train_check(who, h.dtype, h.device, ("h", h, h.dtype, (T, H)), ("W", W, h.dtype, (V, H)),
+                 ("targets", targets, torch.int64, (T,)), *per_token)
+    return T, V, H
+
+
+def token_logp(h: "torch.Tensor", W: "torch.Tensor", targets: "torch.Tensor") -> "torch.Tensor":
+    """Log-probabilities float32 [T] of int64 targets [T] under the softmax of the logits h W^T (h [T, H],
+    W [V, H]); 0 where a target lies outside [0, V).  There is no matrix of logits."""
+    T, V, H = _token_check("token_logp", h, W, targets)
+    dev, lib = h.device, load_library()
+    h, W = _at16(h), _at16(W)
+    ws, n = _workspace(dev, "sc_token_logp_workspace", _DT[h.dtype], T, V, H)
+    logp = torch.empty(T, dtype=torch.float32, device=dev)
+    _run(dev, lib.sc_token_logp, _DT[h.dtype], h.data_ptr(), W.data_ptr(), targets.data_ptr(), T, V, H,
+         logp.data_ptr(), ws.data_ptr(), n)
+    return logp
+
+
+def policy_loss(h: "torch.Tensor", W: "torch.Tensor", targets: "torch.Tensor", old_logp: "torch.Tensor",
+                advantages: "torch.Tensor", ref_logp: "torch.Tensor" = None, clip=(0.2, 0.2), kl: float = 0.0,
+                weights: "torch.Tensor" = None, limit: int = 0) -> PolicyLoss:
+    """The clipped policy loss of sampled tokens, with gradients: r = exp(logp - old_logp),
+    loss = -min(r A, clip(r, 1 - clip[0], 1 + clip[1]) A) + kl (exp(x) - x - 1) with x = ref_logp - logp.
+    total is the sum of weights * loss; without weights the mean over the counted tokens.  Tokens
+    whose target lies outside [0, V) (prompts, padding) are not counted; only the others' rows are
+    worked on.  old_logp, advantages, ref_logp and weights are float32 [T]; limit as xent's."""
+    T, V, H = _token_check("policy_loss", h, W, targets, ("old_logp", old_logp), ("advantages", advantages),
+                           ("ref_logp", ref_logp), ("weights", weights))
+    low, high = clip
+    if kl and ref_logp is None:
+        raise ValueError("policy_loss: kl needs ref_logp")
+    dev, lib = h.device, load_library()
+    h, W = _at16(h), _at16(W)
+    ws, n = _workspace(dev, "sc_token_loss_workspace", _DT[h.dtype], T, V, H, int(limit))
+    loss, logp = torch.empty(2, T, dtype=torch.float32, device=dev).unbind()
+    total, mean_kl, clipped = torch.empty(3, dtype=torch.float32, device=dev).unbind()
+    dh, dW = torch.empty_like(h), torch.empty_like(W)
+    _run(dev, lib.sc_policy_loss, _DT[h.dtype], h.data_ptr(), W.data_ptr(), targets.data_ptr(), old_logp.data_ptr(),
+         advantages.data_ptr(), _ptr(ref_logp), _ptr(weights), T, V, H, float(low), float(high), float(kl), int(limit),
+         loss.data_ptr(), total.data_ptr(), None if ref_logp is None else mean_kl.data_ptr(), clipped.data_ptr(),
+         logp.data_ptr(), dh.data_ptr(), dW.data_ptr(), ws.data_ptr(), n)
+    return PolicyLoss(loss, total, None if ref_logp is None else mean_kl, clipped, logp, dh, dW)
+
+
+def preference_loss(h: "torch.Tensor", W: "torch.Tensor", targets: "torch.Tensor", starts: "torch.Tensor",
+                    ref_logp: "torch.Tensor" = None, beta: float = 0.1, margin: float = 0.0, smoothing: float = 0.0,
+                    average: bool = False, limit: int = 0) -> PreferenceLoss:
+    """The preference loss of pairs of sequences, with gradients.  starts: int64 [2 pairs + 1], ascending;
+    sequence i is the tokens starts[i] to starts[i + 1], the preferred one of pair p is sequence 2 p and the
+    other 2 p + 1.  With R the rewards, beta times the sum (average: the mean) of logp - ref_logp over a
+    sequence's counted tokens, z = R[p, 0] - R[p, 1] - margin and
+    loss = -(1 - smoothing) log sigmoid(z) - smoothing log sigmoid(-z), averaged over the pairs.
+    Tokens whose target lies outside [0, V) are not counted.  ref_logp float32 [T]; limit as xent's."""
+    T, V, H = _token_check("preference_loss", h, W, targets, ("ref_logp", ref_logp))
+    pairs = (starts.numel() - 1) // 2
+    _train_check("preference_loss", h.dtype, h.device, ("starts", starts, torch.int64, (2 * max(pairs, 0) + 1,)))
+    dev, lib = h.device, load_library()
+    h, W = _at16(h), _at16(W)
+    ws, n = _workspace(dev, "sc_token_loss_workspace", _DT[h.dtype], T, V, H, int(limit))
+    logp = torch.empty(T, dtype=torch.float32, device=dev)
+    loss = torch.empty(pairs, dtype=torch.float32, device=dev)
+    rewards = torch.empty(pairs, 2, dtype=torch.float32, device=dev)
+    mean = torch.empty((), dtype=torch.float32, device=dev)
+    dh, dW = torch.empty_like(h), torch.empty_like(W)
+    _run(dev, lib.sc_preference_loss, _DT[h.dtype], h.data_ptr(), W.data_ptr(), targets.data_ptr(), starts.data_ptr(),
+         _ptr(ref_logp), pairs, T, V, H, float(beta), float(margin), float(smoothing), int(bool(average)), int(limit),
+         loss.data_ptr(), mean.data_ptr(), rewards.data_ptr(), logp.data_ptr(), dh.data_ptr(), dW.data_ptr(),
+         ws.data_ptr(), n)
+    return PreferenceLoss(loss, mean, rewards, logp, dh, dW)
+
+
+# ---- layer norm --------------------------------------------------------------------------
+
+LayerNorm = collections.namedtuple("LayerNorm", "h y mean rstd kept")
+LayerNorm.__doc__ = """Of layernorm: the residual sum h, the output y, the rows' mean and 1 / standard deviation
+(float32 [T]) and the checkpoint of the normalised rows (None where none was kept)."""
+
+
+def layernorm(x: "torch.Tensor", gain: "torch.Tensor", bias: "torch.Tensor" = None, residual: "torch.Tensor" = None,
+              eps: float = 1e-5, keep: bool = True) -> LayerNorm:
+    """h = x + residual (x without one), rstd = 1 / sqrt(variance of h + eps), n = (h - mean) * rstd and
+    y = n * gain + bias for rows of x [T, H], and with keep the 8-bit checkpoint of n for the backward pass."""
+    T, H = _matrix("layernorm", "x", x)
+    named = [("x", x, x.dtype, (T, H)), ("gain", gain, x.dtype, (H,))]
+    if bias is not None:
+        named.append(("bias", bias, x.dtype, (H,)))
+    if residual is not None:
+        named.append(("residual", residual, x.dtype, (T, H)))
+    dev = x.device
+    _train_check("layernorm", x.dtype, dev, *named)
+    h = x if residual is None else torch.empty_like(x)
+    y = torch.empty_like(x)
+    mean, rstd = torch.empty(2, T, dtype=torch.float32, device=dev).unbind()
+    kept = None
+    if keep:
+        kept = ActCheckpoint(torch.empty((T, H), dtype=torch.int8, device=dev),
+                             torch.empty((T, -(-H // 32)), dtype=torch.uint8, device=dev))
+    _run(dev, load_library().sc_layernorm, _DT[x.dtype], x.data_ptr(), _ptr(residual), gain.data_ptr(), _ptr(bias),
+         float(eps), T, H, None if residual is None else h.data_ptr(), y.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+         kept.q.data_ptr() if keep else None, kept.e.data_ptr() if keep else None)
+    return LayerNorm(h, y, mean, rstd, kept)
+
+
+def layernorm_grad(dy: "torch.Tensor", gain: "torch.Tensor", rstd: "torch.Tensor", kept: ActCheckpoint = None,
+                   h: "torch.Tensor" = None, mean: "torch.Tensor" = None, dh: "torch.Tensor" = None):
+    """(dx, dgain, dbias) of layernorm from its checkpoint, or from h and mean without one: dx [T, H] is the
+    gradient of x and of the residual, with dh, the gradient that reaches h past the norm, added;
+    dgain and dbias float32 [H]."""
+    T, H = _matrix("layernorm_grad", "dy", dy)
+    if (kept is None) == (h is None) or (h is None) != (mean is None):
+        raise ValueError("layernorm_grad: either kept or h and mean are needed")
+    named = [("dy", dy, dy.dtype, (T, H)), ("gain", gain, dy.dtype, (H,)), ("rstd", rstd, torch.float32, (T,))]
+    if h is not None:
+        named += [("h", h, dy.dtype, (T, H)), ("mean", mean, torch.float32, (T,))]
+    if dh is not None:
+        named.append(("dh", dh, dy.dtype, (T, H)))
+    dev = dy.device
+    _train_check("layernorm_grad", dy.dtype, dev, *named)
+    if kept is not None:
+        _check_kept("layernorm_grad", kept, T, H, dy.dtype, dev)
+    lib = load_library()
+    ws, n = _workspace(dev, "sc_layernorm_grad_workspace", T, H)
+    dx = torch.empty_like(dy)
+    dgain, dbias = torch.empty(2, H, dtype=torch.float32, device=dev).unbind()
+    _run(dev, lib.sc_layernorm_grad, _DT[dy.dtype], dy.data_ptr(), gain.data_ptr(), rstd.data_ptr(),
+         None if kept is None else kept.q.data_ptr(), None if kept is None else kept.e.data_ptr(), _ptr(h), _ptr(mean),
+         _ptr(dh), T, H, dx.data_ptr(), dgain.data_ptr(), dbias.data_ptr(), ws.data_ptr(), n)
+    return dx, dgain, dbias
+
+
+# ---- global gradient norm ------------------------------------------------------------------
+
+GradNorm = collections.namedtuple("GradNorm", "norm scale grads")
+GradNorm.__doc__ = "Of clip_grads: the norm and the factor (float32, 0-dim) and the clipped gradients."
+
+
+def _grad_table(who, tensors, like=None):
+    """Host arrays (types, sizes, pointers) of a list of gradients; like: the list that they have to match."""
+    n = len(tensors)
+    if like is not None and len(like) != n:
+        raise ValueError(f"{who}: {n} outputs for {len(like)} gradients")
+    dev = tensors[0].device
+    if dev.type != "cuda":
+        raise ValueError(f"{who}: tensors must be on a GPU, got {dev}")
+    dtypes, sizes, where = (ctypes.c_int * n)(), (ctypes.c_int64 * n)(), (ctypes.c_void_p * n)()
+    for i, t in enumerate(tensors):
+        dt = _DT.get(t.dtype)
+        if dt is None or t.device != dev or not t.is_contiguous():
+            raise ValueError(f"{who}: tensor {i} must be a contiguous float32 or bfloat16 tensor on {dev}, got "
+                             f"{t.dtype} {tuple(t.shape)} on {t.device}"
+                             f"{'' if t.is_contiguous() else ' (not contiguous)'}")
+        if like is not None and (t.shape != like[i].shape or t.dtype is not like[i].dtype):
+            raise ValueError(f"{who}: output {i} is {t.dtype} {tuple(t.shape)}, its gradient {like[i].dtype} "
+                             f"{tuple(like[i].shape)}")
+        dtypes[i], sizes[i], where[i] = dt, t.numel(), t.data_ptr()
+    return dev, dtypes, sizes, where
+
+
+def _sumsq(dev, n, dtypes, sizes, where):
+    lib, bytes_ = load_library(), ctypes.c_int64()
+    _check(lib.sc_grad_sumsq_workspace(n, dtypes, sizes, ctypes.byref(bytes_)))
+    ws = torch.empty(bytes_.value, dtype=torch.uint8, device=dev)
+    sumsq = torch.empty((), dtype=torch.float64, device=dev)
+    _run(dev, lib.sc_grad_sumsq, n, dtypes, sizes, where, sumsq.data_ptr(), ws.data_ptr(), bytes_.value)
+    return sumsq
+
+
+def grad_sumsq(grads) -> "torch.Tensor":
+    """The sum of squares (float64, 0-dim) of a list of float32 or bfloat16 tensors of any shapes, in a
+    fixed order.  Where gradients are sharded, the ranks' sums added up go to clip_grads."""
+    grads = list(grads)
+    if not grads:
+        raise ValueError("grad_sumsq: no tensors")
+    dev, *table = _grad_table("grad_sumsq", grads)
+    return _sumsq(dev, len(grads), *table)
+
+
+def clip_grads(grads, max_norm: float, out=None, sumsq: "torch.Tensor" = None) -> GradNorm:
+    """Gradients scaled to a global norm of at most max_norm: norm = sqrt(sum of all squares),
+    scale = min(1, max_norm / (norm + 1e-6)), in place or into the tensors of out.  sumsq: the sum of
+    squares where it is known already (grad_sumsq, added over the ranks)."""
+    grads = list(grads)
+    if not grads:
+        raise ValueError("clip_grads: no tensors")
+    dev, dtypes, sizes, where = _grad_table("clip_grads", grads)
+    to, where_to = grads, where
+    if out is not None:
+        to = list(out)
+        where_to = _grad_table("clip_grads", to, like=grads)[3]
+    if sumsq is None:
+        sumsq = _sumsq(dev, len(grads), dtypes, sizes, where)
+    else:
+        _train_check("clip_grads", torch.float32, dev, ("sumsq", sumsq, torch.float64, ()))
+    norm, scale = torch.empty(2, dtype=torch.float32, device=dev).unbind()
+    _run(dev, load_library().sc_clip_grads, len(grads), dtypes, sizes, where, where_to, sumsq.data_ptr(),
+         float(max_norm), norm.data_ptr(), scale.data_ptr())
+    return GradNorm(norm, scale, to)

@@ -13,8 +13,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libscopt.so")
 
-SOURCES = ["act.hip", "api.cpp", "cholesky.hip", "elementwise.hip", "embed.hip", "gemm.hip", "jacobi.hip",
-           "mask.hip", "quad.hip", "tile_product.hip", "train_api.cpp", "xent.hip"]
+SOURCES = ["act.hip", "api.cpp", "cholesky.hip", "clip.hip", "elementwise.hip", "embed.hip", "gemm.hip", "jacobi.hip",
+           "layernorm.hip", "mask.hip", "quad.hip", "tile_product.hip", "token_loss.hip", "train_api.cpp", "xent.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -1,0 +1,210 @@
+// The global gradient norm over many tensors, and clipping by it:
+//
+//   sumsq = sum of g^2 over all elements,  norm = sqrt(sumsq),  scale = min(1, max_norm / (norm + 1e-6)),
+//   out = g scale
+//
+// Two passes, each bound by HBM.  The tensors' addresses come with the launch (kernel arguments, so the calls
+// can be captured and hold nothing between them); a workgroup finds its tensor by the number of
+// chunks before it.  Squares are summed in 64 bits: those of float32's largest and smallest gradients
+// are out of its own range.
+#include "common.hpp"
+#include "internal.hpp"
+#include "rows.hpp"
+#include "train.hpp"
+
+namespace scopt {
+
+constexpr int kClipThreads = 256, kClipGroups = 4;
+constexpr int64_t kClipChunk = (int64_t)kClipThreads * kClipGroups * 8;  // elements of a chunk
+constexpr int kClipTensors = 128;
+constexpr int kSumsqGrid = 2048;
+
+struct ClipTable {
+    const void* src[kClipTensors];
+    void* dst[kClipTensors];
+    int64_t size[kClipTensors];
+    uint32_t first[kClipTensors + 1];  // chunks before each tensor
+    int count;
+};
+
+// tensor of a chunk: the last one that begins at or before it
+__device__ __forceinline__ int clip_find(const ClipTable& t, uint32_t chunk) {
+    int lo = 0, hi = t.count;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (t.first[mid] <= chunk) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// eight elements at p, `left` of them inside the tensor
+template <typename E> __device__ __forceinline__ void clip_load(const E* p, int64_t left, float (&v)[8]) {
+    if (left >= 8) {
+        Group8<E, ROW_WHOLE> g;
+        g.load(p, 0, 8);
+        g.raw(v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < left ? Elem<E>::load(p, i) : 0.0f;
+    }
+}
+
+template <typename E>
+__global__ __launch_bounds__(kClipThreads) void sumsq_kernel(const ClipTable t, double* __restrict__ part) {
+    __shared__ double red[kClipThreads / 64];
+    double s = 0.0;
+    const uint32_t chunks = t.first[t.count];
+    for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+        const int i = clip_find(t, c);
+        const int64_t at = (int64_t)(c - t.first[i]) * kClipChunk;
+        const E* p = (const E*)t.src[i] + at;
+        const int64_t left = t.size[i] - at;
+        float v[kClipGroups][8];
+#pragma unroll
+        for (int k = 0; k < kClipGroups; ++k) {
+            const int o = (k * kClipThreads + (int)threadIdx.x) * 8;
+            clip_load(p + o, left - o, v[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < kClipGroups; ++k)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s = fma((double)v[k][j], (double)v[k][j], s);
+    }
+    s = block_sum_f64(s, red);
+    if (threadIdx.x == 0) gst(part + blockIdx.x, s);
+}
+
+__global__ __launch_bounds__(1024) void sumsq_join_kernel(const double* __restrict__ part, int parts,
+                                                          double* __restrict__ sumsq) {
+    __shared__ double red[16];
+    double s = 0.0;
+    for (int i = threadIdx.x; i < parts; i += 1024) s += gld(part + i);
+    s = block_sum_f64(s, red);
+    if (threadIdx.x == 0) gst(sumsq, s);
+}
+
+template <typename E>
+__global__ __launch_bounds__(kClipThreads) void clip_kernel(const ClipTable t, const double* __restrict__ sumsq,
+                                                            float max_norm, float* norm, float* scale_out) {
+    const double n = sqrt(gld(sumsq));
+    const double want = (double)max_norm / (n + 1e-6);
+    const float scale = want < 1.0 || want != want ? (float)want : 1.0f;
+    if (norm && blockIdx.x == 0 && threadIdx.x == 0) {
+        gst(norm, (float)n);
+        gst(scale_out, scale);
+    }
+    const uint32_t c = blockIdx.x;
+    if (c >= t.first[t.count]) return;
+    const int i = clip_find(t, c);
+    const int64_t at = (int64_t)(c - t.first[i]) * kClipChunk;
+    const E* p = (const E*)t.src[i] + at;
+    E* o = (E*)t.dst[i] + at;
+    if (p == o && scale == 1.0f) return;
+    const int64_t left = t.size[i] - at;
+    float v[kClipGroups][8];
+#pragma unroll
+    for (int k = 0; k < kClipGroups; ++k) {
+        const int e = (k * kClipThreads + (int)threadIdx.x) * 8;
+        clip_load(p + e, left - e, v[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kClipGroups; ++k) {
+        const int e = (k * kClipThreads + (int)threadIdx.x) * 8;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[k][j] *= scale;
+        store8(o + e, left - e < 8 ? (int)(left - e < 0 ? 0 : left - e) : 8, v[k]);
+    }
+}
+
+namespace {
+int64_t chunks_of(int64_t size) { return (size + kClipChunk - 1) / kClipChunk; }
+// calls f(table) for tables of one type's tensors that are not empty; most: chunks of a table
+template <typename F>
+hipError_t each_table(const GradTensors& g, bool bf16, F f) {
+    constexpr int64_t most = (int64_t)1 << 24;  // a launch holds fewer than 2^32 threads
+    ClipTable t;
+    t.count = 0;
+    t.first[0] = 0;
+    auto flush = [&]() {
+        const hipError_t e = t.count ? f(t) : hipSuccess;
+        t.count = 0;
+        return e;
+    };
+    for (int i = 0; i < g.n; ++i) {
+        if ((g.dtypes[i] == SC_BF16) != bf16) continue;
+        const int64_t bytes = bf16 ? 2 : 4;
+        for (int64_t at = 0; at < g.sizes[i];) {  // a tensor of more chunks than a table holds goes in parts
+            int64_t size = g.sizes[i] - at;
+            const int64_t room = (most - 1 - t.first[t.count]) * kClipChunk;
+            if (room <= 0 || t.count == kClipTensors) {
+                const hipError_t e = flush();
+                if (e != hipSuccess) return e;
+                continue;
+            }
+            if (size > room) size = room;
+            t.src[t.count] = g.src ? (const char*)g.src[i] + at * bytes : nullptr;
+            t.dst[t.count] = g.dst ? (char*)g.dst[i] + at * bytes : nullptr;
+            t.size[t.count] = size;
+            t.first[t.count + 1] = t.first[t.count] + (uint32_t)chunks_of(size);
+            ++t.count;
+            at += size;
+        }
+    }
+    return flush();
+}
+int sumsq_grid(const ClipTable& t) {
+    const uint32_t chunks = t.first[t.count];
+    return (int)(chunks < (uint32_t)kSumsqGrid ? chunks : (uint32_t)kSumsqGrid);
+}
+}  // namespace
+
+int64_t grad_sumsq_parts(const GradTensors& g) {
+    int64_t parts = 0;
+    for (int b = 0; b < 2; ++b)
+        (void)each_table(g, b, [&](const ClipTable& t) {
+            parts += sumsq_grid(t);
+            return hipSuccess;
+        });
+    return parts;
+}
+
+hipError_t launch_grad_sumsq(const GradTensors& g, double* sumsq, double* part, hipStream_t st) {
+    int64_t parts = 0;
+    for (int b = 0; b < 2; ++b) {
+        const hipError_t e = each_table(g, b, [&](const ClipTable& t) {
+            const int grid = sumsq_grid(t);
+            if (b) hipLaunchKernelGGL(sumsq_kernel<uint16_t>, dim3(grid), dim3(kClipThreads), 0, st, t, part + parts);
+            else hipLaunchKernelGGL(sumsq_kernel<float>, dim3(grid), dim3(kClipThreads), 0, st, t, part + parts);
+            parts += grid;
+            return hipGetLastError();
+        });
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL(sumsq_join_kernel, dim3(1), dim3(1024), 0, st, part, (int)parts, sumsq);
+    return hipGetLastError();
+}
+
+hipError_t launch_clip(const GradTensors& g, const double* sumsq, float max_norm, float* norm, float* scale,
+                       hipStream_t st) {
+    bool told = false;
+    for (int b = 0; b < 2; ++b) {
+        const hipError_t e = each_table(g, b, [&](const ClipTable& t) {
+            const dim3 grid(t.first[t.count]);
+            float* to = told ? nullptr : norm;
+            told = true;
+            if (b) hipLaunchKernelGGL(clip_kernel<uint16_t>, grid, dim3(kClipThreads), 0, st, t, sumsq, max_norm, to, scale);
+            else hipLaunchKernelGGL(clip_kernel<float>, grid, dim3(kClipThreads), 0, st, t, sumsq, max_norm, to, scale);
+            return hipGetLastError();
+        });
+        if (e != hipSuccess) return e;
+    }
+    if (told) return hipSuccess;
+    ClipTable none;  // no element at all: the norm is still told
+    none.count = 0;
+    none.first[0] = 0;
+    hipLaunchKernelGGL(clip_kernel<float>, dim3(1), dim3(kClipThreads), 0, st, none, sumsq, max_norm, norm, scale);
+    return hipGetLastError();
+}
+
+}  // namespace scopt

@@ -23,13 +23,14 @@ __device__ __forceinline__ float tp_gain(const TpArgs& P, int n) {
 // acc: an earlier sum that is added (NULL: none); out_acc: the sum is kept there in float32
 // instead of being stored.
 __global__ __launch_bounds__(256) void tp_reduce_kernel(const TpArgs P, const float* acc, float* out_acc) {
-    const int64_t groups = (int64_t)P.M * ((P.N + 3) / 4);
+    const int M = P.live_rows ? min(P.M, gld(P.live)) : P.M;
+    const int64_t groups = (int64_t)M * ((P.N + 3) / 4);
     const float alpha = P.alpha ? gld(P.alpha) : 1.0f;
     for (int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x; g < groups; g += (int64_t)gridDim.x * 256) {
         const int64_t m = g / ((P.N + 3) / 4);
         const int n = (int)(g - m * ((P.N + 3) / 4)) * 4;
         const int left = P.N - n;
-        const int64_t at = m * P.N + n, stride = (int64_t)P.M * P.N;
+        const int64_t at = m * P.N + n, stride = (int64_t)M * P.N;
         float v[4] = {0.f, 0.f, 0.f, 0.f};
         if (left >= 4) {
             if (acc) {
@@ -55,7 +56,7 @@ __global__ __launch_bounds__(256) void tp_reduce_kernel(const TpArgs P, const fl
         } else {
 #pragma unroll
             for (int r = 0; r < 4; ++r) v[r] *= alpha * tp_gain(P, min(n + r, P.N - 1));
-            tp_store(P.C, P.c_bf16, m * P.ldc + n, v, left);
+            tp_store(P.C, P.c_bf16, tp_row(P, (int)m) * P.ldc + n, v, left);
         }
     }
 }
@@ -140,6 +141,7 @@ hipError_t launch_tile_product(TpKind kind, const TpPlan& plan, TpArgs P, const 
     P.tiles_m = plan.tiles_m;
     P.tiles_n = plan.tiles_n;
     P.splits = plan.splits;
+    P.live_rows = P.live && kind == TPK_STATES;
     const bool part = (kind == TPK_STATES || kind == TPK_WEIGHTS) && (plan.splits > 1 || sum.acc || sum.out_acc);
     hipError_t e = plan.shape == 0   ? launch_shape<Big>(kind, P, part, st)
                    : plan.shape == 1 ? launch_shape<Mid>(kind, P, part, st)
@@ -186,11 +188,13 @@ __device__ __forceinline__ Split8 split8_any(const float (&f)[8]) {
     return Split8{__builtin_bit_cast(v8bf, h), __builtin_bit_cast(v8bf, m), __builtin_bit_cast(v8bf, l)};
 }
 
-// planes[p][r][c]: kGroups groups of eight columns a thread (ld is a multiple of 8)
+// planes[p][r][c]: kGroups groups of eight columns a thread (ld is a multiple of 8).  With `place` row r
+// goes to row place[r]; where that is negative its row of `cleared` is set to zeros instead.
 template <typename E, int ENDS>
 __global__ __launch_bounds__(256) void to_planes_kernel(const E* __restrict__ src, int64_t rows, int cols,
                                                         uint16_t* __restrict__ dst, int64_t ld, int64_t plane,
-                                                        const int64_t* __restrict__ targets, int64_t vocab) {
+                                                        const int64_t* __restrict__ targets, int64_t vocab,
+                                                        const int* __restrict__ place, E* __restrict__ cleared) {
     const int per_row = (int)(ld / 8);
     const int64_t n = rows * per_row;
     const bool small = n < (int64_t)1 << 31;
@@ -198,18 +202,25 @@ __global__ __launch_bounds__(256) void to_planes_kernel(const E* __restrict__ sr
          g0 += (int64_t)gridDim.x * 256 * kGroups) {
         Group8<E, ENDS> w[kGroups];
         int64_t r[kGroups], tgt[kGroups];
-        int in[kGroups];
+        int in[kGroups], at[kGroups];
 #pragma unroll
         for (int k = 0; k < kGroups; ++k) {
             const int64_t g = g0 + k * 256;
             split_group(g < n ? g : n - 1, per_row, small, r[k], in[k]);
             w[k].load(src + r[k] * cols, in[k] * 8, cols);
             tgt[k] = targets ? gld(targets + r[k]) : 0;
+            at[k] = place ? gld(place + r[k]) : 0;
         }
 #pragma unroll
         for (int k = 0; k < kGroups; ++k) {
             if (g0 + k * 256 >= n) break;
-            uint16_t* o = dst + r[k] * ld + in[k] * 8;
+            if (at[k] < 0) {
+                const int c = in[k] * 8;
+                const float none[8] = {};
+                if (cleared && c < cols) store8(cleared + r[k] * cols + c, cols - c, none);
+                continue;
+            }
+            uint16_t* o = dst + (place ? at[k] : r[k]) * ld + in[k] * 8;
             const bool live = tgt[k] >= 0 && tgt[k] < vocab;
             float f[8];
             value8(w[k], in[k] * 8, cols, f);
@@ -228,7 +239,8 @@ __global__ __launch_bounds__(256) void to_planes_kernel(const E* __restrict__ sr
 }
 
 hipError_t launch_to_planes(bool bf16, const void* src, int64_t rows, int64_t cols, uint16_t* dst, int64_t ld,
-                            int64_t plane, const int64_t* targets, int64_t vocab, hipStream_t st) {
+                            int64_t plane, const int64_t* targets, int64_t vocab, hipStream_t st, const int* place,
+                            void* cleared) {
     const int64_t n = rows * (ld / 8);
     if (n <= 0) return hipSuccess;
     if (!targets) vocab = 1;  // every row counts
@@ -236,7 +248,7 @@ hipError_t launch_to_planes(bool bf16, const void* src, int64_t rows, int64_t co
     const dim3 grid((unsigned)(blocks < 65536 ? blocks : 65536));
 #define SC_PLANES(E_, ENDS_)                                                                                         \
     hipLaunchKernelGGL((to_planes_kernel<E_, ENDS_>), grid, dim3(256), 0, st, (const E_*)src, rows, (int)cols, dst, \
-                       ld, plane, targets, vocab);
+                       ld, plane, targets, vocab, place, (E_*)cleared);
     SC_BY_ENDS(bf16, cols, SC_PLANES)
 #undef SC_PLANES
     return hipGetLastError();

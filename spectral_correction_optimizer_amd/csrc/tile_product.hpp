@@ -232,6 +232,8 @@ __device__ __forceinline__ int64_t tp_target(const int64_t* targets, int64_t voc
     const int64_t t = gld(targets + m);
     return t >= 0 && t < vocab ? t : -1;
 }
+// the row of C that holds row m of the product
+__device__ __forceinline__ int64_t tp_row(const TpArgs& P, int m) { return P.rows ? gld(P.rows + m) : m; }
 constexpr float kLog2e = 1.44269504088896340736f;
 // The reference of a tile's exponentials.  TP_KEEP_EXP: the row maximum in powers of two,
 // rounded up; otherwise the maximum itself.  A tile whose row is all -infinity takes 0, so
@@ -317,10 +319,22 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
 
     v4f acc[MI][NI];
 
+    // Tokens are the rows of A where it has k contiguous, else k; only the first of them may be live.
+    int M = P.M, K = P.K, tiles_m = P.tiles_m;
+    if (P.live) {
+        const int live = __builtin_amdgcn_readfirstlane(gld(P.live));
+        if constexpr (AKC) {
+            M = min(M, live);
+            tiles_m = (M + BM - 1) / BM;
+            if (M == 0) return;
+        } else {
+            K = min(K, live);
+        }
+    }
     // k goes in turns of the buffers; what lies past its end multiplies zeros.
-    const int kturns = (P.K + 64 * NBUF - 1) / (64 * NBUF), total = kturns * P.nseg;
+    const int kturns = max(1, (K + 64 * NBUF - 1) / (64 * NBUF)), total = kturns * P.nseg;
     const int per = (total + P.splits - 1) / P.splits;
-    const int tiles = P.tiles_m * P.tiles_n, all = tiles * P.splits;
+    const int tiles = tiles_m * P.tiles_n, all = tiles * P.splits;
 
     // the turn that is fetched next: its tile, segment and place in the segment
     struct Ahead {
@@ -330,7 +344,7 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
         const int id = turn < all ? xcd_remap(turn, all) : 0;
         const int split = id / tiles;
         int tm, tn;
-        tp_tile(id - split * tiles, P.tiles_m, P.tiles_n, tm, tn);
+        tp_tile(id - split * tiles, tiles_m, P.tiles_n, tm, tn);
         ah.m0 = tm * BM;
         ah.n0 = tn * BN;
         const int at = split * per;
@@ -342,8 +356,8 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
         const bool live = ah.left > 0;
         const uint32_t planes = live ? (uint32_t)(P.segs >> (4 * ah.seg)) : 0;
         const int k0 = ah.kt * 64 * NBUF;
-        la.prepare(P.A + (planes & 3) * P.a_plane, P.lda, P.M, P.K, ah.m0, k0, live);
-        lb.prepare(P.B + ((planes >> 2) & 3) * P.b_plane, P.ldb, P.N, P.K, ah.n0, k0, live);
+        la.prepare(P.A + (planes & 3) * P.a_plane, P.lda, M, K, ah.m0, k0, live);
+        lb.prepare(P.B + ((planes >> 2) & 3) * P.b_plane, P.ldb, P.N, K, ah.n0, k0, live);
         --ah.left;
         const bool wrap = ++ah.kt == kturns;
         ah.kt = wrap ? 0 : ah.kt;
@@ -412,7 +426,7 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
     for (int turn = blockIdx.x; turn < all; turn += gridDim.x) {
         const int id = xcd_remap(turn, all), split = id / tiles;
         int tm, tn;
-        tp_tile(id - split * tiles, P.tiles_m, P.tiles_n, tm, tn);
+        tp_tile(id - split * tiles, tiles_m, P.tiles_n, tm, tn);
         const int m0 = tm * BM, n0 = tn * BN;
         // (TP_STATS: a column past the last one starts at -infinity and, its operand being zero, stays)
 #pragma unroll
@@ -465,7 +479,7 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
         int lane = threadIdx.x & 63;
         asm volatile("" : "+v"(lane));
         const int lm = m0 + wm + (lane & 15), ln = n0 + wn + 4 * (lane >> 4);
-        const int M = P.M, N = P.N;
+        const int N = P.N;
         const bool whole = n0 + BN <= N;  // all columns of the tile exist
         if constexpr (EPI == TP_STORE) {
             const float alpha = P.alpha ? gld(P.alpha) : 1.0f;
@@ -498,7 +512,7 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
                             d[j][w] = pack_bf16x2(acc[i][j][2 * w] * g[j][2 * w],
                                                   acc[i][j][2 * w + 1] * g[j][2 * w + 1]);
                     const int c = tp_gather_row<NI>(d);
-                    if (m < M) tp_store_row<NI>((uint16_t*)P.C + (int64_t)m * P.ldc + n0 + wn + c, d);
+                    if (m < M) tp_store_row<NI>((uint16_t*)P.C + tp_row(P, m) * P.ldc + n0 + wn + c, d);
                 }
             } else {
                 auto store = [&](auto bf16) SC_INLINE {
@@ -511,7 +525,7 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
                             float v[4];
 #pragma unroll
                             for (int r = 0; r < 4; ++r) v[r] = acc[i][j][r] * g[j][r];
-                            if (m < M) tp_store(P.C, decltype(bf16)::value, (int64_t)m * P.ldc + n, v, N - n);
+                            if (m < M) tp_store(P.C, decltype(bf16)::value, tp_row(P, m) * P.ldc + n, v, N - n);
                         }
                     }
                 };
@@ -600,7 +614,7 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
                 z += __shfl_xor(z, 32);
                 if (lane < 16) sums[(wave % S::WVN) * BM + wm + 16 * i + lane] = z;
                 if (wave % S::WVN == 0 && lane < 16 && m < M)
-                    gst(P.stat_max + (int64_t)(P.stat_first + tn) * M + m,
+                    gst(P.stat_max + (int64_t)(P.stat_first + tn) * P.M + m,
                         mx == -__builtin_huge_valf() ? mx : ref);
             }
             tp_lds_barrier();
@@ -608,16 +622,17 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
                 float z = sums[r];
 #pragma unroll
                 for (int w = 1; w < S::WVN; ++w) z += sums[w * BM + r];
-                if (m0 + r < M) gst(P.stat_sum + (int64_t)(P.stat_first + tn) * M + m0 + r, z);
+                if (m0 + r < M) gst(P.stat_sum + (int64_t)(P.stat_first + tn) * P.M + m0 + r, z);
             }
         } else {
-            const float alpha = gld(P.alpha);
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
                 const int m = lm + 16 * i;
                 row_block(i);
                 if (m >= M) continue;
-                const int64_t tgt = tp_target(P.targets, P.vocab, m);
+                const float alpha = gld(P.coef ? P.coef + m : P.alpha);
+                // a row without weight is one of zeros, whatever its logits are
+                const int64_t tgt = alpha != 0.0f ? tp_target(P.targets, P.vocab, m) : -1;
                 const float lse = gld(P.lse + m);
 #pragma unroll
                 for (int j = 0; j < NI; ++j) {

@@ -1,9 +1,12 @@
 // Training-step operators of libscopt: arguments and launchers shared by their kernels
-// (tile_product.hip, xent.hip, act.hip, embed.hip) and their C entries (train_api.cpp).
+// (tile_product.hip, xent.hip, token_loss.hip, act.hip, layernorm.hip, clip.hip, embed.hip) and
+// their C entries (train_api.cpp).
 #pragma once
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include "scopt.h"
 
 namespace scopt {
 
@@ -50,6 +53,12 @@ struct TpArgs {
     float* stat_sum = nullptr;
     int64_t stat_first = 0;
     const float* lse = nullptr;
+    const float* coef = nullptr;  // TP_GRAD: a factor of each row's values, in place of alpha
+    // Only the first *live tokens exist (NULL: all).  Tokens are the rows of the logits and of the
+    // states' gradients, and k of the weights'.
+    const int* live = nullptr;
+    int live_rows = 0;          // set by the launch: live counts the rows of C
+    const int* rows = nullptr;  // TP_STORE, reduction: row m is stored as row rows[m] (NULL: m)
 };
 
 // The product's operand layouts and what is done with its sums.
@@ -84,11 +93,14 @@ hipError_t launch_tile_product(TpKind kind, const TpPlan& plan, TpArgs args, con
 hipError_t launch_zero(void* p, int64_t bytes, hipStream_t st);
 
 // planes[p][r][c] of a float32 (three planes) or bfloat16 (one plane) matrix, zero in the
-// columns from `cols` to ld and, with targets, in the rows whose target is not in [0, vocab)
+// columns from `cols` to ld and, with targets, in the rows whose target is not in [0, vocab).  With
+// `place` row r goes to row place[r], and one with a negative place clears its row of `cleared`
+// ([rows][cols] of src's type, or NULL) instead.
 hipError_t launch_to_planes(bool bf16, const void* src, int64_t rows, int64_t cols, uint16_t* dst, int64_t ld,
-                            int64_t plane, const int64_t* targets, int64_t vocab, hipStream_t st);
+                            int64_t plane, const int64_t* targets, int64_t vocab, hipStream_t st,
+                            const int* place = nullptr, void* cleared = nullptr);
 
-// ---- cross entropy (xent.hip) --------------------------------------------------------
+// ---- losses over a large vocabulary (xent.hip, token_loss.hip) -------------------------
 struct XentPlan {
     bool bf16, planes;         // planes: W is copied into planes (float32, or H % 8), as h always is
     int64_t T, V, H, Hp, Hh;   // columns of W's operand (H, or padded when planes) and of h's
@@ -101,10 +113,65 @@ struct XentPlan {
     // offsets into the workspace
     int64_t o_factors, o_h, o_w, o_s, o_p, o_tl, o_lse, o_smax, o_ssum, o_part, o_dh, bytes;
 };
-// limit: bytes that the kept probabilities (or a piece's) may take
-XentPlan xent_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit);
+// limit: bytes that the kept probabilities (or a piece's) may take; gradients = false: only the logits'
+// statistics are taken, and there is room for nothing else
+XentPlan xent_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit, bool gradients = true);
+
+// One call's buffers, and the steps that the losses share.  Without `rows` the rows of h are the tokens; with
+// them only the counted ones, in order: row c is token rows[c], *live of them exist, and `targets`, lse
+// and coef go by c.
+struct XentRun {
+    const XentPlan* p = nullptr;
+    const void *h = nullptr, *W = nullptr;
+    const int64_t* targets = nullptr;
+    char* ws = nullptr;
+    const int *live = nullptr, *rows = nullptr, *place = nullptr;  // place[t]: token t's row, or -1
+    // the logit gradients are (softmax - onehot) times coef[row], or times factors[1] without coef; the
+    // stores of dh and dW multiply by factors[0]
+    const float* coef = nullptr;
+    hipStream_t st = nullptr;
+
+    template <typename E> E* at(int64_t offset) const { return (E*)(ws + offset); }
+    // h and, where it needs planes, W as operands.  dh: its rows of tokens that are not counted are cleared
+    // (with rows; else NULL)
+    hipError_t operands(void* dh) const;
+    hipError_t logits() const;                       // row statistics, and what is kept
+    hipError_t log_sums(float* loss, float* logp) const;  // lse; the tokens' losses, or with rows their negative
+    hipError_t gradients(void* dh, void* dW) const;
+
+private:
+    TpArgs logit_args(int piece) const;
+    const uint16_t* w_operand() const { return p->planes ? at<uint16_t>(p->o_w) : (const uint16_t*)W; }
+    uint64_t segments() const;
+};
 hipError_t launch_xent(const XentPlan& p, const void* h, const void* W, const int64_t* targets, float* loss,
                        float* mean, void* dh, void* dW, void* workspace, hipStream_t st);
+
+struct TokenLossPlan {
+    XentPlan x;
+    int64_t o_live, o_rows, o_place, o_targets, o_coef, bytes;
+};
+TokenLossPlan token_loss_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit, bool gradients);
+hipError_t launch_token_logp(const TokenLossPlan& p, const void* h, const void* W, const int64_t* targets,
+                             float* logp, void* workspace, hipStream_t st);
+struct PolicyArgs {
+    const float *old_logp, *advantages, *ref_logp, *weights;  // [T]; ref_logp, weights or NULL
+    double lo, hi;                                            // the ratio is clipped to [lo, hi]
+    float kl;
+    float *loss, *total, *kl_mean, *clipped, *logp;
+};
+hipError_t launch_policy_loss(const TokenLossPlan& p, const void* h, const void* W, const int64_t* targets,
+                              const PolicyArgs& a, void* dh, void* dW, void* workspace, hipStream_t st);
+struct PreferenceArgs {
+    const int64_t* starts;  // [2 pairs + 1]
+    const float* ref_logp;  // [T] or NULL
+    int64_t pairs;
+    float beta, margin, smoothing;
+    int average;
+    float *loss, *mean, *rewards, *logp;
+};
+hipError_t launch_preference_loss(const TokenLossPlan& p, const void* h, const void* W, const int64_t* targets,
+                                  const PreferenceArgs& a, void* dh, void* dW, void* workspace, hipStream_t st);
 
 // ---- 8-bit activation checkpoints and the residual norm (act.hip) ----------------------
 hipError_t launch_act_pack(bool bf16, const void* x, int64_t T, int H, int8_t* q, uint8_t* e, hipStream_t st);
@@ -116,6 +183,28 @@ int64_t rmsnorm_grad_parts(int64_t T, int H);
 hipError_t launch_rmsnorm_grad(bool bf16, const void* dy, const void* gain, const float* rstd, const int8_t* q,
                                const uint8_t* e, const void* dh, int64_t T, int H, void* dx, float* dgain,
                                float* partial, hipStream_t st);
+
+// ---- layer norm (layernorm.hip) ----------------------------------------------------------
+hipError_t launch_layernorm(bool bf16, const void* x, const void* residual, const void* gain, const void* bias,
+                            float eps, int64_t T, int H, void* h, void* y, float* mean, float* rstd, int8_t* q,
+                            uint8_t* e, hipStream_t st);
+int64_t layernorm_grad_parts(int64_t T, int H);  // rows of 2 H float32 of `partial`
+hipError_t launch_layernorm_grad(bool bf16, const void* dy, const void* gain, const float* rstd, const float* mean,
+                                 const int8_t* q, const uint8_t* e, const void* h, const void* dh, int64_t T, int H,
+                                 void* dx, float* dgain, float* dbias, float* partial, hipStream_t st);
+
+// ---- global gradient norm (clip.hip) -----------------------------------------------------
+struct GradTensors {  // host arrays
+    int n;
+    const sc_dtype* dtypes;
+    const int64_t* sizes;
+    const void* const* src;
+    void* const* dst;  // NULL where only the norm is taken
+};
+int64_t grad_sumsq_parts(const GradTensors& g);  // float64 partial sums
+hipError_t launch_grad_sumsq(const GradTensors& g, double* sumsq, double* part, hipStream_t st);
+hipError_t launch_clip(const GradTensors& g, const double* sumsq, float max_norm, float* norm, float* scale,
+                       hipStream_t st);
 
 struct WgradPlan {
     bool bf16, planes;  // planes: dy is copied into planes (float32, or N % 8)

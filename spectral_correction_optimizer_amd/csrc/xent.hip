@@ -41,18 +41,23 @@ constexpr int64_t kAlign = 256;
 int64_t up(int64_t n, int64_t a) { return (n + a - 1) / a * a; }
 }  // namespace
 
-// 64 tokens a workgroup, one a lane, the tiles dealt to 16 wavefronts: a row's log-sum-exp from
+// 64 rows a workgroup, one a lane, the tiles dealt to 16 wavefronts: a row's log-sum-exp from
 // its tiles' references and sums [tile][T], and its loss.  pow2: the references are powers of
 // two.  A row of -infinity only has no finite log-sum-exp; like a row with NaN or +infinity
-// it gives NaN.
+// it gives NaN.  With `rows` the first *live rows are counted tokens, and logp[rows[row]] is the target's
+// log-probability.
 __global__ __launch_bounds__(1024) void xent_lse_kernel(const float* __restrict__ smax,
                                                         const float* __restrict__ ssum, int tiles, int pow2,
                                                         const float* __restrict__ target_logit,
                                                         const int64_t* __restrict__ targets, int64_t T, int64_t V,
-                                                        float* __restrict__ lse, float* __restrict__ loss) {
+                                                        float* __restrict__ lse, float* __restrict__ loss,
+                                                        const int* __restrict__ live, const int* __restrict__ rows,
+                                                        float* __restrict__ logp) {
     __shared__ float red[16][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t t = (int64_t)blockIdx.x * 64 + lane, at = t < T ? t : T - 1;
+    const int64_t end = rows ? gld(live) : T;
+    if ((int64_t)blockIdx.x * 64 >= end) return;
+    const int64_t t = (int64_t)blockIdx.x * 64 + lane, at = t < end ? t : end - 1;
     const float none = -__builtin_huge_valf();
     // a difference of references as a factor; a tile of -infinity has sum 0 (or NaN)
     auto scaled = [&](float s, float r, float to) {
@@ -86,16 +91,17 @@ __global__ __launch_bounds__(1024) void xent_lse_kernel(const float* __restrict_
     __syncthreads();
     red[wave][lane] = z;
     __syncthreads();
-    if (wave > 0 || t >= T) return;
+    if (wave > 0 || t >= end) return;
     z = 0.0f;
 #pragma unroll
     for (int w = 0; w < 16; ++w) z += red[w][lane];
     // a power of two's logarithm in two parts: m * ln2 is off by less than 2^-40 of m
     const float base = pow2 ? m * 0.693145751953125f : m, rest = pow2 ? m * 1.42860682030941723e-6f : 0.0f;
     const float logz = m == none ? __builtin_nanf("") : logf(z) + rest;
-    const bool counted = tp_target(targets, V, t) >= 0;
     gst(lse + t, base + logz);
-    gst(loss + t, counted ? (base - gld(target_logit + t)) + logz : 0.0f);
+    const float off = (base - gld(target_logit + t)) + logz;
+    if (rows) gst(logp + gld(rows + t), -off);
+    else gst(loss + t, tp_target(targets, V, t) >= 0 ? off : 0.0f);
 }
 
 // d from what the logits product kept: exponentials in 16 bits (in place) or float32 logits
@@ -108,10 +114,14 @@ __global__ __launch_bounds__(256) void xent_dlogits_kernel(const float* __restri
                                                            const float* __restrict__ lse,
                                                            const float* __restrict__ target_logit,
                                                            const int64_t* __restrict__ targets, int64_t V,
-                                                           const float* __restrict__ scale_at) {
+                                                           const float* __restrict__ scale_at,
+                                                           const int* __restrict__ live,
+                                                           const float* __restrict__ coef) {
     const int64_t t = blockIdx.x / chunks;
-    const float scale = gld(scale_at);
-    const int64_t tgt = tp_target(targets, V, t);
+    if (live && t >= gld(live)) return;
+    const float scale = gld(coef ? coef + t : scale_at);
+    // a row without weight is one of zeros, whatever its logits are
+    const int64_t tgt = scale != 0.0f ? tp_target(targets, V, t) : -1;
     const float ls = gld(lse + t);
     const float ls2 = ls * kLog2e;
     const float at_target = tgt >= 0 ? (expf(gld(target_logit + t) - ls) - 1.0f) * scale : 0.0f;
@@ -176,7 +186,7 @@ __global__ __launch_bounds__(1024) void xent_mean_kernel(const float* __restrict
     }
 }
 
-XentPlan xent_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit) {
+XentPlan xent_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit, bool gradients) {
     XentPlan p{};
     p.bf16 = bf16;
     p.T = T;
@@ -188,9 +198,9 @@ XentPlan xent_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit) {
     const int nseg = bf16 ? 1 : 6;
     // bytes of a vocabulary column: the kept exponentials, or the logits and d's planes
     const int64_t col_kept = T * (bf16 ? 2 : 10), col_piece = T * (bf16 ? 2 : 6);
-    p.keep = up(V, 256) * col_kept <= limit;
+    p.keep = gradients && up(V, 256) * col_kept <= limit;
     p.piece = V;
-    if (!p.keep) {
+    if (gradients && !p.keep) {
         p.piece = limit / col_piece / 256 * 256;
         if (p.piece < 256) p.piece = 256;
         if (p.piece > V) p.piece = V;
@@ -200,9 +210,11 @@ XentPlan xent_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit) {
     const int64_t last = V - (int64_t)(p.pieces - 1) * p.piece;
     p.logits = tp_plan((int)T, (int)p.piece, (int)H, nseg, false);
     p.logits_last = tp_plan((int)T, (int)last, (int)H, nseg, false);
-    p.dh = tp_plan((int)T, (int)H, (int)p.piece, nseg, true);
-    p.dw = tp_plan((int)p.piece, (int)H, (int)T, nseg, true);
-    p.dw_last = tp_plan((int)last, (int)H, (int)T, nseg, true);
+    if (gradients) {
+        p.dh = tp_plan((int)T, (int)H, (int)p.piece, nseg, true);
+        p.dw = tp_plan((int)p.piece, (int)H, (int)T, nseg, true);
+        p.dw_last = tp_plan((int)last, (int)H, (int)T, nseg, true);
+    }
     p.stat_tiles = (int64_t)(p.pieces - 1) * p.logits.tiles_n + p.logits_last.tiles_n;
     int64_t o = 0;
     auto take = [&](int64_t bytes) {
@@ -215,12 +227,12 @@ XentPlan xent_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit) {
     p.o_h = take(2 * np * T * p.Hh);
     p.o_w = p.planes ? take(2 * np * V * p.Hp) : 0;
     p.o_s = !bf16 && p.keep ? take(4 * T * p.ldp) : 0;
-    p.o_p = take(2 * np * T * p.ldp);
+    p.o_p = gradients ? take(2 * np * T * p.ldp) : 0;
     p.o_tl = take(4 * T);
     p.o_lse = take(4 * T);
     p.o_smax = take(4 * T * p.stat_tiles);
     p.o_ssum = take(4 * T * p.stat_tiles);
-    const bool join = p.pieces > 1;
+    const bool join = gradients && p.pieces > 1;
     int64_t part = p.dh.part_bytes;
     if (join && part == 0) part = 4 * T * H;
     part = part > p.dw.part_bytes ? part : p.dw.part_bytes;
@@ -231,144 +243,166 @@ XentPlan xent_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit) {
     return p;
 }
 
-hipError_t launch_xent(const XentPlan& p, const void* h, const void* W, const int64_t* targets, float* loss,
-                       float* mean, void* dh, void* dW, void* workspace, hipStream_t st) {
-    char* ws = (char*)workspace;
-    const int64_t T = p.T, V = p.V, H = p.H, Hp = p.Hp, Hh = p.Hh;
-    const int np = p.bf16 ? 1 : 3;
-    float* factors = (float*)(ws + p.o_factors);
-    uint16_t* P = (uint16_t*)(ws + p.o_p);
-    float* S = (float*)(ws + p.o_s);
-    float *tl = (float*)(ws + p.o_tl), *lse = (float*)(ws + p.o_lse);
-    float *smax = (float*)(ws + p.o_smax), *ssum = (float*)(ws + p.o_ssum);
-    float *part = (float*)(ws + p.o_part), *dhs = (float*)(ws + p.o_dh);
-    hipError_t e;
-    if (T == 0) {
-        if ((e = launch_zero(mean, 4, st)) != hipSuccess) return e;
-        return launch_zero(dW, V * H * (p.bf16 ? 2 : 4), st);
-    }
-#define SC_RUN(expr) \
-    if ((e = (expr)) != hipSuccess) return e
+#define SC_RUN(expr)                          \
+    do {                                      \
+        const hipError_t e_ = (expr);         \
+        if (e_ != hipSuccess) return e_;      \
+    } while (0)
 
-    // h is always copied, with zeros for the tokens that are not counted: whatever they hold
-    // (a NaN too) reaches no product
-    uint16_t* hp = (uint16_t*)(ws + p.o_h);
-    const uint16_t* wp = (const uint16_t*)W;
-    SC_RUN(launch_to_planes(p.bf16, h, T, H, hp, Hh, T * Hh, targets, V, st));
-    if (p.planes) {
-        wp = (uint16_t*)(ws + p.o_w);
-        SC_RUN(launch_to_planes(p.bf16, W, V, H, (uint16_t*)wp, Hp, V * Hp, nullptr, 0, st));
-    }
-    // planes (A | B << 2) of the six products of two split operands, smallest first
-    const uint64_t segs = p.bf16 ? 0 : 0x0 << 20 | 0x4 << 16 | 0x1 << 12 | 0x8 << 8 | 0x5 << 4 | 0x2;
-    const int nseg = p.bf16 ? 1 : 6;
+hipError_t XentRun::operands(void* dh) const {
+    // h is always copied, without the tokens that are not counted or with zeros for them: whatever
+    // they hold (a NaN too) reaches no product
+    SC_RUN(launch_to_planes(p->bf16, h, p->T, p->H, at<uint16_t>(p->o_h), p->Hh, p->T * p->Hh,
+                            rows ? nullptr : targets, p->V, st, place, dh));
+    if (p->planes)
+        SC_RUN(launch_to_planes(p->bf16, W, p->V, p->H, at<uint16_t>(p->o_w), p->Hp, p->V * p->Hp, nullptr, 0, st));
+    return hipSuccess;
+}
 
-    auto logits = [&](int i) {
-        TpArgs a;
-        const int64_t v0 = (int64_t)i * p.piece;
-        a.A = hp;
-        a.lda = Hh;
-        a.a_plane = T * Hh;
-        a.B = wp + v0 * Hp;
-        a.ldb = Hp;
-        a.b_plane = V * Hp;
-        a.M = (int)T;
-        a.N = (int)(V - v0 < p.piece ? V - v0 : p.piece);
-        a.K = (int)up(H, 8);
-        a.nseg = nseg;
-        a.segs = segs;
-        a.targets = targets;
-        a.vocab = V;
-        a.n_first = v0;
-        a.ldp = p.ldp;
-        a.p_plane = T * p.ldp;
-        a.p_planes = np;
-        a.target_logit = tl;
-        a.stat_max = smax;
-        a.stat_sum = ssum;
-        a.stat_first = (int64_t)i * p.logits.tiles_n;
-        a.lse = lse;
-        return a;
-    };
-    auto logits_plan = [&](int i) -> const TpPlan& { return i + 1 < p.pieces ? p.logits : p.logits_last; };
-    for (int i = 0; i < p.pieces; ++i) {
-        TpArgs a = logits(i);
-        a.keep = !p.keep ? TP_KEEP_NONE : p.bf16 ? TP_KEEP_EXP : TP_KEEP_LOGIT;
-        a.P = p.bf16 ? (void*)P : (void*)S;
-        SC_RUN(launch_tile_product(TPK_LOGIT_STATS, logits_plan(i), a, TpSum{}, st));
-    }
-    const int pow2 = p.keep && p.bf16;
-    hipLaunchKernelGGL(xent_lse_kernel, dim3((unsigned)((T + 63) / 64)), dim3(1024), 0, st, smax, ssum,
-                       (int)p.stat_tiles, pow2, tl, targets, T, V, lse, loss);
-    SC_RUN(hipGetLastError());
-    hipLaunchKernelGGL(xent_mean_kernel, dim3(1), dim3(1024), 0, st, loss, targets, T, V, factors, mean);
-    SC_RUN(hipGetLastError());
+// planes (A | B << 2) of the six products of two split operands, smallest first
+uint64_t XentRun::segments() const { return p->bf16 ? 0 : 0x0 << 20 | 0x4 << 16 | 0x1 << 12 | 0x8 << 8 | 0x5 << 4 | 0x2; }
 
-    for (int i = 0; i < p.pieces; ++i) {
-        const int64_t v0 = (int64_t)i * p.piece;
-        const int n = (int)(V - v0 < p.piece ? V - v0 : p.piece);
-        if (p.keep) {
+TpArgs XentRun::logit_args(int i) const {
+    TpArgs a;
+    const int64_t v0 = (int64_t)i * p->piece;
+    a.A = at<uint16_t>(p->o_h);
+    a.lda = p->Hh;
+    a.a_plane = p->T * p->Hh;
+    a.B = w_operand() + v0 * p->Hp;
+    a.ldb = p->Hp;
+    a.b_plane = p->V * p->Hp;
+    a.M = (int)p->T;
+    a.N = (int)(p->V - v0 < p->piece ? p->V - v0 : p->piece);
+    a.K = (int)up(p->H, 8);
+    a.nseg = p->bf16 ? 1 : 6;
+    a.segs = segments();
+    a.targets = targets;
+    a.vocab = p->V;
+    a.n_first = v0;
+    a.ldp = p->ldp;
+    a.p_plane = p->T * p->ldp;
+    a.p_planes = p->bf16 ? 1 : 3;
+    a.target_logit = at<float>(p->o_tl);
+    a.stat_max = at<float>(p->o_smax);
+    a.stat_sum = at<float>(p->o_ssum);
+    a.stat_first = (int64_t)i * p->logits.tiles_n;
+    a.lse = at<float>(p->o_lse);
+    a.live = live;
+    return a;
+}
+
+hipError_t XentRun::logits() const {
+    for (int i = 0; i < p->pieces; ++i) {
+        TpArgs a = logit_args(i);
+        a.keep = !p->keep ? TP_KEEP_NONE : p->bf16 ? TP_KEEP_EXP : TP_KEEP_LOGIT;
+        a.P = p->bf16 ? at<void>(p->o_p) : at<void>(p->o_s);
+        SC_RUN(launch_tile_product(TPK_LOGIT_STATS, i + 1 < p->pieces ? p->logits : p->logits_last, a, TpSum{}, st));
+    }
+    return hipSuccess;
+}
+
+hipError_t XentRun::log_sums(float* loss, float* logp) const {
+    hipLaunchKernelGGL(xent_lse_kernel, dim3((unsigned)((p->T + 63) / 64)), dim3(1024), 0, st, at<float>(p->o_smax),
+                       at<float>(p->o_ssum), (int)p->stat_tiles, p->keep && p->bf16, at<float>(p->o_tl), targets, p->T,
+                       p->V, at<float>(p->o_lse), loss, live, rows, logp);
+    return hipGetLastError();
+}
+
+hipError_t XentRun::gradients(void* dh, void* dW) const {
+    const int64_t T = p->T, V = p->V, H = p->H;
+    const float* factors = at<float>(p->o_factors);
+    uint16_t* P = at<uint16_t>(p->o_p);
+    float *part = at<float>(p->o_part), *dhs = at<float>(p->o_dh);
+    const int nseg = p->bf16 ? 1 : 6;
+    for (int i = 0; i < p->pieces; ++i) {
+        const int64_t v0 = (int64_t)i * p->piece;
+        const int n = (int)(V - v0 < p->piece ? V - v0 : p->piece);
+        if (p->keep) {
             // enough workgroups for the chip, at least 2048 columns each
             const int64_t chunk = up((n * T + 4095) / 4096, 2048);
             const int chunks = (int)((n + chunk - 1) / chunk);
             const dim3 grid((unsigned)(chunks * T));
-            if (p.bf16)
-                hipLaunchKernelGGL(xent_dlogits_kernel<true>, grid, dim3(256), 0, st, nullptr, P, T * p.ldp, p.ldp, n,
-                                   p.logits.bn, chunk, chunks, smax, T, lse, tl, targets, V, factors + 1);
-            else
-                hipLaunchKernelGGL(xent_dlogits_kernel<false>, grid, dim3(256), 0, st, S, P, T * p.ldp, p.ldp, n,
-                                   p.logits.bn, chunk, chunks, smax, T, lse, tl, targets, V, factors + 1);
+            auto kernel = p->bf16 ? xent_dlogits_kernel<true> : xent_dlogits_kernel<false>;
+            hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, p->bf16 ? nullptr : at<float>(p->o_s), P, T * p->ldp,
+                               p->ldp, n, p->logits.bn, chunk, chunks, at<float>(p->o_smax), T, at<float>(p->o_lse),
+                               at<float>(p->o_tl), targets, V, factors + 1, live, coef);
             SC_RUN(hipGetLastError());
         } else {
-            TpArgs a = logits(i);
+            TpArgs a = logit_args(i);
             a.P = P;
             a.alpha = factors + 1;
-            SC_RUN(launch_tile_product(TPK_LOGIT_GRAD, logits_plan(i), a, TpSum{}, st));
+            a.coef = coef;
+            SC_RUN(launch_tile_product(TPK_LOGIT_GRAD, i + 1 < p->pieces ? p->logits : p->logits_last, a, TpSum{}, st));
         }
         TpArgs a;  // dh (+)= d W: k runs over the piece
         a.A = P;
-        a.lda = p.ldp;
-        a.a_plane = T * p.ldp;
-        a.B = wp + v0 * Hp;
-        a.ldb = Hp;
-        a.b_plane = V * Hp;
+        a.lda = p->ldp;
+        a.a_plane = T * p->ldp;
+        a.B = w_operand() + v0 * p->Hp;
+        a.ldb = p->Hp;
+        a.b_plane = V * p->Hp;
         a.M = (int)T;
         a.N = (int)H;
         a.K = n;
         a.nseg = nseg;
-        a.segs = segs;
+        a.segs = segments();
         a.C = dh;
         a.ldc = H;
-        a.c_bf16 = p.bf16;
+        a.c_bf16 = p->bf16;
         a.alpha = factors;
         a.part = part;
+        a.live = live;
+        a.rows = rows;
         TpSum sum;
-        if (p.pieces > 1) {
+        if (p->pieces > 1) {
             sum.acc = i > 0 ? dhs : nullptr;
-            sum.out_acc = i + 1 < p.pieces ? dhs : nullptr;
+            sum.out_acc = i + 1 < p->pieces ? dhs : nullptr;
         }
-        SC_RUN(launch_tile_product(TPK_STATES, p.dh, a, sum, st));
+        SC_RUN(launch_tile_product(TPK_STATES, p->dh, a, sum, st));
         TpArgs b;  // dW = d^T h: k runs over the tokens
         b.A = P;
-        b.lda = p.ldp;
-        b.a_plane = T * p.ldp;
-        b.B = hp;
-        b.ldb = Hh;
-        b.b_plane = T * Hh;
+        b.lda = p->ldp;
+        b.a_plane = T * p->ldp;
+        b.B = at<uint16_t>(p->o_h);
+        b.ldb = p->Hh;
+        b.b_plane = T * p->Hh;
         b.M = n;
         b.N = (int)H;
         b.K = (int)T;
         b.nseg = nseg;
-        b.segs = segs;
-        b.C = (char*)dW + v0 * H * (p.bf16 ? 2 : 4);
+        b.segs = segments();
+        b.C = (char*)dW + v0 * H * (p->bf16 ? 2 : 4);
         b.ldc = H;
-        b.c_bf16 = p.bf16;
+        b.c_bf16 = p->bf16;
         b.alpha = factors;
         b.part = part;
-        SC_RUN(launch_tile_product(TPK_WEIGHTS, i + 1 < p.pieces ? p.dw : p.dw_last, b, TpSum{}, st));
+        b.live = live;
+        SC_RUN(launch_tile_product(TPK_WEIGHTS, i + 1 < p->pieces ? p->dw : p->dw_last, b, TpSum{}, st));
     }
-#undef SC_RUN
     return hipSuccess;
 }
+
+hipError_t launch_xent(const XentPlan& p, const void* h, const void* W, const int64_t* targets, float* loss,
+                       float* mean, void* dh, void* dW, void* workspace, hipStream_t st) {
+    if (p.T == 0) {
+        SC_RUN(launch_zero(mean, 4, st));
+        return launch_zero(dW, p.V * p.H * (p.bf16 ? 2 : 4), st);
+    }
+    XentRun run;
+    run.p = &p;
+    run.h = h;
+    run.W = W;
+    run.targets = targets;
+    run.ws = (char*)workspace;
+    run.st = st;
+    SC_RUN(run.operands(nullptr));
+    SC_RUN(run.logits());
+    SC_RUN(run.log_sums(loss, nullptr));
+    hipLaunchKernelGGL(xent_mean_kernel, dim3(1), dim3(1024), 0, st, loss, targets, p.T, p.V,
+                       run.at<float>(p.o_factors), mean);
+    SC_RUN(hipGetLastError());
+    return run.gradients(dh, dW);
+}
+#undef SC_RUN
 
 }  // namespace scopt
