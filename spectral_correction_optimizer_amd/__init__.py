@@ -825,45 +825,53 @@ GradNorm = collections.namedtuple("GradNorm", "norm scale grads")
 GradNorm.__doc__ = "Of clip_grads: the norm and the factor (float32, 0-dim) and the clipped gradients."
 
 
+@functools.lru_cache(maxsize=None)
+def _marshal():
+    path = os.path.join(_HERE, "libscopt_marshal.so")
+    if not os.path.exists(path):
+        raise ScoptError(-100, f"{path} is missing; build it with __graft_entry__.build()")
+    f = ctypes.PyDLL(path).scopt_tensor_table
+    f.restype = ctypes.c_int
+    f.argtypes = [ctypes.py_object, ctypes.c_void_p, ctypes.c_int, ctypes.c_int] + [ctypes.c_void_p] * 3
+    return f
+
+
 def _grad_table(who, tensors, like=None):
-    """Host arrays (types, sizes, pointers) of a list of gradients; like: the list that they have to match."""
+    """Device and host arrays (types, sizes, pointers) of a list of gradients; like: the list that they have to match."""
     n = len(tensors)
+    if n == 0:
+        raise ValueError(f"{who}: no tensors")
     if like is not None and len(like) != n:
         raise ValueError(f"{who}: {n} outputs for {len(like)} gradients")
-    dev = tensors[0].device
+    dev = (tensors if like is None else like)[0].device
     if dev.type != "cuda":
         raise ValueError(f"{who}: tensors must be on a GPU, got {dev}")
     dtypes, sizes, where = (ctypes.c_int * n)(), (ctypes.c_int64 * n)(), (ctypes.c_void_p * n)()
-    for i, t in enumerate(tensors):
-        dt = _DT.get(t.dtype)
-        if dt is None or t.device != dev or not t.is_contiguous():
-            raise ValueError(f"{who}: tensor {i} must be a contiguous float32 or bfloat16 tensor on {dev}, got "
-                             f"{t.dtype} {tuple(t.shape)} on {t.device}"
-                             f"{'' if t.is_contiguous() else ' (not contiguous)'}")
-        if like is not None and (t.shape != like[i].shape or t.dtype is not like[i].dtype):
-            raise ValueError(f"{who}: output {i} is {t.dtype} {tuple(t.shape)}, its gradient {like[i].dtype} "
-                             f"{tuple(like[i].shape)}")
-        dtypes[i], sizes[i], where[i] = dt, t.numel(), t.data_ptr()
-    return dev, dtypes, sizes, where
+    bad = _marshal()(tensors, None if like is None else id(like), n, dev.index, dtypes, sizes, where)
+    if bad >= 0:
+        t = tensors[bad]
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{who}: entry {bad} is a {type(t).__name__}, not a tensor")
+        want = "float32 or bfloat16 tensor" if like is None else f"{like[bad].dtype} tensor of shape {tuple(like[bad].shape)}"
+        raise ValueError(f"{who}: {'gradient' if like is None else 'output'} {bad} must be a contiguous {want} on {dev}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ' (not contiguous)'}")
+    return dev, n, dtypes, sizes, where
 
 
-def _sumsq(dev, n, dtypes, sizes, where):
-    lib, bytes_ = load_library(), ctypes.c_int64()
-    _check(lib.sc_grad_sumsq_workspace(n, dtypes, sizes, ctypes.byref(bytes_)))
-    ws = torch.empty(bytes_.value, dtype=torch.uint8, device=dev)
-    sumsq = torch.empty((), dtype=torch.float64, device=dev)
-    _run(dev, lib.sc_grad_sumsq, n, dtypes, sizes, where, sumsq.data_ptr(), ws.data_ptr(), bytes_.value)
-    return sumsq
+def _sumsq(dev, n, dtypes, sizes, where, sumsq):
+    lib, size = load_library(), ctypes.c_int64()
+    _check(lib.sc_grad_sumsq_workspace(n, dtypes, sizes, ctypes.byref(size)))
+    ws = torch.empty(size.value, dtype=torch.uint8, device=dev)
+    _run(dev, lib.sc_grad_sumsq, n, dtypes, sizes, where, sumsq, ws.data_ptr(), size.value)
 
 
 def grad_sumsq(grads) -> "torch.Tensor":
     """The sum of squares (float64, 0-dim) of a list of float32 or bfloat16 tensors of any shapes, in a
     fixed order.  Where gradients are sharded, the ranks' sums added up go to clip_grads."""
-    grads = list(grads)
-    if not grads:
-        raise ValueError("grad_sumsq: no tensors")
-    dev, *table = _grad_table("grad_sumsq", grads)
-    return _sumsq(dev, len(grads), *table)
+    dev, *table = _grad_table("grad_sumsq", list(grads))
+    sumsq = torch.empty((), dtype=torch.float64, device=dev)
+    _sumsq(dev, *table, sumsq.data_ptr())
+    return sumsq
 
 
 def clip_grads(grads, max_norm: float, out=None, sumsq: "torch.Tensor" = None) -> GradNorm:
@@ -871,18 +879,19 @@ def clip_grads(grads, max_norm: float, out=None, sumsq: "torch.Tensor" = None) -
     scale = min(1, max_norm / (norm + 1e-6)), in place or into the tensors of out.  sumsq: the sum of
     squares where it is known already (grad_sumsq, added over the ranks)."""
     grads = list(grads)
-    if not grads:
-        raise ValueError("clip_grads: no tensors")
-    dev, dtypes, sizes, where = _grad_table("clip_grads", grads)
+    dev, n, dtypes, sizes, where = _grad_table("clip_grads", grads)
     to, where_to = grads, where
     if out is not None:
         to = list(out)
-        where_to = _grad_table("clip_grads", to, like=grads)[3]
+        where_to = _grad_table("clip_grads", to, like=grads)[4]
+    both = torch.empty(4, dtype=torch.float32, device=dev)  # the norm, the factor, and room for a float64
     if sumsq is None:
-        sumsq = _sumsq(dev, len(grads), dtypes, sizes, where)
+        total = both.data_ptr() + 8
+        _sumsq(dev, n, dtypes, sizes, where, total)
     else:
         _train_check("clip_grads", torch.float32, dev, ("sumsq", sumsq, torch.float64, ()))
-    norm, scale = torch.empty(2, dtype=torch.float32, device=dev).unbind()
-    _run(dev, load_library().sc_clip_grads, len(grads), dtypes, sizes, where, where_to, sumsq.data_ptr(),
-         float(max_norm), norm.data_ptr(), scale.data_ptr())
+        total = sumsq.data_ptr()
+    _run(dev, load_library().sc_clip_grads, n, dtypes, sizes, where, where_to, total, float(max_norm),
+         both.data_ptr(), both.data_ptr() + 4)
+    norm, scale, _, _ = both.unbind()
     return GradNorm(norm, scale, to)

@@ -1,9 +1,11 @@
-"""Build libscopt.so (HIP kernels + C ABI) for gfx950 with hipcc, in-tree."""
+"""Build libscopt.so (HIP kernels + C ABI) for gfx950 with hipcc, and libscopt_marshal.so, the binding's
+helper for lists of tensors, with the host compiler, in-tree."""
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -12,12 +14,14 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libscopt.so")
+MARSHAL = os.path.join(PKG, "libscopt_marshal.so")
 
 SOURCES = ["act.hip", "api.cpp", "cholesky.hip", "clip.hip", "elementwise.hip", "embed.hip", "gemm.hip", "jacobi.hip",
            "layernorm.hip", "mask.hip", "quad.hip", "tile_product.hip", "token_loss.hip", "train_api.cpp", "xent.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+CXX = os.environ.get("CXX", "g++")
 COMMON = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-result",
     # Compile without packed-FP32 instructions (the host pass only warns that it
@@ -39,10 +43,27 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _build_marshal() -> None:
+    import torch
+    base = os.path.dirname(torch.__file__)
+    tmp = MARSHAL + ".tmp"
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-I", INCLUDE, "-isystem", os.path.join(base, "include"), "-isystem",
+           os.path.join(base, "include", "torch", "csrc", "api", "include"), "-isystem",
+           sysconfig.get_paths()["include"], os.path.join(CSRC, "marshal.cpp"), "-o", tmp, "-L",
+           os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("marshal.cpp failed:\n" + r.stdout + r.stderr)
+    os.replace(tmp, MARSHAL)
+
+
 def build_library(verbose: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
-    with ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as ex:
+    with ThreadPoolExecutor(max_workers=min(8, len(SOURCES) + 1)) as ex:
+        marshal = ex.submit(_build_marshal)
         objs = list(ex.map(_compile, SOURCES))
+        marshal.result()
     tmp = LIB + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -16,7 +16,7 @@ namespace scopt {
 
 constexpr int kClipThreads = 256, kClipGroups = 4;
 constexpr int64_t kClipChunk = (int64_t)kClipThreads * kClipGroups * 8;  // elements of a chunk
-constexpr int kClipTensors = 128;
+constexpr int kClipTensors = 140;  // a launch takes 4 KiB of arguments
 constexpr int kSumsqGrid = 2048;
 
 struct ClipTable {
@@ -26,6 +26,8 @@ struct ClipTable {
     uint32_t first[kClipTensors + 1];  // chunks before each tensor
     int count;
 };
+
+static_assert(sizeof(ClipTable) <= 4000, "a launch's arguments");
 
 // tensor of a chunk: the last one that begins at or before it
 __device__ __forceinline__ int clip_find(const ClipTable& t, uint32_t chunk) {

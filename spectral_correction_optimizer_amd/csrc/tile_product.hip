@@ -56,8 +56,38 @@ __global__ __launch_bounds__(256) void tp_reduce_kernel(const TpArgs P, const fl
         } else {
 #pragma unroll
             for (int r = 0; r < 4; ++r) v[r] *= alpha * tp_gain(P, min(n + r, P.N - 1));
+            if (P.coef) {
+                const float f = gld(P.coef + m);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v[r] *= f;
+            }
             tp_store(P.C, P.c_bf16, tp_row(P, (int)m) * P.ldc + n, v, left);
         }
+    }
+}
+
+// Sum of the parts of TP_TAIL's cut tiles, in order, with its stores: four columns a thread.
+template <int BM, int BN>
+__global__ __launch_bounds__(256) void tp_tail_kernel(const TpArgs P) {
+    const TpTail t = {gld(&P.tail->full), gld(&P.tail->rest), gld(&P.tail->splits)};
+    if (t.splits == 1) return;
+    const int M = P.live_rows ? min(P.M, gld(P.live)) : P.M, tiles_m = (M + BM - 1) / BM;
+    constexpr int GROUPS = BM * BN / 4;
+    const int64_t stride = (int64_t)t.rest * BM * BN;
+    for (int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x; g < (int64_t)t.rest * GROUPS;
+         g += (int64_t)gridDim.x * 256) {
+        const int tile = (int)(g / GROUPS), in = (int)(g % GROUPS) * 4;
+        int tm, tn;
+        tp_tile(t.full + tile, tiles_m, P.tiles_n, tm, tn);
+        const int m = tm * BM + in / BN, n = tn * BN + in % BN;
+        if (m >= M || n >= P.N) continue;
+        const float* p = P.part + (int64_t)tile * BM * BN + in;
+        v4f x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+        for (int s = 0; s < t.splits; ++s) x += gld4(p + s * stride);
+        const float f = P.coef ? gld(P.coef + m) : 1.0f;
+        const float v[4] = {x[0] * f, x[1] * f, x[2] * f, x[3] * f};
+        tp_store(P.C, P.c_bf16, tp_row(P, m) * P.ldc + n, v, P.N - n);
     }
 }
 
@@ -70,17 +100,20 @@ __global__ __launch_bounds__(256) void tp_reduce_kernel(const TpArgs P, const fl
 // The same figures choose for the logits (k contiguous, row statistics behind every tile) and for the
 // segments of float32 products, which were not fitted.
 // A split's partial sums are written and read once more, at about 5 TB/s, by another kernel.
+namespace {
+struct ShapeTimes {
+    int bm, bn, per_cu, turn;
+    double step, tile;
+};
+constexpr ShapeTimes kShapes[3] = {
+    {256, 256, 1, 2, 1.70, 12.0}, {128, 128, 2, 2, 1.20, 3.7}, {64, 128, 2, 3, 0.81, 1.2}};
+}  // namespace
+
 TpPlan tp_plan(int M, int N, int K, int nseg, bool may_split) {
-    struct Shape {
-        int bm, bn, per_cu, turn;
-        double step, tile;
-    };
-    static const Shape shapes[3] = {
-        {256, 256, 1, 2, 1.70, 12.0}, {128, 128, 2, 2, 1.20, 3.7}, {64, 128, 2, 3, 0.81, 1.2}};
     TpPlan best;
     double best_us = 1e300;
     for (int s = 0; s < 3; ++s) {
-        const Shape& S = shapes[s];
+        const ShapeTimes& S = kShapes[s];
         const int64_t tm = (M + S.bm - 1) / S.bm, tn = (N + S.bn - 1) / S.bn;
         const int64_t turns = (int64_t)((K + 64 * S.turn - 1) / (64 * S.turn)) * nseg;
         for (int sp = 1; sp <= (may_split ? 64 : 1); sp *= 2) {
@@ -104,7 +137,57 @@ TpPlan tp_plan(int M, int N, int K, int nseg, bool may_split) {
     return best;
 }
 
+// The least time for the most tokens there can be; with fewer of them the last round is cut anew on the device.
+TpPlan tp_plan_live(int M, int N, int K, int nseg, bool live_k) {
+    TpPlan best;
+    double best_us = 1e300;
+    for (int s = 0; s < 3; ++s) {
+        const ShapeTimes& S = kShapes[s];
+        const int slots = kCus * S.per_cu;
+        TpTailQuery q;
+        q.M = M;
+        q.K = K;
+        q.live_k = live_k;
+        q.bm = S.bm;
+        q.turn_k = 64 * S.turn;
+        q.tiles_n = (N + S.bn - 1) / S.bn;
+        q.nseg = nseg;
+        q.slots = slots;
+        q.turn_ns = (int)(1000.0 * S.step * S.turn);
+        q.tile_ns = (int)(1000.0 * S.tile);
+        q.join_ns = 8 * S.bm * S.bn / 5000;  // a tile's partial sums written and read once more, at about 5 TB/s
+        const int live = live_k ? K : M, tiles = q.tiles(live), total = q.total(live);
+        // parts of any number of live tokens: fewer than two turns each are none, nor more than two rounds
+        const int64_t parts = total < 4 ? 0 : (int64_t)tiles * (total / 2 < 64 ? total / 2 : 64);
+        q.most = (int)(parts < 2 * slots ? parts : 2 * slots);
+        const int rest = tiles % slots;
+        int ns = 0x7fffffff;
+        for (int p = 1; p <= 64; ++p) ns = q.ns(rest, total, p) < ns ? q.ns(rest, total, p) : ns;
+        const double us = (double)(tiles / slots) * ((double)total * S.step * S.turn + S.tile) + 1e-3 * ns;
+        if (us < best_us) {
+            best_us = us;
+            best.shape = s;
+            best.bm = S.bm;
+            best.bn = S.bn;
+            best.tiles_m = (M + S.bm - 1) / S.bm;
+            best.tiles_n = q.tiles_n;
+            best.part_bytes = 4ll * S.bm * S.bn * q.most;
+            best.tail = q;
+        }
+    }
+    return best;
+}
+
 namespace {
+template <class S>
+hipError_t launch_tail(TpKind kind, const TpPlan& plan, const TpArgs& P, hipStream_t st) {
+    const dim3 grid((unsigned)plan.tail.slots), blk(S::NT);
+    if (kind == TPK_STATES_LIVE) hipLaunchKernelGGL((tile_product_kernel<S, true, false, TP_TAIL>), grid, blk, 0, st, P);
+    else hipLaunchKernelGGL((tile_product_kernel<S, false, false, TP_TAIL>), grid, blk, 0, st, P);
+    if (plan.part_bytes > 0)
+        hipLaunchKernelGGL((tp_tail_kernel<S::BM, S::BN>), dim3(2048), dim3(256), 0, st, P);
+    return hipGetLastError();
+}
 template <class S>
 hipError_t launch_shape(TpKind kind, const TpArgs& P, bool part, hipStream_t st) {
     const int all = P.tiles_m * P.tiles_n * P.splits, most = kCus * S::PER_CU;
@@ -124,6 +207,7 @@ hipError_t launch_shape(TpKind kind, const TpArgs& P, bool part, hipStream_t st)
             if (part) hipLaunchKernelGGL((tile_product_kernel<S, false, false, TP_PART>), grid, blk, 0, st, P);
             else hipLaunchKernelGGL((tile_product_kernel<S, false, false, TP_STORE>), grid, blk, 0, st, P);
             break;
+        default: return hipErrorInvalidValue;
     }
     return hipGetLastError();
 }
@@ -141,7 +225,11 @@ hipError_t launch_tile_product(TpKind kind, const TpPlan& plan, TpArgs P, const 
     P.tiles_m = plan.tiles_m;
     P.tiles_n = plan.tiles_n;
     P.splits = plan.splits;
-    P.live_rows = P.live && kind == TPK_STATES;
+    P.live_rows = P.live && (kind == TPK_STATES || kind == TPK_STATES_LIVE);
+    if (kind == TPK_STATES_LIVE || kind == TPK_WEIGHTS_LIVE)
+        return plan.shape == 0   ? launch_tail<Big>(kind, plan, P, st)
+               : plan.shape == 1 ? launch_tail<Mid>(kind, plan, P, st)
+                                 : launch_tail<Small>(kind, plan, P, st);
     const bool part = (kind == TPK_STATES || kind == TPK_WEIGHTS) && (plan.splits > 1 || sum.acc || sum.out_acc);
     hipError_t e = plan.shape == 0   ? launch_shape<Big>(kind, P, part, st)
                    : plan.shape == 1 ? launch_shape<Mid>(kind, P, part, st)

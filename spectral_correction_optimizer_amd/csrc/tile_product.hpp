@@ -263,6 +263,8 @@ enum TpEpi {
     TP_PART = 1,    // float32 sums of one split of k, [split][M][N]
     TP_STATS = 2,   // row maxima and exp sums of the tile; logits kept as P.keep says
     TP_GRAD = 3,    // (exp(acc - lse[m]) - [n is m's target]) * alpha, as bfloat16 planes
+    TP_TAIL = 4,    // C = acc * coef[m] at row rows[m]; tiles that do not fill a round are cut along k
+                    // (TpTail) and leave float32 sums, [split][tile][BM][BN]
 };
 
 template <int BM_, int BN_, int WVM_, int WVN_, int NBUF_, int PER_CU_>
@@ -333,24 +335,49 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
     }
     // k goes in turns of the buffers; what lies past its end multiplies zeros.
     const int kturns = max(1, (K + 64 * NBUF - 1) / (64 * NBUF)), total = kturns * P.nseg;
-    const int per = (total + P.splits - 1) / P.splits;
-    const int tiles = tiles_m * P.tiles_n, all = tiles * P.splits;
+    const int tiles = tiles_m * P.tiles_n;
+    TpTail tail = {0, tiles, P.splits};
+    if constexpr (EPI == TP_TAIL) {
+        tail.full = __builtin_amdgcn_readfirstlane(gld(&P.tail->full));
+        tail.rest = __builtin_amdgcn_readfirstlane(gld(&P.tail->rest));
+        tail.splits = __builtin_amdgcn_readfirstlane(gld(&P.tail->splits));
+    }
+    const int all = tail.full + tail.rest * tail.splits;
+    // tile and part of k of a turn
+    struct Item {
+        int tile, split, from, to;
+    };
+    auto item = [&](int turn) SC_INLINE {
+        Item i;
+        if (EPI == TP_TAIL && turn < tail.full) {
+            i.tile = xcd_remap(turn, tail.full);
+            i.split = i.from = 0;
+            i.to = total;
+        } else {
+            const int id = xcd_remap(turn - tail.full, all - tail.full);
+            const int per = (total + tail.splits - 1) / tail.splits;
+            i.split = id / tail.rest;
+            i.tile = tail.full + id - i.split * tail.rest;
+            i.from = i.split * per;
+            i.to = min(total, i.from + per);
+        }
+        return i;
+    };
 
     // the turn that is fetched next: its tile, segment and place in the segment
     struct Ahead {
         int m0, n0, seg, kt, left;
     } ah;
     auto begin_tile = [&](int turn) SC_INLINE {
-        const int id = turn < all ? xcd_remap(turn, all) : 0;
-        const int split = id / tiles;
+        Item it = {0, 0, 0, 0};
+        if (turn < all) it = item(turn);
         int tm, tn;
-        tp_tile(id - split * tiles, tiles_m, P.tiles_n, tm, tn);
+        tp_tile(it.tile, tiles_m, P.tiles_n, tm, tn);
         ah.m0 = tm * BM;
         ah.n0 = tn * BN;
-        const int at = split * per;
-        ah.left = turn < all ? min(total, at + per) - at : 0;
-        ah.seg = at / kturns;
-        ah.kt = at - ah.seg * kturns;
+        ah.left = it.to - it.from;
+        ah.seg = it.from / kturns;
+        ah.kt = it.from - ah.seg * kturns;
     };
     auto prepare = [&]() SC_INLINE {
         const bool live = ah.left > 0;
@@ -424,9 +451,10 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(PER * (NBUF - 1)) : "memory");
 
     for (int turn = blockIdx.x; turn < all; turn += gridDim.x) {
-        const int id = xcd_remap(turn, all), split = id / tiles;
+        const Item it = item(turn);
+        const int split = it.split;
         int tm, tn;
-        tp_tile(id - split * tiles, tiles_m, P.tiles_n, tm, tn);
+        tp_tile(it.tile, tiles_m, P.tiles_n, tm, tn);
         const int m0 = tm * BM, n0 = tn * BN;
         // (TP_STATS: a column past the last one starts at -infinity and, its operand being zero, stays)
 #pragma unroll
@@ -450,7 +478,7 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
         for (int i = 0; i < MI; ++i) fa[1][i / MG][i % MG] = zeros;
         __builtin_amdgcn_s_barrier();  // the first buffer has landed for every wave
         asm volatile("s_nop 7" ::: "memory");  // and the zeros are written
-        for (int turns = max(1, min(total, split * per + per) - split * per); turns > 0; --turns) {
+        for (int turns = max(1, it.to - it.from); turns > 0; --turns) {
             if (turns == 1) begin_tile(turn + gridDim.x);  // the last turn fetches the next tile's first one
             prepare();
             buffer(0, a0, b0);
@@ -512,7 +540,7 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
                             d[j][w] = pack_bf16x2(acc[i][j][2 * w] * g[j][2 * w],
                                                   acc[i][j][2 * w + 1] * g[j][2 * w + 1]);
                     const int c = tp_gather_row<NI>(d);
-                    if (m < M) tp_store_row<NI>((uint16_t*)P.C + tp_row(P, m) * P.ldc + n0 + wn + c, d);
+                    if (m < M) tp_store_row<NI>((uint16_t*)P.C + (int64_t)m * P.ldc + n0 + wn + c, d);
                 }
             } else {
                 auto store = [&](auto bf16) SC_INLINE {
@@ -525,7 +553,7 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
                             float v[4];
 #pragma unroll
                             for (int r = 0; r < 4; ++r) v[r] = acc[i][j][r] * g[j][r];
-                            if (m < M) tp_store(P.C, decltype(bf16)::value, tp_row(P, m) * P.ldc + n, v, N - n);
+                            if (m < M) tp_store(P.C, decltype(bf16)::value, (int64_t)m * P.ldc + n, v, N - n);
                         }
                     }
                 };
@@ -541,6 +569,43 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
                     const int m = lm + 16 * i, n = ln + 16 * j;
                     const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
                     if (m < M) tp_store(P.part, 0, ((int64_t)split * M + m) * N + n, v, N - n);
+                }
+            }
+        } else if constexpr (EPI == TP_TAIL) {
+            // Each row block leaves the accumulation registers at one place, whatever becomes of it: where
+            // the ways of storing it each read them, the register allocator moved sums ahead of the
+            // waits above.
+            const bool cut = turn >= tail.full && tail.splits > 1;
+            float* part = P.part + ((int64_t)split * tail.rest + (it.tile - tail.full)) * (BM * BN);
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                row_block(i);
+                const int m = lm + 16 * i, in = min(m, M - 1);
+                const float f = P.coef && !cut ? gld(P.coef + in) : 1.0f;
+                float v[NI][4];
+#pragma unroll
+                for (int j = 0; j < NI; ++j)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) v[j][r] = acc[i][j][r] * f;
+                if (cut) {
+#pragma unroll
+                    for (int j = 0; j < NI; ++j)
+                        gst4(part + (m - m0) * BN + ln - n0 + 16 * j, v4f{v[j][0], v[j][1], v[j][2], v[j][3]});
+                    continue;
+                }
+                const int64_t at = tp_row(P, in) * P.ldc + n0 + wn;
+                if (P.c_bf16 && whole) {
+                    uint32_t d[NI][2];
+#pragma unroll
+                    for (int j = 0; j < NI; ++j)
+#pragma unroll
+                        for (int w = 0; w < 2; ++w) d[j][w] = pack_bf16x2(v[j][2 * w], v[j][2 * w + 1]);
+                    const int c = tp_gather_row<NI>(d);
+                    if (m < M) tp_store_row<NI>((uint16_t*)P.C + at + c, d);
+                } else if (m < M) {
+#pragma unroll
+                    for (int j = 0; j < NI; ++j)
+                        tp_store(P.C, P.c_bf16, at + 4 * (lane >> 4) + 16 * j, v[j], N - (ln + 16 * j));
                 }
             }
         } else if constexpr (EPI == TP_STATS) {
@@ -630,7 +695,8 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
                 const int m = lm + 16 * i;
                 row_block(i);
                 if (m >= M) continue;
-                const float alpha = gld(P.coef ? P.coef + m : P.alpha);
+                float alpha = gld(P.coef ? P.coef + m : P.alpha);
+                if (P.coef_zeros && alpha != 0.0f) alpha = 1.0f;
                 // a row without weight is one of zeros, whatever its logits are
                 const int64_t tgt = alpha != 0.0f ? tp_target(P.targets, P.vocab, m) : -1;
                 const float lse = gld(P.lse + m);

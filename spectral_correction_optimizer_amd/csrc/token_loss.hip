@@ -22,14 +22,19 @@
 
 namespace scopt {
 
+struct Tails {
+    TpTailQuery q[3];  // dh, dW, and dW of the last piece
+};
+
 // The counted tokens in order: rows[c] = t, place[t] = c (-1 where not counted), their targets; logp and
 // loss (or NULL) of the others are 0, and coef starts at 0.  One workgroup, eight tokens a thread
 // and turn: a turn's positions are the sums over the threads before.
 __global__ __launch_bounds__(1024) void token_rows_kernel(const int64_t* __restrict__ targets, int64_t T, int64_t V,
                                                           int* __restrict__ live, int* __restrict__ rows,
                                                           int* __restrict__ place, int64_t* __restrict__ kept,
-                                                          float* __restrict__ coef, float* __restrict__ factors,
-                                                          float* __restrict__ logp, float* __restrict__ loss) {
+                                                          float* __restrict__ coef, float* __restrict__ logp,
+                                                          float* __restrict__ loss, const Tails q,
+                                                          TpTail* __restrict__ tails) {
     __shared__ int sums[2][16];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     int base = 0, turn = 0;
@@ -74,30 +79,40 @@ __global__ __launch_bounds__(1024) void token_rows_kernel(const int64_t* __restr
             }
         }
     }
-    if (threadIdx.x == 0) {
-        gst(live, base);
-        gst(factors, 1.0f);
+    if (threadIdx.x == 0) gst(live, base);
+    if (!tails || wave >= 3) return;
+    // how the gradients' products are dealt out: a wavefront a product, a lane a number of parts
+    const TpTailQuery& p = q.q[wave];
+    const int tiles = p.tiles(base), total = p.total(base), rest = tiles % p.slots;
+    int best = p.ns(rest, total, lane + 1), splits = lane + 1;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int ns = __shfl_xor(best, o), s = __shfl_xor(splits, o);
+        const bool less = ns < best || (ns == best && s < splits);
+        best = less ? ns : best;
+        splits = less ? s : splits;
+    }
+    if (lane == 0) {
+        gst(&tails[wave].full, tiles - rest);
+        gst(&tails[wave].rest, rest);
+        gst(&tails[wave].splits, splits);
     }
 }
 
 // The policy's losses and the coefficients of its logit gradients.  One workgroup: sums in a fixed
-// order.  Without weights the coefficients carry the power of two next below 1 / count, and the stores of
-// the gradients the rest of it, as in cross entropy.
+// order.
 __global__ __launch_bounds__(1024) void policy_kernel(const int* __restrict__ live, const int* __restrict__ rows,
-                                                      PolicyArgs a, float* __restrict__ coef,
-                                                      float* __restrict__ factors) {
+                                                      PolicyArgs a, float* __restrict__ coef) {
     __shared__ double red[16];
     const int n = gld(live);
     const double share = n > 0 ? 1.0 / n : 1.0;
-    double unit = 1.0;
-    while (unit > share) unit *= 0.5;
     double total = 0.0, kl = 0.0, stopped = 0.0;
 #pragma unroll 4
     for (int c = threadIdx.x; c < n; c += 1024) {
         const int64_t t = gld(rows + c);
         const double lp = gld(a.logp + t), A = gld(a.advantages + t);
         const double r = exp(lp - (double)gld(a.old_logp + t));
-        const double w = a.weights ? (double)gld(a.weights + t) : 1.0;
+        const double w = a.weights ? (double)gld(a.weights + t) : share;
         const bool high = A > 0.0 && r > a.hi, low = A < 0.0 && r < a.lo;
         double L = -A * (high ? a.hi : low ? a.lo : r);
         double g = high || low ? 0.0 : A * r;
@@ -112,14 +127,13 @@ __global__ __launch_bounds__(1024) void policy_kernel(const int* __restrict__ li
         stopped += high || low ? 1.0 : 0.0;
         total += w != 0.0 ? w * L : 0.0;  // a token of weight 0 counts for nothing, finite or not
         gst(a.loss + t, (float)L);
-        gst(coef + c, w != 0.0 ? (float)(g * (a.weights ? w : unit)) : 0.0f);
+        gst(coef + c, w != 0.0 ? (float)(g * w) : 0.0f);
     }
     total = block_sum_f64(total, red);
     kl = block_sum_f64(kl, red);
     stopped = block_sum_f64(stopped, red);
     if (threadIdx.x == 0) {
-        gst(factors, a.weights ? 1.0f : (float)(share / unit));
-        gst(a.total, (float)(a.weights ? total : total * share));
+        gst(a.total, (float)total);
         if (a.kl_mean) gst(a.kl_mean, (float)(kl * share));
         gst(a.clipped, (float)(stopped * share));
     }
@@ -160,6 +174,7 @@ __global__ __launch_bounds__(1024) void preference_kernel(const int* __restrict_
     const double g = (double)a.beta / (double)a.pairs * ((1.0 - e) * lose - e * win);
     if (threadIdx.x == 0) {
         gst(a.loss + pair, (float)(z == z ? L : z));
+        if (a.pairs == 1) gst(a.mean, (float)(z == z ? L : z));
         gst(a.rewards + 2 * pair, (float)reward[0]);
         gst(a.rewards + 2 * pair + 1, (float)reward[1]);
     }
@@ -185,7 +200,8 @@ __global__ __launch_bounds__(1024) void pair_mean_kernel(const float* __restrict
 
 TokenLossPlan token_loss_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit, bool gradients) {
     TokenLossPlan p{};
-    p.x = xent_plan(bf16, T, V, H, limit, gradients);
+    p.x = xent_plan(bf16, T, V, H, limit, gradients, true);
+    p.gradients = gradients;
     int64_t o = p.x.bytes;
     auto take = [&](int64_t bytes) {
         const int64_t at = o;
@@ -224,8 +240,9 @@ hipError_t forward(const TokenLossPlan& p, XentRun& run, const void* h, const vo
     run.rows = rows;
     run.place = place;
     run.coef = coef;
+    const Tails tails = {{p.x.dh.tail, p.x.dw.tail, p.x.dw_last.tail}};
     hipLaunchKernelGGL(token_rows_kernel, dim3(1), dim3(1024), 0, st, targets, p.x.T, p.x.V, live, rows, place, kept,
-                       coef, run.at<float>(p.x.o_factors), logp, loss);
+                       coef, logp, loss, tails, p.gradients ? run.at<TpTail>(p.x.o_tails) : nullptr);
     SC_RUN(hipGetLastError());
     SC_RUN(run.operands(dh));
     SC_RUN(run.logits());
@@ -250,8 +267,7 @@ hipError_t launch_policy_loss(const TokenLossPlan& p, const void* h, const void*
     }
     XentRun run;
     SC_RUN(forward(p, run, h, W, targets, a.logp, a.loss, dh, workspace, st));
-    hipLaunchKernelGGL(policy_kernel, dim3(1), dim3(1024), 0, st, run.live, run.rows, a, run.at<float>(p.o_coef),
-                       run.at<float>(p.x.o_factors));
+    hipLaunchKernelGGL(policy_kernel, dim3(1), dim3(1024), 0, st, run.live, run.rows, a, run.at<float>(p.o_coef));
     SC_RUN(hipGetLastError());
     return run.gradients(dh, dW);
 }
@@ -265,8 +281,10 @@ hipError_t launch_preference_loss(const TokenLossPlan& p, const void* h, const v
                            (float*)((char*)workspace + p.o_coef));
         SC_RUN(hipGetLastError());
     }
-    hipLaunchKernelGGL(pair_mean_kernel, dim3(1), dim3(1024), 0, st, a.loss, a.pairs, a.mean);
-    SC_RUN(hipGetLastError());
+    if (a.pairs != 1) {
+        hipLaunchKernelGGL(pair_mean_kernel, dim3(1), dim3(1024), 0, st, a.loss, a.pairs, a.mean);
+        SC_RUN(hipGetLastError());
+    }
     if (p.x.T == 0) return launch_zero(dW, p.x.V * p.x.H * (p.x.bf16 ? 2 : 4), st);
     return run.gradients(dh, dW);
 }

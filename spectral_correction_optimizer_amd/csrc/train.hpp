@@ -19,6 +19,31 @@ enum TpKeep {
     TP_KEEP_LOGIT = 2,  // the logits in float32
 };
 
+// How the `tiles` whole tiles of a product of `total` turns of k go to `slots` workgroups (TP_TAIL): the first
+// `full` one after the other, in whole rounds, and of the others (`rest`) each in `splits` parts of k.
+struct TpTail {
+    int full, rest, splits;
+};
+// What that depends on: sizes, one of them bounded by the live tokens, and the tile's times (tp_plan).
+struct TpTailQuery {
+    int M = 0, K = 0, live_k = 0;  // live_k: the tokens are k, else the rows
+    int bm = 1, turn_k = 1, tiles_n = 0, nseg = 1, slots = 1;
+    int turn_ns = 0, tile_ns = 0, join_ns = 0;
+    int most = 0;  // parts that there is room for
+    __host__ __device__ int tiles(int live) const { return ((live_k || M < live ? M : live) + bm - 1) / bm * tiles_n; }
+    __host__ __device__ int total(int live) const {
+        const int k = live_k && live < K ? live : K;
+        return (k > 0 ? (k + turn_k - 1) / turn_k : 1) * nseg;
+    }
+    // time of the last round's tiles in s parts, their sums and join included; the largest number where that is
+    // not to be
+    __host__ __device__ int ns(int rest, int total, int s) const {
+        if (s > 1 && (rest * s > most || total < 2 * s)) return 0x7fffffff;
+        return (rest * s + slots - 1) / slots * ((total + s - 1) / s * turn_ns + tile_ns) +
+               (s > 1 ? 4000 + rest * s * join_ns : 0);
+    }
+};
+
 // One tiled product (tile_product.hpp).  An operand's rows are readable up to the next
 // multiple of 8 elements; with k contiguous, what lies between K and there is finite where
 // the other operand's rows beyond K do not exist (they count as zeros), else zero.
@@ -53,12 +78,16 @@ struct TpArgs {
     float* stat_sum = nullptr;
     int64_t stat_first = 0;
     const float* lse = nullptr;
-    const float* coef = nullptr;  // TP_GRAD: a factor of each row's values, in place of alpha
+    // TP_GRAD: a factor of each row's values, in place of alpha; with coef_zeros only its zeros count, and
+    // the others' factor is 1.  TP_TAIL: a factor of each row of C (NULL: 1)
+    const float* coef = nullptr;
+    int coef_zeros = 0;
     // Only the first *live tokens exist (NULL: all).  Tokens are the rows of the logits and of the
     // states' gradients, and k of the weights'.
     const int* live = nullptr;
     int live_rows = 0;          // set by the launch: live counts the rows of C
-    const int* rows = nullptr;  // TP_STORE, reduction: row m is stored as row rows[m] (NULL: m)
+    const int* rows = nullptr;  // TP_TAIL, reduction: row m is stored as row rows[m] (NULL: m)
+    const TpTail* tail = nullptr;  // TP_TAIL: on the device
 };
 
 // The product's operand layouts and what is done with its sums.
@@ -67,6 +96,8 @@ enum TpKind {
     TPK_LOGIT_GRAD,   // A [M][K], B [N][K]
     TPK_STATES,       // A [M][K], B [K][N]: store, or partial sums when splits > 1
     TPK_WEIGHTS,      // A [K][M], B [K][N]: likewise
+    TPK_STATES_LIVE,  // as TPK_STATES and TPK_WEIGHTS, for sizes that are only known on the device: the tiles
+    TPK_WEIGHTS_LIVE, // that do not fill a round of workgroups are cut along k there
 };
 
 // Tile shapes, and the choice between them for an M x N product of `steps` 64-deep steps.
@@ -76,10 +107,13 @@ struct TpPlan {
     int tiles_m = 0, tiles_n = 0;
     int splits = 1;
     int64_t part_bytes = 0;  // float32 partial sums (splits > 1)
+    TpTailQuery tail;        // tp_plan_live
 };
 // Row stride of an operand that the library lays out itself
 inline int64_t tp_pad(int64_t cols) { return cols % 512 == 0 ? cols + 64 : cols; }
 TpPlan tp_plan(int M, int N, int K, int nseg, bool may_split);
+// For the kinds of live tokens: M, N, K are the most there can be, and live_k tells whether the tokens are k
+TpPlan tp_plan_live(int M, int N, int K, int nseg, bool live_k);
 // A product whose sums join others (TPK_STATES, TPK_WEIGHTS): acc is added before the store;
 // with out_acc the float32 sum goes there and C is not written.  Either asks for args.part
 // also without splits.
@@ -111,11 +145,13 @@ struct XentPlan {
     int64_t stat_tiles;        // tiles of a row
     TpPlan logits, logits_last, dh, dw, dw_last;
     // offsets into the workspace
-    int64_t o_factors, o_h, o_w, o_s, o_p, o_tl, o_lse, o_smax, o_ssum, o_part, o_dh, bytes;
+    int64_t o_factors, o_h, o_scaled, o_w, o_s, o_p, o_tl, o_lse, o_smax, o_ssum, o_part, o_dh, o_tails, o_factor, bytes;
 };
 // limit: bytes that the kept probabilities (or a piece's) may take; gradients = false: only the logits'
 // statistics are taken, and there is room for nothing else
-XentPlan xent_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit, bool gradients = true);
+// live: the counted tokens' rows are put together (XentRun::rows)
+XentPlan xent_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit, bool gradients = true,
+                   bool live = false);
 
 // One call's buffers, and the steps that the losses share.  Without `rows` the rows of h are the tokens; with
 // them only the counted ones, in order: row c is token rows[c], *live of them exist, and `targets`, lse
@@ -126,8 +162,11 @@ struct XentRun {
     const int64_t* targets = nullptr;
     char* ws = nullptr;
     const int *live = nullptr, *rows = nullptr, *place = nullptr;  // place[t]: token t's row, or -1
-    // the logit gradients are (softmax - onehot) times coef[row], or times factors[1] without coef; the
-    // stores of dh and dW multiply by factors[0]
+    // The logit gradients are (softmax - onehot) times coef[row].  In bfloat16 the matrix keeps softmax - onehot,
+    // and coef joins dh's rows as they are stored and the rows of h that dW reads, times what makes the target's
+    // entry exact (factor): the target's share of the gradients is the largest, and one coefficient for all
+    // of a sequence's tokens would be rounded the same way in all of them.  Without coef the factor is factors[1], and the stores of dh and dW
+    // multiply by factors[0].
     const float* coef = nullptr;
     hipStream_t st = nullptr;
 
@@ -149,6 +188,7 @@ hipError_t launch_xent(const XentPlan& p, const void* h, const void* W, const in
 
 struct TokenLossPlan {
     XentPlan x;
+    bool gradients;
     int64_t o_live, o_rows, o_place, o_targets, o_coef, bytes;
 };
 TokenLossPlan token_loss_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit, bool gradients);

@@ -104,8 +104,37 @@ __global__ __launch_bounds__(1024) void xent_lse_kernel(const float* __restrict_
     else gst(loss + t, tp_target(targets, V, t) >= 0 ? off : 0.0f);
 }
 
+// softmax - onehot at a token's target, as the logit gradients of live tokens hold it
+__device__ __forceinline__ float target_entry(float target_logit, float lse) {
+    return __builtin_amdgcn_exp2f((target_logit - lse) * kLog2e) - 1.0f;
+}
+// 256 threads: row t's factor, coef times what bfloat16's rounding took from the target's entry, and its H states
+// times that.  A coefficient of 0 gives zeros, whatever the states are.
+__device__ __forceinline__ void scale_row(int64_t t, float coef, const float* target_logit, const float* lse,
+                                          float* factor, const uint16_t* from, uint16_t* to, int64_t H) {
+    const float q = target_entry(gld(target_logit + t), gld(lse + t)), r = bf16_to_f32(f32_to_bf16(q));
+    const float c = coef != 0.0f && r != 0.0f ? coef * (q / r) : coef;
+    if (threadIdx.x == 0) gst(factor + t, c);
+    for (int64_t i = 8 * threadIdx.x; i < H; i += 8 * 256) {
+        const v4u w = *(const SC_GLOBAL v4u*)(from + t * H + i);
+        v4u o;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = coef != 0.0f ? pack_bf16x2(bf16_lo(w[k]) * c, bf16_hi(w[k]) * c) : 0u;
+        *(SC_GLOBAL v4u*)(to + t * H + i) = o;
+    }
+}
+__global__ __launch_bounds__(256) void scale_rows_kernel(const int* __restrict__ live, const float* __restrict__ coef,
+                                                         const float* __restrict__ target_logit,
+                                                         const float* __restrict__ lse, float* __restrict__ factor,
+                                                         const uint16_t* __restrict__ from, uint16_t* __restrict__ to,
+                                                         int64_t H) {
+    const int64_t t = blockIdx.x;
+    if (t < gld(live)) scale_row(t, gld(coef + t), target_logit, lse, factor, from, to, H);
+}
+
 // d from what the logits product kept: exponentials in 16 bits (in place) or float32 logits
-// (into three planes).  `chunks` workgroups a row; a thread takes 8 columns at a time.
+// (into three planes).  `chunks` workgroups a row; a thread takes 8 columns at a time.  With coef and EXP the
+// row's first workgroup scales its row of h, and d has only coef's zeros.
 template <bool EXP>
 __global__ __launch_bounds__(256) void xent_dlogits_kernel(const float* __restrict__ logits, uint16_t* P,
                                                            int64_t plane, int64_t ldp, int N, int bn,
@@ -116,15 +145,22 @@ __global__ __launch_bounds__(256) void xent_dlogits_kernel(const float* __restri
                                                            const int64_t* __restrict__ targets, int64_t V,
                                                            const float* __restrict__ scale_at,
                                                            const int* __restrict__ live,
-                                                           const float* __restrict__ coef) {
+                                                           const float* __restrict__ coef, float* factor, uint16_t* h,
+                                                           int64_t Hh) {
     const int64_t t = blockIdx.x / chunks;
     if (live && t >= gld(live)) return;
-    const float scale = gld(coef ? coef + t : scale_at);
+    float scale = gld(coef ? coef + t : scale_at);
+    if (EXP && coef) {
+        if (blockIdx.x % chunks == 0) scale_row(t, scale, target_logit, lse, factor, h, h, Hh);
+        scale = scale != 0.0f ? 1.0f : 0.0f;
+    }
     // a row without weight is one of zeros, whatever its logits are
     const int64_t tgt = scale != 0.0f ? tp_target(targets, V, t) : -1;
     const float ls = gld(lse + t);
     const float ls2 = ls * kLog2e;
-    const float at_target = tgt >= 0 ? (expf(gld(target_logit + t) - ls) - 1.0f) * scale : 0.0f;
+    float at_target = 0.0f;
+    if (tgt >= 0) at_target = EXP && coef ? target_entry(gld(target_logit + t), ls) :
+                                            (expf(gld(target_logit + t) - ls) - 1.0f) * scale;
     const int64_t end = (N + 7) & ~7;  // the products read no further
     const int64_t from = (int64_t)(blockIdx.x % chunks) * chunk, to = from + chunk < end ? from + chunk : end;
     for (int64_t c = from + 8 * threadIdx.x; c < to; c += 8 * 256) {
@@ -186,7 +222,8 @@ __global__ __launch_bounds__(1024) void xent_mean_kernel(const float* __restrict
     }
 }
 
-XentPlan xent_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit, bool gradients) {
+XentPlan xent_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit, bool gradients,
+                   bool live) {
     XentPlan p{};
     p.bf16 = bf16;
     p.T = T;
@@ -211,9 +248,15 @@ XentPlan xent_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit, bo
     p.logits = tp_plan((int)T, (int)p.piece, (int)H, nseg, false);
     p.logits_last = tp_plan((int)T, (int)last, (int)H, nseg, false);
     if (gradients) {
-        p.dh = tp_plan((int)T, (int)H, (int)p.piece, nseg, true);
-        p.dw = tp_plan((int)p.piece, (int)H, (int)T, nseg, true);
-        p.dw_last = tp_plan((int)last, (int)H, (int)T, nseg, true);
+        const bool join = p.pieces > 1;  // sums over pieces have splits of their own
+        p.dh = live && !join ? tp_plan_live((int)T, (int)H, (int)p.piece, nseg, false)
+                             : tp_plan((int)T, (int)H, (int)p.piece, nseg, true);
+        auto weights = [&](int64_t rows) {
+            return live ? tp_plan_live((int)rows, (int)H, (int)T, nseg, true)
+                        : tp_plan((int)rows, (int)H, (int)T, nseg, true);
+        };
+        p.dw = weights(p.piece);
+        p.dw_last = weights(last);
     }
     p.stat_tiles = (int64_t)(p.pieces - 1) * p.logits.tiles_n + p.logits_last.tiles_n;
     int64_t o = 0;
@@ -225,6 +268,7 @@ XentPlan xent_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit, bo
     const int np = bf16 ? 1 : 3;
     p.o_factors = take(8);
     p.o_h = take(2 * np * T * p.Hh);
+    p.o_scaled = live && gradients && bf16 && !p.keep ? take(2 * T * p.Hh) : p.o_h;
     p.o_w = p.planes ? take(2 * np * V * p.Hp) : 0;
     p.o_s = !bf16 && p.keep ? take(4 * T * p.ldp) : 0;
     p.o_p = gradients ? take(2 * np * T * p.ldp) : 0;
@@ -239,6 +283,10 @@ XentPlan xent_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit, bo
     part = part > p.dw_last.part_bytes ? part : p.dw_last.part_bytes;
     p.o_part = take(part);
     p.o_dh = join ? take(4 * T * H) : 0;
+    if (live && gradients) {
+        p.o_tails = take(3 * sizeof(TpTail));
+        p.o_factor = take(4 * T);
+    }
     p.bytes = o;
     return p;
 }
@@ -314,6 +362,12 @@ hipError_t XentRun::gradients(void* dh, void* dW) const {
     uint16_t* P = at<uint16_t>(p->o_p);
     float *part = at<float>(p->o_part), *dhs = at<float>(p->o_dh);
     const int nseg = p->bf16 ? 1 : 6;
+    if (coef && p->o_scaled != p->o_h) {
+        hipLaunchKernelGGL(scale_rows_kernel, dim3((unsigned)T), dim3(256), 0, st, live, coef, at<float>(p->o_tl),
+                           at<float>(p->o_lse), at<float>(p->o_factor), at<uint16_t>(p->o_h),
+                           at<uint16_t>(p->o_scaled), p->Hh);
+        SC_RUN(hipGetLastError());
+    }
     for (int i = 0; i < p->pieces; ++i) {
         const int64_t v0 = (int64_t)i * p->piece;
         const int n = (int)(V - v0 < p->piece ? V - v0 : p->piece);
@@ -325,13 +379,15 @@ hipError_t XentRun::gradients(void* dh, void* dW) const {
             auto kernel = p->bf16 ? xent_dlogits_kernel<true> : xent_dlogits_kernel<false>;
             hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, p->bf16 ? nullptr : at<float>(p->o_s), P, T * p->ldp,
                                p->ldp, n, p->logits.bn, chunk, chunks, at<float>(p->o_smax), T, at<float>(p->o_lse),
-                               at<float>(p->o_tl), targets, V, factors + 1, live, coef);
+                               at<float>(p->o_tl), targets, V, factors + 1, live, coef,
+                               at<float>(p->o_factor), at<uint16_t>(p->o_h), p->Hh);
             SC_RUN(hipGetLastError());
         } else {
             TpArgs a = logit_args(i);
             a.P = P;
             a.alpha = factors + 1;
             a.coef = coef;
+            a.coef_zeros = coef && p->bf16;
             SC_RUN(launch_tile_product(TPK_LOGIT_GRAD, i + 1 < p->pieces ? p->logits : p->logits_last, a, TpSum{}, st));
         }
         TpArgs a;  // dh (+)= d W: k runs over the piece
@@ -349,7 +405,9 @@ hipError_t XentRun::gradients(void* dh, void* dW) const {
         a.C = dh;
         a.ldc = H;
         a.c_bf16 = p->bf16;
-        a.alpha = factors;
+        a.alpha = coef ? nullptr : factors;
+        a.coef = coef && p->bf16 ? at<float>(p->o_factor) : nullptr;
+        a.tail = at<TpTail>(p->o_tails);
         a.part = part;
         a.live = live;
         a.rows = rows;
@@ -358,12 +416,12 @@ hipError_t XentRun::gradients(void* dh, void* dW) const {
             sum.acc = i > 0 ? dhs : nullptr;
             sum.out_acc = i + 1 < p->pieces ? dhs : nullptr;
         }
-        SC_RUN(launch_tile_product(TPK_STATES, p->dh, a, sum, st));
+        SC_RUN(launch_tile_product(live && p->pieces == 1 ? TPK_STATES_LIVE : TPK_STATES, p->dh, a, sum, st));
         TpArgs b;  // dW = d^T h: k runs over the tokens
         b.A = P;
         b.lda = p->ldp;
         b.a_plane = T * p->ldp;
-        b.B = at<uint16_t>(p->o_h);
+        b.B = at<uint16_t>(p->o_scaled);
         b.ldb = p->Hh;
         b.b_plane = T * p->Hh;
         b.M = n;
@@ -374,10 +432,12 @@ hipError_t XentRun::gradients(void* dh, void* dW) const {
         b.C = (char*)dW + v0 * H * (p->bf16 ? 2 : 4);
         b.ldc = H;
         b.c_bf16 = p->bf16;
-        b.alpha = factors;
+        b.alpha = coef ? nullptr : factors;
         b.part = part;
         b.live = live;
-        SC_RUN(launch_tile_product(TPK_WEIGHTS, i + 1 < p->pieces ? p->dw : p->dw_last, b, TpSum{}, st));
+        b.tail = at<TpTail>(p->o_tails) + (i + 1 < p->pieces ? 1 : 2);
+        SC_RUN(launch_tile_product(live ? TPK_WEIGHTS_LIVE : TPK_WEIGHTS, i + 1 < p->pieces ? p->dw : p->dw_last, b,
+                                   TpSum{}, st));
     }
     return hipSuccess;
 }

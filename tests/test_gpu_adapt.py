@@ -58,6 +58,8 @@ class Tokens:
         terms, da, ha, wa = 1 if b16 else 6, d.abs() + ed, self.h.abs(), self.W.abs()
         tdh = ed @ wa + (terms * (self.V + 64) + 8) * 2 * U * (da @ wa) + dh.abs() * (half + 4 * U) + TINY
         tdW = ed.t() @ ha + (terms * (self.T + 64) + 8) * 2 * U * (da.t() @ ha) + dW.abs() * (half + 4 * U) + TINY
+        if b16:  # dW's product takes c h in bfloat16: one rounding of each
+            tdW += half * (da.t() @ ha)
         return dh, dW, tdh, tdW
 
 
@@ -678,3 +680,30 @@ def test_policy_many_tiles(dtype):
     dh, dW, tdh, tdW = ref.gradients(c, dc)
     within("dh", out.dh.cpu(), dh, tdh)
     within("dW", out.dW.cpu(), dW, tdW)
+
+
+# whole tiles of every shape and several rounds of them, with the last round cut along k: rows and columns that end
+# inside a tile, more tokens left out than a tile has
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("T,V,H,masked", [(1500, 5000, 1032, 700), (900, 16000, 520, 100), (700, 40000, 257, 400)])
+def test_policy_large_tiles(T, V, H, masked, dtype):
+    say(f"case: policy large tiles T {T} V {V} H {H} masked {masked} {dtype}")
+    g = gen(63)
+    h, W, tgt = _xent_case(g, T, V, H, dtype)
+    tgt[torch.randperm(T, generator=g, device="cuda")[:masked]] = -1
+    ref = Tokens(h, W, tgt, dtype)
+    old, adv, refl, _ = _policy_inputs(g, ref, (0.2, 0.2))
+    args = (h, W, tgt, old.cuda(), adv.cuda())
+    out = sco().policy_loss(*args, ref_logp=refl.cuda(), kl=0.02)
+    loss, dloss, _, _, _, _, c, dc, _ = _policy_ref(ref, old, adv, refl, None, (0.2, 0.2), 0.02)
+    within("loss", out.loss.cpu(), loss, dloss)
+    dh, dW, tdh, tdW = ref.gradients(c, dc)
+    within("dh", out.dh.cpu(), dh, tdh)
+    within("dW", out.dW.cpu(), dW, tdW)
+    # and nearer in the mean: each element of the gradients has a few roundings of its own
+    for got, want in ((out.dh, dh), (out.dW, dW)):
+        off = (got.cpu().to(F64) - want).norm() / want.norm()
+        assert off <= (4 * HALF[dtype] if dtype == torch.bfloat16 else 2.0 ** -16), off
+    for _ in range(3):
+        for a, b in zip(out, sco().policy_loss(*args, ref_logp=refl.cuda(), kl=0.02)):
+            assert torch.equal(a, b)
