@@ -16,8 +16,8 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libscopt.so")
 MARSHAL = os.path.join(PKG, "libscopt_marshal.so")
 
-SOURCES = ["act.hip", "api.cpp", "cholesky.hip", "clip.hip", "elementwise.hip", "embed.hip", "gemm.hip", "jacobi.hip",
-           "layernorm.hip", "mask.hip", "quad.hip", "tile_product.hip", "token_loss.hip", "train_api.cpp", "xent.hip"]
+SOURCES = ["act.hip", "api.cpp", "cholesky.hip", "clip.hip", "elementwise.hip", "embed.hip", "few_tokens.hip",
+           "gemm.hip", "jacobi.hip", "layernorm.hip", "mask.hip", "quad.hip", "tile_product.hip", "token_loss.hip", "train_api.cpp", "xent.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

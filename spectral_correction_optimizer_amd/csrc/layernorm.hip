@@ -5,7 +5,9 @@
 //
 // The gradient reads n from the 8-bit checkpoint that the norm may leave (act.hip), or forms it from
 // h, mu and rstd.  Each element passes once, so HBM bounds both: the row stays in registers between
-// its sums and the outputs; a wavefront owns a row of up to 1024 elements, a workgroup a longer one.
+// its sums and the outputs.  65536 x 2048 in bfloat16 with a residual: norm 197 us (5.5 TB/s), 236 us with the
+// checkpoint (5.1); gradient from the checkpoint 179 us (5.3), from h 196 us (5.5); a copy of 1 GiB
+// reaches 5.1.
 #include <cmath>
 
 #include "rows.hpp"
@@ -13,6 +15,27 @@
 #include "train.hpp"
 
 namespace scopt {
+
+// The norm's threads of a workgroup (its rows share no barriers), and workgroups of a launch, that further
+// rows are dealt to: 2048 are resident at once where a row takes few registers (65536 x 2048 in bfloat16:
+// 197 us; a workgroup for each row 244).
+constexpr int ln_block(int tpr) { return tpr == 64 ? 256 : tpr; }
+constexpr int64_t kLnGrid = 2048;
+
+// The gradient's shapes by row length: threads of a row, its groups of 8 a thread, rows of a workgroup and the
+// most workgroups.  Each workgroup leaves two partial rows of float32, so few of them with many rows save
+// traffic (2051 x 4100 in float32: 32.0 us with 256 workgroups of 768 threads, 35.1 with 512 of 256 and three groups).
+struct LnGradShape {
+    int most_h, tpr, c, rows, parts;
+};
+constexpr LnGradShape kLnGrad[7] = {{512, 64, 1, 4, 512},   {1024, 64, 2, 4, 512},  {2048, 256, 1, 4, 256},
+                                    {4096, 256, 2, 2, 256}, {6144, 768, 1, 1, 256}, {8192, 512, 2, 1, 256},
+                                    {16384, 512, 4, 1, 256}};
+constexpr int ln_grad_shape(int H) {
+    int i = 0;
+    while (H > kLnGrad[i].most_h) ++i;
+    return i;
+}
 
 // Sums of N values over the TPR threads of a row, used in turn as act.hip's row_sum.
 template <int TPR, int N, typename F>
@@ -24,7 +47,7 @@ __device__ __forceinline__ void row_sums(F (&v)[N], F (*red)[TPR / 64][N], int t
     if constexpr (TPR > 64) {
         if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-            for (int k = 0; k < N; ++k) red[turn][threadIdx.x >> 6][k] = v[k];
+            for (int k = 0; k < N; ++k) red[turn][threadIdx.x % TPR / 64][k] = v[k];
         }
         __syncthreads();
 #pragma unroll
@@ -38,59 +61,78 @@ __device__ __forceinline__ void row_sums(F (&v)[N], F (*red)[TPR / 64][N], int t
 
 // Rows are summed and normalised in 64 bits, as the root-mean-square norm's are: a value next to
 // the border of two of the checkpoint's steps falls to the side that it belongs to.  The variance is taken
-// about the mean, from the registers: nothing cancels.  h may be x or res: a row is loaded whole
-// before its first sum, and stored after the second.
-template <typename E, int ENDS, int TPR, int C>
-__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void layernorm_kernel(const E* x, const E* res,
+// about the mean, from the registers: nothing cancels.  h may be x or res: a row is stored after its first
+// sum, which every thread of the row has loaded for.  Gain and bias stay in registers over the rows of
+// a workgroup, and where the registers allow (C <= 2) a row is fetched while the one before it is worked on.
+template <typename E, int ENDS, int C> struct LnInput {
+    Group8<E, ENDS> x[C], r[C];
+};
+template <typename E, int ENDS, int TPR, int C, bool KEEP>
+__global__ __launch_bounds__(ln_block(TPR)) void layernorm_kernel(const E* x, const E* res,
                                                                           const E* __restrict__ gain,
                                                                           const E* __restrict__ bias, float eps,
                                                                           int64_t T, int H, E* h, E* y, float* mean,
                                                                           float* rstd, int8_t* q, uint8_t* e) {
-    constexpr int ROWS = TPR > 256 ? 1 : 256 / TPR;
+    constexpr int ROWS = ln_block(TPR) / TPR;
     __shared__ double red[2][TPR / 64][1];
     const int in = threadIdx.x % TPR;
     const int nb = (H + kActBlock - 1) / kActBlock;
-    for (int64_t t = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR; t < T;  // wave-uniform
-         t += (int64_t)gridDim.x * ROWS) {
-        Group8<E, ENDS> xw[C], rw[C], gw[C], bw[C];
+    Group8<E, ENDS> gw[C], bw[C];
 #pragma unroll
-        for (int j = 0; j < C; ++j) xw[j].load(x + t * H, (j * TPR + in) * 8, H);
+    for (int j = 0; j < C; ++j) gw[j].load(gain, (j * TPR + in) * 8, H);
+    if (bias) {
+#pragma unroll
+        for (int j = 0; j < C; ++j) bw[j].load(bias, (j * TPR + in) * 8, H);
+    }
+    using Input = LnInput<E, ENDS, C>;
+    auto fetch = [&](int64_t t, Input& r) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < C; ++j) r.x[j].load(x + t * H, (j * TPR + in) * 8, H);
         if (res) {
 #pragma unroll
-            for (int j = 0; j < C; ++j) rw[j].load(res + t * H, (j * TPR + in) * 8, H);
+            for (int j = 0; j < C; ++j) r.r[j].load(res + t * H, (j * TPR + in) * 8, H);
         }
-#pragma unroll
-        for (int j = 0; j < C; ++j) gw[j].load(gain, (j * TPR + in) * 8, H);
-        if (bias) {
-#pragma unroll
-            for (int j = 0; j < C; ++j) bw[j].load(bias, (j * TPR + in) * 8, H);
+    };
+    constexpr bool AHEAD = C <= 2;
+    const int64_t stride = (int64_t)gridDim.x * ROWS;
+    int64_t t = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
+    Input cur, next;
+    if (AHEAD && t < T) fetch(t, next);
+    for (; t < T; t += stride) {  // wave-uniform
+        if (AHEAD) {
+            cur = next;
+            if (t + stride < T) fetch(t + stride, next);
+        } else {
+            fetch(t, cur);
         }
-        auto sums = [&](int j, double (&v)[8]) __attribute__((always_inline)) {
-            float a[8], r[8];
-            value8(xw[j], (j * TPR + in) * 8, H, a);
-            if (res) value8(rw[j], (j * TPR + in) * 8, H, r);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = res ? (double)a[i] + (double)r[i] : (double)a[i];
-        };
-        double s[1] = {0.0};
+        double v[C][8], s[1] = {0.0};
 #pragma unroll
         for (int j = 0; j < C; ++j) {
-            double v[8];
-            sums(j, v);
+            float a[8], r[8];
+            value8(cur.x[j], (j * TPR + in) * 8, H, a);
+            if (res) value8(cur.r[j], (j * TPR + in) * 8, H, r);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s[0] += v[i];
+            for (int i = 0; i < 8; ++i) {
+                v[j][i] = res ? (double)a[i] + (double)r[i] : (double)a[i];
+                s[0] += v[j][i];
+            }
         }
         row_sums<TPR>(s, red, 0);
         const double mu = s[0] / (double)H;
         s[0] = 0.0;
 #pragma unroll
         for (int j = 0; j < C; ++j) {
-            double v[8];
-            sums(j, v);
+            const int c = (j * TPR + in) * 8, left = H - c;
+            if (h && left > 0) {
+                float f[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] = (float)v[j][i];
+                store8(h + t * H + c, left, f);
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const double d = (j * TPR + in) * 8 + i < H ? v[i] - mu : 0.0;
-                s[0] = fma(d, d, s[0]);
+                v[j][i] = i < left ? v[j][i] - mu : 0.0;  // the norm of the sum, not of the rounded h
+                s[0] = fma(v[j][i], v[j][i], s[0]);
             }
         }
         row_sums<TPR>(s, red, 1);
@@ -102,24 +144,19 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void layernorm_kernel(const 
 #pragma unroll
         for (int j = 0; j < C; ++j) {
             const int c = (j * TPR + in) * 8, left = H - c;
-            double v[8];
             float f[8], g[8], b[8];
-            sums(j, v);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = (float)v[i];
-            if (h && left > 0) store8(h + t * H + c, left, f);
             value8(gw[j], c, H, g);
             if (bias) value8(bw[j], c, H, b);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                v[i] = i < left ? (v[i] - mu) * rs : 0.0;  // the norm of the sum, not of the rounded h
-                f[i] = bias ? fmaf((float)v[i], g[i], b[i]) : (float)v[i] * g[i];
+                v[j][i] *= rs;
+                f[i] = bias ? fmaf((float)v[j][i], g[i], b[i]) : (float)v[j][i] * g[i];
             }
             if (left > 0) store8(y + t * H + c, left, f);
-            if (q) {
+            if constexpr (KEEP) {
                 int8_t k[8];
                 uint8_t ex;
-                act_encode8(v, k, ex);
+                act_encode8(v[j], k, ex);
                 if (left > 0) {
                     store_q8(q + t * H + c, left, k);
                     if ((in & 3) == 0) gst(e + t * nb + c / kActBlock, ex);
@@ -154,10 +191,10 @@ template <typename E> struct LnGradArgs {
 // Rows are dealt to the workgroups in turn; each keeps its rows' sums of dy n and dy in registers
 // and writes two rows of `partial`, summed in a fixed order by layernorm_dgain_kernel.  Where the
 // registers allow (C <= 2) a row is fetched while the one before it is worked on.
-template <typename E, int ENDS, int TPR, int C, bool KEPT>
-__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void layernorm_grad_kernel(const LnGradArgs<E> P) {
-    constexpr int ROWS = TPR > 256 ? 1 : 256 / TPR;
-    __shared__ float red[2][TPR / 64][2];
+template <typename E, int ENDS, int TPR, int C, int ROWS, bool KEPT>
+__global__ __launch_bounds__(TPR * ROWS) void layernorm_grad_kernel(const LnGradArgs<E> P) {
+    constexpr bool JOINT = ROWS > 1 && TPR > 64;  // the rows share barriers: all of them take every turn
+    __shared__ float red[ROWS][2][TPR / 64][2];
     __shared__ float sums[ROWS > 1 ? TPR * 16 : 1];
     const int in = threadIdx.x % TPR, row = threadIdx.x / TPR;
     const int H = P.H, nb = (H + kActBlock - 1) / kActBlock;
@@ -186,23 +223,28 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void layernorm_grad_kernel(c
             for (int j = 0; j < C; ++j) r.dh[j].load(P.dh + t * H, (j * TPR + in) * 8, H);
         }
     };
-    constexpr bool AHEAD = C <= 2;
+    constexpr bool AHEAD = C <= 2 && TPR < 1024;
     Row cur, next;
     int64_t t = (int64_t)blockIdx.x * ROWS + row;
     int turn = 0;
-    if (AHEAD && t < T) fetch(t, next);
-    for (; t < T; t += stride, turn ^= 1) {
+    if (AHEAD) fetch(t < T ? t : T - 1, next);
+    for (; t - (JOINT ? row : 0) < T; t += stride, turn ^= 1) {
+        const bool live = !JOINT || t < T;
         if (AHEAD) {
             cur = next;
-            fetch(t + stride < T ? t + stride : t, next);
+            fetch(t + stride < T ? t + stride : T - 1, next);
         } else {
-            fetch(t, cur);
+            fetch(live ? t : T - 1, cur);
         }
         float a[C][8], n[C][8], s[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int j = 0; j < C; ++j) {
             const int c = (j * TPR + in) * 8;
             value8(cur.dy[j], c, H, a[j]);
+            if constexpr (JOINT) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) a[j][i] = live ? a[j][i] : 0.0f;
+            }
             if constexpr (KEPT) {
                 cur.q[j].value(c, H, n[j]);
             } else {
@@ -227,7 +269,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void layernorm_grad_kernel(c
                 for (int j = 0; j < C; ++j) cur.dh[j].arrived();
             }
         }
-        row_sums<TPR>(s, red, turn);
+        row_sums<TPR>(s, red[row], turn);
         const float c0 = s[0] / (float)H, c1 = s[1] / (float)H;
 #pragma unroll
         for (int j = 0; j < C; ++j) {
@@ -241,7 +283,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void layernorm_grad_kernel(c
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) d[i] = fmaf(cur.rs, fmaf(-n[j][i], c1, a[j][i] - c0), d[i]);
-            if (left > 0) store8(P.dx + t * H + c, left, d);
+            if (left > 0 && live) store8(P.dx + t * H + c, left, d);
         }
     }
     float* out = P.partial + (int64_t)blockIdx.x * 2 * H;
@@ -302,41 +344,45 @@ __global__ __launch_bounds__(1024) void layernorm_dgain_kernel(const float* __re
     }
 }
 
-// Threads and groups of 8 a row: a wave up to 1024 elements, a workgroup beyond.
-template <typename E, int ENDS, template <typename, int, int, int> class L, typename... A>
+// The norm's threads and groups of 8 a row.  A wavefront takes rows of up to 2048 elements by itself: no
+// barriers (65536 x 2048: 197 us in bfloat16, 394 in float32; four wavefronts a row 220 and 421).
+template <typename E, int ENDS, int TPR, int C, typename... A>
+static void ln_rows(int64_t T, hipStream_t st, int8_t* q, A... args) {
+    constexpr int64_t rows = ln_block(TPR) / TPR;
+    const int64_t b = (T + rows - 1) / rows;
+    const dim3 grid((unsigned)(b < kLnGrid ? b : kLnGrid)), blk(ln_block(TPR));
+    if (q) hipLaunchKernelGGL((layernorm_kernel<E, ENDS, TPR, C, true>), grid, blk, 0, st, args...);
+    else hipLaunchKernelGGL((layernorm_kernel<E, ENDS, TPR, C, false>), grid, blk, 0, st, args...);
+}
+template <typename E, int ENDS, typename... A>
 static void ln_sizes(int H, A... args) {
-    if (ENDS == ROW_SHORT || H <= 512) L<E, ENDS, 64, 1>::launch(args...);
+    if (ENDS == ROW_SHORT || H <= 512) ln_rows<E, ENDS, 64, 1>(args...);
     else if constexpr (ENDS != ROW_SHORT) {
-        if (H <= 1024) L<E, ENDS, 64, 2>::launch(args...);
-        else if (H <= 2048) L<E, ENDS, 256, 1>::launch(args...);
-        else if (H <= 4096) L<E, ENDS, 256, 2>::launch(args...);
-        else if (H <= 6144) L<E, ENDS, 256, 3>::launch(args...);
-        else if (H <= 8192) L<E, ENDS, 256, 4>::launch(args...);
-        else L<E, ENDS, 1024, 2>::launch(args...);
+        if (H <= 1024) ln_rows<E, ENDS, 64, 2>(args...);
+        else if (H <= 1536) ln_rows<E, ENDS, 64, 3>(args...);
+        else if (H <= 2048) ln_rows<E, ENDS, 64, 4>(args...);
+        else if (H <= 4096) ln_rows<E, ENDS, 256, 2>(args...);
+        else if (H <= 6144) ln_rows<E, ENDS, 256, 3>(args...);
+        else if (H <= 8192) ln_rows<E, ENDS, 256, 4>(args...);
+        else ln_rows<E, ENDS, 512, 4>(args...);
     }
 }
-template <typename E, int ENDS, int TPR, int C> struct LnForward {
-    template <typename... A> static void launch(int64_t T, hipStream_t st, A... args) {
-        constexpr int64_t rows = TPR > 256 ? 1 : 256 / TPR;
-        const int64_t b = (T + rows - 1) / rows;
-        hipLaunchKernelGGL((layernorm_kernel<E, ENDS, TPR, C>), dim3((unsigned)(b < 1 << 20 ? b : 1 << 20)),
-                           dim3(TPR > 256 ? TPR : 256), 0, st, args...);
-    }
-};
-template <typename E, int ENDS, int TPR, int C> struct LnBackward {
-    static void launch(int parts, hipStream_t st, const LnGradArgs<E>& a) {
-        const dim3 grid((unsigned)parts), blk(TPR > 256 ? TPR : 256);
-        if (a.q) hipLaunchKernelGGL((layernorm_grad_kernel<E, ENDS, TPR, C, true>), grid, blk, 0, st, a);
-        else hipLaunchKernelGGL((layernorm_grad_kernel<E, ENDS, TPR, C, false>), grid, blk, 0, st, a);
-    }
-};
+template <typename E, int ENDS, int I>
+static void ln_grad_sizes(int H, int parts, hipStream_t st, const LnGradArgs<E>& a) {
+    constexpr LnGradShape S = kLnGrad[I];
+    if constexpr (I + 1 < 7 && ENDS != ROW_SHORT)
+        if (H > S.most_h) return ln_grad_sizes<E, ENDS, I + 1>(H, parts, st, a);
+    const dim3 grid((unsigned)parts), blk(S.tpr * S.rows);
+    if (a.q) hipLaunchKernelGGL((layernorm_grad_kernel<E, ENDS, S.tpr, S.c, S.rows, true>), grid, blk, 0, st, a);
+    else hipLaunchKernelGGL((layernorm_grad_kernel<E, ENDS, S.tpr, S.c, S.rows, false>), grid, blk, 0, st, a);
+}
 
 hipError_t launch_layernorm(bool bf16, const void* x, const void* residual, const void* gain, const void* bias,
                             float eps, int64_t T, int H, void* h, void* y, float* mean, float* rstd, int8_t* q,
                             uint8_t* e, hipStream_t st) {
     if (T <= 0) return hipSuccess;
 #define SC_NORM(E_, ENDS_)                                                                                      \
-    ln_sizes<E_, ENDS_, LnForward>(H, T, st, (const E_*)x, (const E_*)residual, (const E_*)gain, (const E_*)bias, \
+    ln_sizes<E_, ENDS_>(H, T, st, q, (const E_*)x, (const E_*)residual, (const E_*)gain, (const E_*)bias, \
                                    eps, T, H, (E_*)h, (E_*)y, mean, rstd, q, e);
     SC_BY_ENDS(bf16, H, SC_NORM)
 #undef SC_NORM
@@ -344,8 +390,9 @@ hipError_t launch_layernorm(bool bf16, const void* x, const void* residual, cons
 }
 
 int64_t layernorm_grad_parts(int64_t T, int H) {
-    const int64_t wgs = H <= 1024 ? (T + 3) / 4 : T, most = H <= 4096 ? 1024 : H <= 8192 ? 512 : 256;
-    return wgs < most ? wgs : most;
+    const LnGradShape& S = kLnGrad[ln_grad_shape(H)];
+    const int64_t wgs = (T + S.rows - 1) / S.rows;
+    return wgs < S.parts ? wgs : S.parts;
 }
 
 hipError_t launch_layernorm_grad(bool bf16, const void* dy, const void* gain, const float* rstd, const float* mean,
@@ -356,7 +403,7 @@ hipError_t launch_layernorm_grad(bool bf16, const void* dy, const void* gain, co
 #define SC_GRAD(E_, ENDS_)                                                                                      \
     LnGradArgs<E_> a{(const E_*)dy, (const E_*)gain, rstd, mean, q, e, (const E_*)h, (const E_*)dh, T, H, (E_*)dx, \
                      partial};                                                                                  \
-    ln_sizes<E_, ENDS_, LnBackward>(H, parts, st, a);
+    ln_grad_sizes<E_, ENDS_, 0>(H, parts, st, a);
         SC_BY_ENDS(bf16, H, SC_GRAD)
 #undef SC_GRAD
         const hipError_t err = hipGetLastError();

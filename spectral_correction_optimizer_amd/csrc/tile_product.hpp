@@ -581,19 +581,20 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
             for (int i = 0; i < MI; ++i) {
                 row_block(i);
                 const int m = lm + 16 * i, in = min(m, M - 1);
-                const float f = P.coef && !cut ? gld(P.coef + in) : 1.0f;
+                float f = 1.0f;  // (only the states' rows are tokens)
+                if constexpr (AKC) f = P.coef && !cut ? gld(P.coef + in) : 1.0f;
                 float v[NI][4];
 #pragma unroll
                 for (int j = 0; j < NI; ++j)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) v[j][r] = acc[i][j][r] * f;
+                    for (int r = 0; r < 4; ++r) v[j][r] = AKC ? acc[i][j][r] * f : acc[i][j][r];
                 if (cut) {
 #pragma unroll
                     for (int j = 0; j < NI; ++j)
                         gst4(part + (m - m0) * BN + ln - n0 + 16 * j, v4f{v[j][0], v[j][1], v[j][2], v[j][3]});
                     continue;
                 }
-                const int64_t at = tp_row(P, in) * P.ldc + n0 + wn;
+                const int64_t at = (AKC ? tp_row(P, in) : in) * P.ldc + n0 + wn;
                 if (P.c_bf16 && whole) {
                     uint32_t d[NI][2];
 #pragma unroll

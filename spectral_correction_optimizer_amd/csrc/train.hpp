@@ -1,5 +1,5 @@
 // Training-step operators of libscopt: arguments and launchers shared by their kernels
-// (tile_product.hip, xent.hip, token_loss.hip, act.hip, layernorm.hip, clip.hip, embed.hip) and
+// (tile_product.hip, few_tokens.hip, xent.hip, token_loss.hip, act.hip, layernorm.hip, clip.hip, embed.hip) and
 // their C entries (train_api.cpp).
 #pragma once
 
@@ -122,6 +122,12 @@ struct TpSum {
     float* out_acc = nullptr;
 };
 hipError_t launch_tile_product(TpKind kind, const TpPlan& plan, TpArgs args, const TpSum& sum, hipStream_t st);
+
+// dW[v][n] = sum over the first *live of T <= kFewTokens tokens of d[t][v] h[t][n], bfloat16 (few_tokens.hip): d
+// [T][ldd], h [T][ldh] as operands of a product, dW [V][N]
+constexpr int64_t kFewTokens = 128;
+hipError_t launch_few_tokens(const uint16_t* d, int64_t ldd, const uint16_t* h, int64_t ldh, int T, const int* live,
+                             int V, int N, uint16_t* dW, hipStream_t st);
 
 // `bytes` (even) zeros
 hipError_t launch_zero(void* p, int64_t bytes, hipStream_t st);

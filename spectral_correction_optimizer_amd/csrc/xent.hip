@@ -417,6 +417,11 @@ hipError_t XentRun::gradients(void* dh, void* dW) const {
             sum.out_acc = i + 1 < p->pieces ? dhs : nullptr;
         }
         SC_RUN(launch_tile_product(live && p->pieces == 1 ? TPK_STATES_LIVE : TPK_STATES, p->dh, a, sum, st));
+        if (live && p->bf16 && T <= kFewTokens) {
+            SC_RUN(launch_few_tokens(P, p->ldp, at<uint16_t>(p->o_scaled), p->Hh, (int)T, live, n, (int)H,
+                                     (uint16_t*)dW + v0 * H, st));
+            continue;
+        }
         TpArgs b;  // dW = d^T h: k runs over the tokens
         b.A = P;
         b.lda = p->ldp;

@@ -707,3 +707,27 @@ def test_policy_large_tiles(T, V, H, masked, dtype):
     for _ in range(3):
         for a, b in zip(out, sco().policy_loss(*args, ref_logp=refl.cuda(), kl=0.02)):
             assert torch.equal(a, b)
+
+
+# few tokens: the weights' gradient goes down the vocabulary with all tokens in registers; columns and rows that end
+# inside a panel or a step, more panels than one, tokens of one and of two tiles, pieces
+@pytest.mark.parametrize("limit", [0, 1])
+@pytest.mark.parametrize("T,V,H,kind", [(1, 3000, 300, "none"), (64, 5000, 520, "half"), (65, 4099, 1025, "none"),
+                                        (96, 20000, 264, "runs"), (128, 70001, 72, "half"), (128, 200, 2048, "none"),
+                                        (100, 6400, 64, "all"), (128, 1000, 8191, "half")])
+def test_policy_few_tokens(T, V, H, kind, limit):
+    say(f"case: policy few tokens T {T} V {V} H {H} {kind} limit {limit}")
+    g = gen(64)
+    h, W, tgt = _xent_case(g, T, V, H, torch.bfloat16)
+    tgt = _mask(tgt, kind, V)
+    ref = Tokens(h, W, tgt, torch.bfloat16)
+    old, adv, refl, _ = _policy_inputs(g, ref, (0.2, 0.2))
+    args = (h, W, tgt, old.cuda(), adv.cuda())
+    out = sco().policy_loss(*args, ref_logp=refl.cuda(), kl=0.02, limit=limit)
+    _, _, _, _, _, _, c, dc, _ = _policy_ref(ref, old, adv, refl, None, (0.2, 0.2), 0.02)
+    dh, dW, tdh, tdW = ref.gradients(c, dc)
+    within("dh", out.dh.cpu(), dh, tdh)
+    within("dW", out.dW.cpu(), dW, tdW)
+    for _ in range(2):
+        for a, b in zip(out, sco().policy_loss(*args, ref_logp=refl.cuda(), kl=0.02, limit=limit)):
+            assert torch.equal(a, b)
