@@ -96,8 +96,9 @@ __global__ __launch_bounds__(kClipThreads) void clip_kernel(const ClipTable t, c
         gst(norm, (float)n);
         gst(scale_out, scale);
     }
-    const uint32_t c = blockIdx.x;
-    if (c >= t.first[t.count]) return;
+    if (t.count == 0) return;
+    // what was read last comes first: part of it is still in cache (112 matrices, 3.9 GB: 2115 us, 2129 in order)
+    const uint32_t c = t.first[t.count] - 1 - blockIdx.x;
     const int i = clip_find(t, c);
     const int64_t at = (int64_t)(c - t.first[i]) * kClipChunk;
     const E* p = (const E*)t.src[i] + at;

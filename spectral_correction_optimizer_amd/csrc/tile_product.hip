@@ -1,6 +1,7 @@
 // The tiled products of the training-step operators: instances of the kernel of
 // tile_product.hpp, the choice of tile and split, the sum over splits, and the copies of
 // operands into bfloat16 planes.
+#include "planes.hpp"
 #include "rows.hpp"
 #include "tile_product.hpp"
 
@@ -11,6 +12,9 @@ constexpr int kCus = 256;
 using Big = TpShape<256, 256, 2, 4, 2, 1>;   // 128 KB of LDS: one workgroup of 8 waves per CU
 using Mid = TpShape<128, 128, 2, 2, 2, 2>;   // 64 KB: two workgroups of 4 waves per CU
 using Small = TpShape<64, 128, 1, 4, 3, 2>;  // 72 KB: two workgroups of 4 waves per CU
+// Logits of few tokens: one row of tiles, deep buffers, and every tile its own order of k
+using Few64 = TpShape<64, 128, 1, 4, 4, 1, true>;    // 96 KB: a workgroup of 4 waves per CU
+using Few128 = TpShape<128, 128, 2, 2, 3, 1, true>;  // 96 KB: likewise
 }  // namespace
 
 // a column's factor
@@ -91,6 +95,68 @@ __global__ __launch_bounds__(256) void tp_tail_kernel(const TpArgs P) {
     }
 }
 
+// TP_STATS of the parts' sums: a wavefront a row of a tile, BN / 64 columns a lane.
+template <int BM, int BN>
+__global__ __launch_bounds__(256) void tp_stats_tail_kernel(const TpArgs P) {
+    constexpr int C = BN / 64;
+    static_assert(C == 2 || C == 4, "columns of a lane");
+    const TpTail t = {gld(&P.tail->full), gld(&P.tail->rest), gld(&P.tail->splits)};
+    if (t.splits == 1) return;
+    const int M = min(P.M, gld(P.live)), tiles_m = (M + BM - 1) / BM;
+    const int lane = threadIdx.x & 63;
+    const int64_t stride = (int64_t)t.rest * BM * BN;
+    const bool pow2 = P.keep == TP_KEEP_EXP;
+    for (int row = blockIdx.x * 4 + threadIdx.x / 64; row < t.rest * BM; row += gridDim.x * 4) {
+        const int tile = row / BM;
+        int tm, tn;
+        tp_tile(t.full + tile, tiles_m, P.tiles_n, tm, tn);
+        const int m = tm * BM + row % BM, n = tn * BN + lane * C;
+        if (m >= M) continue;
+        const float* p = P.part + (int64_t)row * BN + lane * C;
+        float v[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) v[c] = 0.0f;
+#pragma unroll 4
+        for (int s = 0; s < t.splits; ++s) {
+            typedef float vec __attribute__((ext_vector_type(C)));
+            const vec x = *(const SC_GLOBAL vec*)(p + s * stride);
+#pragma unroll
+            for (int c = 0; c < C; ++c) v[c] += x[c];
+        }
+        float mx = -__builtin_huge_valf();
+#pragma unroll
+        for (int c = 0; c < C; ++c) mx = fmaxf(mx, v[c]);
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
+        const float ref = tp_reference(mx, pow2);
+        const int64_t hit = gld(P.targets + m) - P.n_first - n;
+        float e[C], z = 0.0f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            e[c] = pow2 ? __builtin_amdgcn_exp2f(fmaf(v[c], kLog2e, -ref))
+                        : __builtin_amdgcn_exp2f((v[c] - ref) * kLog2e);
+            z += e[c];
+            if (hit == c && n + c < P.N) gst(P.target_logit + m, v[c]);
+        }
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) z += __shfl_xor(z, o);
+        if (pow2) {
+            uint32_t* to = (uint32_t*)((uint16_t*)P.P + (int64_t)m * P.ldp + n);
+#pragma unroll
+            for (int c = 0; c < C; c += 2) gst(to + c / 2, tp_pack_unit(e[c], e[c + 1]));
+        } else if (P.keep == TP_KEEP_LOGIT) {
+            float* to = (float*)P.P + (int64_t)m * P.ldp + n;
+#pragma unroll
+            for (int c = 0; c < C; ++c) gst(to + c, v[c]);
+        }
+        if (lane == 0) {
+            const int64_t at = (int64_t)(P.stat_first + tn) * P.M + m;
+            gst(P.stat_max + at, mx == -__builtin_huge_valf() ? mx : ref);
+            gst(P.stat_sum + at, z);
+        }
+    }
+}
+
 // Choice of tile and split: the least estimated time.  A workgroup's 64-deep step takes
 // `step` us with the chip full and a tile `tile` us beside its steps (its first reads, its
 // stores); steps come in whole turns of `turn` buffers for every segment.  Fitted to bf16
@@ -105,8 +171,9 @@ struct ShapeTimes {
     int bm, bn, per_cu, turn;
     double step, tile;
 };
-constexpr ShapeTimes kShapes[3] = {
-    {256, 256, 1, 2, 1.70, 12.0}, {128, 128, 2, 2, 1.20, 3.7}, {64, 128, 2, 3, 0.81, 1.2}};
+constexpr ShapeTimes kShapes[5] = {
+    {256, 256, 1, 2, 1.70, 12.0}, {128, 128, 2, 2, 1.20, 3.7}, {64, 128, 2, 3, 0.81, 1.2},
+    {64, 128, 1, 4, 0.5, 1.2},    {128, 128, 1, 3, 0.8, 3.7}};  // the last two not fitted
 }  // namespace
 
 TpPlan tp_plan(int M, int N, int K, int nseg, bool may_split) {
@@ -138,10 +205,16 @@ TpPlan tp_plan(int M, int N, int K, int nseg, bool may_split) {
 }
 
 // The least time for the most tokens there can be; with fewer of them the last round is cut anew on the device.
-TpPlan tp_plan_live(int M, int N, int K, int nseg, bool live_k) {
+TpPlan tp_plan_live(TpKind kind, int M, int N, int K, int nseg, TpTailQuery& tail) {
+    const bool live_k = kind == TPK_WEIGHTS_LIVE, logits = kind == TPK_LOGIT_STATS_LIVE;
+    const int rounds = logits ? 1 : 2;
     TpPlan best;
     double best_us = 1e300;
-    for (int s = 0; s < 3; ++s) {
+    // Few tokens and enough columns for the weights to be read at memory's rate.  (32000 x 2048 that is not in
+    // cache: log-probabilities of 64 tokens 42.8 us, with the small tiles 48.5; the loss of a pair of 96 tokens 135
+    // and 143.  The order of k makes the difference, not the depth of the buffers: small tiles with it take 42.7.)
+    const bool few = logits && M <= 128 && N >= 128 * 128;
+    for (int s = few ? (M <= 64 ? 3 : 4) : 0; s < (few ? (M <= 64 ? 4 : 5) : 3); ++s) {
         const ShapeTimes& S = kShapes[s];
         const int slots = kCus * S.per_cu;
         TpTailQuery q;
@@ -157,12 +230,15 @@ TpPlan tp_plan_live(int M, int N, int K, int nseg, bool live_k) {
         q.tile_ns = (int)(1000.0 * S.tile);
         q.join_ns = 8 * S.bm * S.bn / 5000;  // a tile's partial sums written and read once more, at about 5 TB/s
         const int live = live_k ? K : M, tiles = q.tiles(live), total = q.total(live);
-        // parts of any number of live tokens: fewer than two turns each are none, nor more than two rounds
+        // what the tokens do not change goes by at about 5 TB/s (the logits of 64 tokens, 32000 x 2048: whole 25 us,
+        // cut in two and joined 35)
+        const int64_t bytes = live_k ? (int64_t)M * N * (nseg > 1 ? 4 : 2) : (int64_t)N * K * (nseg > 1 ? 6 : 2);
+        q.pass_ns = (int)(bytes / 5000 < 1 << 30 ? bytes / 5000 : 1 << 30);
+        // parts of any number of live tokens, none of fewer than two turns
         const int64_t parts = total < 4 ? 0 : (int64_t)tiles * (total / 2 < 64 ? total / 2 : 64);
-        q.most = (int)(parts < 2 * slots ? parts : 2 * slots);
-        const int rest = tiles % slots;
+        q.most = few ? 0 : (int)(parts < rounds * slots ? parts : rounds * slots);
         int ns = 0x7fffffff;
-        for (int p = 1; p <= 64; ++p) ns = q.ns(rest, total, p) < ns ? q.ns(rest, total, p) : ns;
+        for (int p = 1; p <= 64; ++p) ns = q.ns(tiles, total, p) < ns ? q.ns(tiles, total, p) : ns;
         const double us = (double)(tiles / slots) * ((double)total * S.step * S.turn + S.tile) + 1e-3 * ns;
         if (us < best_us) {
             best_us = us;
@@ -172,7 +248,7 @@ TpPlan tp_plan_live(int M, int N, int K, int nseg, bool live_k) {
             best.tiles_m = (M + S.bm - 1) / S.bm;
             best.tiles_n = q.tiles_n;
             best.part_bytes = 4ll * S.bm * S.bn * q.most;
-            best.tail = q;
+            tail = q;
         }
     }
     return best;
@@ -180,12 +256,25 @@ TpPlan tp_plan_live(int M, int N, int K, int nseg, bool live_k) {
 
 namespace {
 template <class S>
-hipError_t launch_tail(TpKind kind, const TpPlan& plan, const TpArgs& P, hipStream_t st) {
-    const dim3 grid((unsigned)plan.tail.slots), blk(S::NT);
-    if (kind == TPK_STATES_LIVE) hipLaunchKernelGGL((tile_product_kernel<S, true, false, TP_TAIL>), grid, blk, 0, st, P);
-    else hipLaunchKernelGGL((tile_product_kernel<S, false, false, TP_TAIL>), grid, blk, 0, st, P);
+hipError_t launch_few(const TpPlan& plan, const TpArgs& P, hipStream_t st) {
+    hipLaunchKernelGGL((tile_product_kernel<S, true, true, TP_STATS_TAIL>), dim3(kCus * S::PER_CU), dim3(S::NT), 0, st, P);
     if (plan.part_bytes > 0)
-        hipLaunchKernelGGL((tp_tail_kernel<S::BM, S::BN>), dim3(2048), dim3(256), 0, st, P);
+        hipLaunchKernelGGL((tp_stats_tail_kernel<S::BM, S::BN>), dim3(2048), dim3(256), 0, st, P);
+    return hipGetLastError();
+}
+template <class S>
+hipError_t launch_tail(TpKind kind, const TpPlan& plan, const TpArgs& P, hipStream_t st) {
+    const dim3 grid(kCus * S::PER_CU), blk(S::NT);
+    if (kind == TPK_LOGIT_STATS_LIVE)
+        hipLaunchKernelGGL((tile_product_kernel<S, true, true, TP_STATS_TAIL>), grid, blk, 0, st, P);
+    else if (kind == TPK_STATES_LIVE)
+        hipLaunchKernelGGL((tile_product_kernel<S, true, false, TP_TAIL>), grid, blk, 0, st, P);
+    else
+        hipLaunchKernelGGL((tile_product_kernel<S, false, false, TP_TAIL>), grid, blk, 0, st, P);
+    if (plan.part_bytes > 0) {
+        auto join = kind == TPK_LOGIT_STATS_LIVE ? tp_stats_tail_kernel<S::BM, S::BN> : tp_tail_kernel<S::BM, S::BN>;
+        hipLaunchKernelGGL(join, dim3(2048), dim3(256), 0, st, P);
+    }
     return hipGetLastError();
 }
 template <class S>
@@ -226,14 +315,16 @@ hipError_t launch_tile_product(TpKind kind, const TpPlan& plan, TpArgs P, const 
     P.tiles_n = plan.tiles_n;
     P.splits = plan.splits;
     P.live_rows = P.live && (kind == TPK_STATES || kind == TPK_STATES_LIVE);
-    if (kind == TPK_STATES_LIVE || kind == TPK_WEIGHTS_LIVE)
-        return plan.shape == 0   ? launch_tail<Big>(kind, plan, P, st)
-               : plan.shape == 1 ? launch_tail<Mid>(kind, plan, P, st)
-                                 : launch_tail<Small>(kind, plan, P, st);
+    if (kind == TPK_LOGIT_STATS_LIVE && plan.shape >= 3)
+        return plan.shape == 3 ? launch_few<Few64>(plan, P, st) : launch_few<Few128>(plan, P, st);
+    if (kind >= TPK_LOGIT_STATS_LIVE)
+        return plan.bm == 256   ? launch_tail<Big>(kind, plan, P, st)
+               : plan.bm == 128 ? launch_tail<Mid>(kind, plan, P, st)
+                                : launch_tail<Small>(kind, plan, P, st);
     const bool part = (kind == TPK_STATES || kind == TPK_WEIGHTS) && (plan.splits > 1 || sum.acc || sum.out_acc);
-    hipError_t e = plan.shape == 0   ? launch_shape<Big>(kind, P, part, st)
-                   : plan.shape == 1 ? launch_shape<Mid>(kind, P, part, st)
-                                     : launch_shape<Small>(kind, P, part, st);
+    hipError_t e = plan.bm == 256   ? launch_shape<Big>(kind, P, part, st)
+                   : plan.bm == 128 ? launch_shape<Mid>(kind, P, part, st)
+                                    : launch_shape<Small>(kind, P, part, st);
     if (e != hipSuccess || !part) return e;
     return launch_tp_reduce(P, sum.acc, sum.out_acc, st);
 }
@@ -251,79 +342,19 @@ hipError_t launch_zero(void* p, int64_t bytes, hipStream_t st) {
     return hipGetLastError();
 }
 
-// The exact split of any float32 values (split8 rounds the first part, which overflows from
-// 0x1.FFp127 on and leaves infinity - infinity): the first part stays at bfloat16's largest value, and
-// an infinity is its own first part, beside zeros.
-__device__ __forceinline__ Split8 split8_any(const float (&f)[8]) {
-    constexpr float most = 0x1.FEp127f;
-    v4u h, m, l;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float first[2], rest[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const float x = f[2 * i + u], a = fabsf(x);
-            first[u] = a >= 0x1.FFp127f && a < __builtin_huge_valf() ? copysignf(most, x) : x;
-        }
-        h[i] = pack_bf16x2(first[0], first[1]);
-        rest[0] = f[2 * i] - bf16_lo(h[i]);
-        rest[1] = f[2 * i + 1] - bf16_hi(h[i]);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) rest[u] = fabsf(f[2 * i + u]) == __builtin_huge_valf() ? 0.0f : rest[u];
-        m[i] = pack_bf16x2(rest[0], rest[1]);
-        l[i] = pack_bf16x2(rest[0] - bf16_lo(m[i]), rest[1] - bf16_hi(m[i]));
-    }
-    return Split8{__builtin_bit_cast(v8bf, h), __builtin_bit_cast(v8bf, m), __builtin_bit_cast(v8bf, l)};
-}
-
-// planes[p][r][c]: kGroups groups of eight columns a thread (ld is a multiple of 8).  With `place` row r
-// goes to row place[r]; where that is negative its row of `cleared` is set to zeros instead.
+// place: where each row goes, or NULL
 template <typename E, int ENDS>
 __global__ __launch_bounds__(256) void to_planes_kernel(const E* __restrict__ src, int64_t rows, int cols,
                                                         uint16_t* __restrict__ dst, int64_t ld, int64_t plane,
                                                         const int64_t* __restrict__ targets, int64_t vocab,
                                                         const int* __restrict__ place, E* __restrict__ cleared) {
-    const int per_row = (int)(ld / 8);
-    const int64_t n = rows * per_row;
-    const bool small = n < (int64_t)1 << 31;
-    for (int64_t g0 = (int64_t)blockIdx.x * 256 * kGroups + threadIdx.x; g0 < n;
-         g0 += (int64_t)gridDim.x * 256 * kGroups) {
-        Group8<E, ENDS> w[kGroups];
-        int64_t r[kGroups], tgt[kGroups];
-        int in[kGroups], at[kGroups];
-#pragma unroll
-        for (int k = 0; k < kGroups; ++k) {
-            const int64_t g = g0 + k * 256;
-            split_group(g < n ? g : n - 1, per_row, small, r[k], in[k]);
-            w[k].load(src + r[k] * cols, in[k] * 8, cols);
-            tgt[k] = targets ? gld(targets + r[k]) : 0;
-            at[k] = place ? gld(place + r[k]) : 0;
-        }
-#pragma unroll
-        for (int k = 0; k < kGroups; ++k) {
-            if (g0 + k * 256 >= n) break;
-            if (at[k] < 0) {
-                const int c = in[k] * 8;
-                const float none[8] = {};
-                if (cleared && c < cols) store8(cleared + r[k] * cols + c, cols - c, none);
-                continue;
-            }
-            uint16_t* o = dst + (place ? at[k] : r[k]) * ld + in[k] * 8;
-            const bool live = tgt[k] >= 0 && tgt[k] < vocab;
-            float f[8];
-            value8(w[k], in[k] * 8, cols, f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = live ? f[i] : 0.0f;
-            if constexpr (sizeof(E) == 2) {
-                store8(o, 8, f);  // exact
-            } else {
-                const Split8 s = split8_any(f);
-                *(SC_GLOBAL v8bf*)o = s.h;
-                *(SC_GLOBAL v8bf*)(o + plane) = s.m;
-                *(SC_GLOBAL v8bf*)(o + 2 * plane) = s.l;
-            }
-        }
-    }
+    planes_of_rows<E, ENDS>(
+        src, rows, cols, dst, ld, plane, cleared,
+        [&](int64_t r) { return place ? gld(place + r) : r; },
+        [&](int64_t r) {
+            const int64_t t = targets ? gld(targets + r) : 0;
+            return t >= 0 && t < vocab;
+        });
 }
 
 hipError_t launch_to_planes(bool bf16, const void* src, int64_t rows, int64_t cols, uint16_t* dst, int64_t ld,

@@ -265,10 +265,14 @@ enum TpEpi {
     TP_GRAD = 3,    // (exp(acc - lse[m]) - [n is m's target]) * alpha, as bfloat16 planes
     TP_TAIL = 4,    // C = acc * coef[m] at row rows[m]; tiles that do not fill a round are cut along k
                     // (TpTail) and leave float32 sums, [split][tile][BM][BN]
+    TP_STATS_TAIL = 5,  // TP_STATS, cut likewise
 };
+constexpr bool tp_stats(int epi) { return epi == TP_STATS || epi == TP_STATS_TAIL; }
+constexpr bool tp_cuts(int epi) { return epi == TP_TAIL || epi == TP_STATS_TAIL; }
 
-template <int BM_, int BN_, int WVM_, int WVN_, int NBUF_, int PER_CU_>
+template <int BM_, int BN_, int WVM_, int WVN_, int NBUF_, int PER_CU_, bool ROTATE_ = false>
 struct TpShape {
+    static constexpr bool ROTATE = ROTATE_;
     static constexpr int BM = BM_, BN = BN_, WVM = WVM_, WVN = WVN_, NBUF = NBUF_, PER_CU = PER_CU_;
     static constexpr int NT = 64 * WVM * WVN;
     static constexpr int WAVES = WVM * WVN * PER_CU / 4;  // per SIMD
@@ -302,10 +306,13 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
     using LA = TpLoader<BM, NT, AKC>;
     using LB = TpLoader<BN, NT, BKC>;
     constexpr int ASZ = BM * 64, BSZ = BN * 64;
-    static_assert(NBUF == 2 || NBUF == 3, "buffers");
+    static_assert(NBUF >= 2 && NBUF <= 6, "buffers");
     __shared__ __align__(1024) uint16_t a0[ASZ], b0[BSZ], a1[ASZ], b1[BSZ];
     __shared__ __align__(1024) uint16_t a2[NBUF > 2 ? ASZ : 8], b2[NBUF > 2 ? BSZ : 8];
-    __shared__ float red[EPI == TP_STATS ? 2 * S::WVN * BM : 1];  // row maxima, then sums
+    __shared__ __align__(1024) uint16_t a3[NBUF > 3 ? ASZ : 8], b3[NBUF > 3 ? BSZ : 8];
+    __shared__ __align__(1024) uint16_t a4[NBUF > 4 ? ASZ : 8], b4[NBUF > 4 ? BSZ : 8];
+    __shared__ __align__(1024) uint16_t a5[NBUF > 5 ? ASZ : 8], b5[NBUF > 5 ? BSZ : 8];
+    __shared__ float red[tp_stats(EPI) ? 2 * S::WVN * BM : 1];  // row maxima, then sums
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = (wave / S::WVN) * WM, wn = (wave % S::WVN) * WN;
@@ -337,7 +344,7 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
     const int kturns = max(1, (K + 64 * NBUF - 1) / (64 * NBUF)), total = kturns * P.nseg;
     const int tiles = tiles_m * P.tiles_n;
     TpTail tail = {0, tiles, P.splits};
-    if constexpr (EPI == TP_TAIL) {
+    if constexpr (tp_cuts(EPI)) {
         tail.full = __builtin_amdgcn_readfirstlane(gld(&P.tail->full));
         tail.rest = __builtin_amdgcn_readfirstlane(gld(&P.tail->rest));
         tail.splits = __builtin_amdgcn_readfirstlane(gld(&P.tail->splits));
@@ -349,7 +356,7 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
     };
     auto item = [&](int turn) SC_INLINE {
         Item i;
-        if (EPI == TP_TAIL && turn < tail.full) {
+        if (tp_cuts(EPI) && turn < tail.full) {
             i.tile = xcd_remap(turn, tail.full);
             i.split = i.from = 0;
             i.to = total;
@@ -366,8 +373,11 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
 
     // the turn that is fetched next: its tile, segment and place in the segment
     struct Ahead {
-        int m0, n0, seg, kt, left;
+        int m0, n0, seg, kt, left, rot;
     } ah;
+    // Each tile's turns in an order of its own: where a row's bytes are a power of two, all tiles at the same k
+    // would read from a few memory channels.
+    constexpr bool ROTATE = S::ROTATE;
     auto begin_tile = [&](int turn) SC_INLINE {
         Item it = {0, 0, 0, 0};
         if (turn < all) it = item(turn);
@@ -376,13 +386,16 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
         ah.m0 = tm * BM;
         ah.n0 = tn * BN;
         ah.left = it.to - it.from;
+        ah.rot = ROTATE ? it.tile % kturns : 0;
         ah.seg = it.from / kturns;
         ah.kt = it.from - ah.seg * kturns;
     };
     auto prepare = [&]() SC_INLINE {
         const bool live = ah.left > 0;
         const uint32_t planes = live ? (uint32_t)(P.segs >> (4 * ah.seg)) : 0;
-        const int k0 = ah.kt * 64 * NBUF;
+        int kt = ah.kt;
+        if constexpr (ROTATE) kt = kt + ah.rot < kturns ? kt + ah.rot : kt + ah.rot - kturns;
+        const int k0 = kt * 64 * NBUF;
         la.prepare(P.A + (planes & 3) * P.a_plane, P.lda, M, K, ah.m0, k0, live);
         lb.prepare(P.B + ((planes >> 2) & 3) * P.b_plane, P.ldb, P.N, K, ah.n0, k0, live);
         --ah.left;
@@ -448,6 +461,9 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
     issue(0, a0, b0);
     issue(1, a1, b1);
     if constexpr (NBUF > 2) issue(2, a2, b2);
+    if constexpr (NBUF > 3) issue(3, a3, b3);
+    if constexpr (NBUF > 4) issue(4, a4, b4);
+    if constexpr (NBUF > 5) issue(5, a5, b5);
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(PER * (NBUF - 1)) : "memory");
 
     for (int turn = blockIdx.x; turn < all; turn += gridDim.x) {
@@ -460,7 +476,7 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
 #pragma unroll
         for (int j = 0; j < NI; ++j) {
             v4f start = {0.f, 0.f, 0.f, 0.f};
-            if constexpr (EPI == TP_STATS) {
+            if constexpr (tp_stats(EPI)) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int n = n0 + wn + 16 * j + 4 * ((threadIdx.x & 63) >> 4) + r;
@@ -484,6 +500,9 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
             buffer(0, a0, b0);
             buffer(1, a1, b1);
             if constexpr (NBUF > 2) buffer(2, a2, b2);
+            if constexpr (NBUF > 3) buffer(3, a3, b3);
+            if constexpr (NBUF > 4) buffer(4, a4, b4);
+            if constexpr (NBUF > 5) buffer(5, a5, b5);
         }
 #pragma unroll
         for (int grp = 0; grp < 2; ++grp)
@@ -509,6 +528,9 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
         const int lm = m0 + wm + (lane & 15), ln = n0 + wn + 4 * (lane >> 4);
         const int N = P.N;
         const bool whole = n0 + BN <= N;  // all columns of the tile exist
+        // a part of a cut tile
+        const bool cut = tp_cuts(EPI) && turn >= tail.full && tail.splits > 1;
+        float* part = P.part + ((int64_t)split * tail.rest + (it.tile - tail.full)) * (BM * BN);
         if constexpr (EPI == TP_STORE) {
             const float alpha = P.alpha ? gld(P.alpha) : 1.0f;
             float g[NI][4];
@@ -575,8 +597,6 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
             // Each row block leaves the accumulation registers at one place, whatever becomes of it: where
             // the ways of storing it each read them, the register allocator moved sums ahead of the
             // waits above.
-            const bool cut = turn >= tail.full && tail.splits > 1;
-            float* part = P.part + ((int64_t)split * tail.rest + (it.tile - tail.full)) * (BM * BN);
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
                 row_block(i);
@@ -609,7 +629,7 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
                         tp_store(P.C, P.c_bf16, at + 4 * (lane >> 4) + 16 * j, v[j], N - (ln + 16 * j));
                 }
             }
-        } else if constexpr (EPI == TP_STATS) {
+        } else if constexpr (tp_stats(EPI)) {
             // row maximum over the tile's columns: registers, the four lanes of a row, the
             // waves beside each other
             int hit[MI];  // the target's column in this wave's part, or -1
@@ -625,10 +645,20 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
             for (int i = 0; i < MI; ++i) {
                 row_block(i);
                 float v = -__builtin_huge_valf();
+                v4f x[NI];  // (see TP_TAIL: one place)
 #pragma unroll
-                for (int j = 0; j < NI; ++j)
+                for (int j = 0; j < NI; ++j) {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) v = fmaxf(v, acc[i][j][r]);
+                    for (int r = 0; r < 4; ++r) {
+                        x[j][r] = acc[i][j][r];
+                        v = fmaxf(v, x[j][r]);
+                    }
+                }
+                if (tp_cuts(EPI) && cut) {
+#pragma unroll
+                    for (int j = 0; j < NI; ++j) gst4(part + (lm + 16 * i - m0) * BN + ln - n0 + 16 * j, x[j]);
+                    continue;
+                }
                 v = fmaxf(v, __shfl_xor(v, 16));
                 v = fmaxf(v, __shfl_xor(v, 32));
                 if (lane < 16) red[(wave % S::WVN) * BM + wm + 16 * i + lane] = v;
@@ -638,9 +668,10 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
                             if (hit[i] == 16 * j + 4 * (lane >> 4) + r)
-                                gst(P.target_logit + lm + 16 * i, acc[i][j][r]);
+                                gst(P.target_logit + lm + 16 * i, x[j][r]);
                 }
             }
+            if (tp_cuts(EPI) && cut) continue;
             tp_lds_barrier();
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
@@ -701,13 +732,19 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
                 // a row without weight is one of zeros, whatever its logits are
                 const int64_t tgt = alpha != 0.0f ? tp_target(P.targets, P.vocab, m) : -1;
                 const float lse = gld(P.lse + m);
+                // (the rows' factors are made for the target's entry as the statistics' pass saw it)
+                const float tl = P.coef_zeros ? gld(P.target_logit + m) : 0.0f;
+                auto at_target = [&](int n, float x) SC_INLINE {
+                    return P.coef_zeros && P.n_first + n == tgt ? tl : x;
+                };
 #pragma unroll
                 for (int j = 0; j < NI; ++j) {
                     const int n = ln + 16 * j;
                     float v[4];
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        v[r] = tgt >= 0 && n + r < N ? (__builtin_amdgcn_exp2f((acc[i][j][r] - lse) * kLog2e) -
+                        v[r] = tgt >= 0 && n + r < N ? (__builtin_amdgcn_exp2f((at_target(n + r, acc[i][j][r]) - lse) *
+                                                                               kLog2e) -
                                                         (P.n_first + n + r == tgt ? 1.0f : 0.0f)) *
                                                            alpha
                                                      : 0.0f;

@@ -18,43 +18,97 @@
 
 #include "common.hpp"
 #include "internal.hpp"
+#include "planes.hpp"
 #include "train.hpp"
 
 namespace scopt {
 
 struct Tails {
-    TpTailQuery q[3];  // dh, dW, and dW of the last piece
+    TpTailQuery q[5];  // XentPlan::tails
+};
+// What the counted tokens' rows are told in: rows[c] = t, place[t] = c (-1 where not counted), their targets; logp and
+// loss (or NULL) of the others are 0, and coef starts at 0.
+struct Rows {
+    const int64_t* targets;
+    int64_t T, V;
+    int *live, *rows, *place;
+    int64_t* kept;
+    float *coef, *logp, *loss;
+    TpTail* tails;
+    Tails q;
 };
 
-// The counted tokens in order: rows[c] = t, place[t] = c (-1 where not counted), their targets; logp and
-// loss (or NULL) of the others are 0, and coef starts at 0.  One workgroup, eight tokens a thread
-// and turn: a turn's positions are the sums over the threads before.
-__global__ __launch_bounds__(1024) void token_rows_kernel(const int64_t* __restrict__ targets, int64_t T, int64_t V,
-                                                          int* __restrict__ live, int* __restrict__ rows,
-                                                          int* __restrict__ place, int64_t* __restrict__ kept,
-                                                          float* __restrict__ coef, float* __restrict__ logp,
-                                                          float* __restrict__ loss, const Tails q,
-                                                          TpTail* __restrict__ tails) {
+// The next eight tokens' targets, -1 where not counted; returns how many are
+__device__ __forceinline__ int targets_of(const Rows& a, int64_t first, int64_t (&y)[8]) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = gld(a.targets + (first + i < a.T ? first + i : a.T - 1));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (first + i >= a.T || y[i] >= a.V) y[i] = -1;
+        n += y[i] >= 0;
+    }
+    return n;
+}
+__device__ __forceinline__ void tell_rows(const Rows& a, int64_t first, const int64_t (&y)[8], int c) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t t = first + i;
+        if (t >= a.T) break;
+        if (y[i] >= 0) {
+            gst(a.rows + c, (int)t);
+            gst(a.kept + c, y[i]);
+            gst(a.coef + c, 0.0f);
+            gst(a.place + t, c++);
+        } else {
+            gst(a.place + t, -1);
+            gst(a.logp + t, 0.0f);
+            if (a.loss) gst(a.loss + t, 0.0f);
+        }
+    }
+}
+// How the products are dealt out: a wavefront takes one after the other, a lane a number of parts.
+__device__ __forceinline__ void tell_tails(const Rows& a, int live) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    if (threadIdx.x == 0) gst(a.live, live);
+    for (int i = wave; i < 5; i += blockDim.x / 64) {
+        const TpTailQuery& p = a.q.q[i];
+        const int tiles = p.tiles(live), total = p.total(live), rest = tiles % p.slots;
+        int best = p.ns(tiles, total, lane + 1), splits = lane + 1;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int ns = __shfl_xor(best, o), s = __shfl_xor(splits, o);
+            const bool less = ns < best || (ns == best && s < splits);
+            best = less ? ns : best;
+            splits = less ? s : splits;
+        }
+        if (lane == 0) {
+            gst(&a.tails[i].full, tiles - rest);
+            gst(&a.tails[i].rest, rest);
+            gst(&a.tails[i].splits, splits);
+        }
+    }
+}
+// This wavefront's sum of n up to each lane
+__device__ __forceinline__ int wave_scan(int n) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int x = __shfl_up(n, o);
+        n += lane >= o ? x : 0;
+    }
+    return n;
+}
+
+// One workgroup, eight tokens a thread and turn: a turn's positions are the sums over the threads before.
+__global__ __launch_bounds__(1024) void token_rows_kernel(const Rows a) {
     __shared__ int sums[2][16];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     int base = 0, turn = 0;
-    for (int64_t t0 = 0; t0 < T; t0 += 8192, turn ^= 1) {
+    for (int64_t t0 = 0; t0 < a.T; t0 += 8192, turn ^= 1) {
         const int64_t first = t0 + 8 * threadIdx.x;
         int64_t y[8];
-        int n = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = gld(targets + (first + i < T ? first + i : T - 1));
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (first + i >= T || y[i] >= V) y[i] = -1;
-            n += y[i] >= 0;
-        }
-        int upto = n;  // of this wavefront's threads up to this one
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const int x = __shfl_up(upto, o);
-            upto += lane >= o ? x : 0;
-        }
+        const int n = targets_of(a, first, y), upto = wave_scan(n);
         if (lane == 63) sums[turn][wave] = upto;
         __syncthreads();
         int c = base + upto - n;
@@ -63,40 +117,44 @@ __global__ __launch_bounds__(1024) void token_rows_kernel(const int64_t* __restr
             c += w < wave ? sums[turn][w] : 0;
             base += sums[turn][w];
         }
+        tell_rows(a, first, y, c);
+    }
+    tell_tails(a, base);
+}
+
+// The same and h's operand in one launch, for up to kFewRows tokens: every workgroup finds all positions by
+// itself.  (64 tokens x 2048: 6.5 us, the two kernels 3.7 and 4.4; 8192 tokens, half of them counted: 18 and 17 us
+// as two.)
+constexpr int64_t kFewRows = 8192;
+template <typename E, int ENDS>
+__global__ __launch_bounds__(256) void few_rows_kernel(const Rows a, const E* __restrict__ h, int H,
+                                                       uint16_t* __restrict__ dst, int64_t ld, int64_t plane,
+                                                       E* __restrict__ cleared) {
+    __shared__ int sums[2][4];
+    __shared__ int16_t place[kFewRows];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int base = 0, turn = 0;
+    for (int64_t t0 = 0; t0 < a.T; t0 += 2048, turn ^= 1) {
+        const int64_t first = t0 + 8 * threadIdx.x;
+        int64_t y[8];
+        const int n = targets_of(a, first, y), upto = wave_scan(n);
+        if (lane == 63) sums[turn][wave] = upto;
+        __syncthreads();
+        int c = base + upto - n;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int64_t t = first + i;
-            if (t >= T) break;
-            if (y[i] >= 0) {
-                gst(rows + c, (int)t);
-                gst(kept + c, y[i]);
-                if (coef) gst(coef + c, 0.0f);
-                gst(place + t, c++);
-            } else {
-                gst(place + t, -1);
-                gst(logp + t, 0.0f);
-                if (loss) gst(loss + t, 0.0f);
-            }
+        for (int w = 0; w < 4; ++w) {
+            c += w < wave ? sums[turn][w] : 0;
+            base += sums[turn][w];
         }
-    }
-    if (threadIdx.x == 0) gst(live, base);
-    if (!tails || wave >= 3) return;
-    // how the gradients' products are dealt out: a wavefront a product, a lane a number of parts
-    const TpTailQuery& p = q.q[wave];
-    const int tiles = p.tiles(base), total = p.total(base), rest = tiles % p.slots;
-    int best = p.ns(rest, total, lane + 1), splits = lane + 1;
+        int at = c;
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const int ns = __shfl_xor(best, o), s = __shfl_xor(splits, o);
-        const bool less = ns < best || (ns == best && s < splits);
-        best = less ? ns : best;
-        splits = less ? s : splits;
+        for (int i = 0; i < 8; ++i) place[first + i] = (int16_t)(y[i] >= 0 ? at++ : -1);
+        if (blockIdx.x == (unsigned)(t0 / 2048) % gridDim.x) tell_rows(a, first, y, c);
     }
-    if (lane == 0) {
-        gst(&tails[wave].full, tiles - rest);
-        gst(&tails[wave].rest, rest);
-        gst(&tails[wave].splits, splits);
-    }
+    if (blockIdx.x == 0) tell_tails(a, base);
+    __syncthreads();
+    planes_of_rows<E, ENDS>(
+        h, a.T, H, dst, ld, plane, cleared, [&](int64_t r) { return (int64_t)place[r]; }, [](int64_t) { return true; });
 }
 
 // The policy's losses and the coefficients of its logit gradients.  One workgroup: sums in a fixed
@@ -142,7 +200,7 @@ __global__ __launch_bounds__(1024) void policy_kernel(const int* __restrict__ li
 // A workgroup a pair: both sequences' sums, the pair's loss, and its tokens' coefficients.
 __global__ __launch_bounds__(1024) void preference_kernel(const int* __restrict__ place, int64_t T, PreferenceArgs a,
                                                           float* __restrict__ coef) {
-    __shared__ double red[16];
+    __shared__ double red[4][16];
     const int64_t pair = blockIdx.x;
     int64_t at[3];
 #pragma unroll
@@ -150,19 +208,33 @@ __global__ __launch_bounds__(1024) void preference_kernel(const int* __restrict_
         const int64_t s = gld(a.starts + 2 * pair + i);
         at[i] = s < 0 ? 0 : s < T ? s : T;
     }
-    double reward[2], share[2];
+    double v[4] = {0.0, 0.0, 0.0, 0.0};  // sums and counts
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        double sum = 0.0, n = 0.0;
 #pragma unroll 4
         for (int64_t t = at[k] + threadIdx.x; t < at[k + 1]; t += 1024) {
             const bool counted = gld(place + t) >= 0;
             const double x = (double)gld(a.logp + t) - (a.ref_logp ? (double)gld(a.ref_logp + t) : 0.0);
-            sum += counted ? x : 0.0;
-            n += counted ? 1.0 : 0.0;
+            v[k] += counted ? x : 0.0;
+            v[2 + k] += counted ? 1.0 : 0.0;
         }
-        sum = block_sum_f64(sum, red);
-        n = block_sum_f64(n, red);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) v[i] += __shfl_xor(v[i], o);
+        if ((threadIdx.x & 63) == 0) red[i][threadIdx.x >> 6] = v[i];
+    }
+    __syncthreads();
+    double reward[2], share[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        double sum = 0.0, n = 0.0;
+#pragma unroll
+        for (int w = 0; w < 16; ++w) {
+            sum += red[k][w];
+            n += red[2 + k][w];
+        }
         share[k] = a.average && n > 0.0 ? 1.0 / n : 1.0;
         reward[k] = (double)a.beta * sum * share[k];
     }
@@ -201,7 +273,6 @@ __global__ __launch_bounds__(1024) void pair_mean_kernel(const float* __restrict
 TokenLossPlan token_loss_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit, bool gradients) {
     TokenLossPlan p{};
     p.x = xent_plan(bf16, T, V, H, limit, gradients, true);
-    p.gradients = gradients;
     int64_t o = p.x.bytes;
     auto take = [&](int64_t bytes) {
         const int64_t at = o;
@@ -240,11 +311,25 @@ hipError_t forward(const TokenLossPlan& p, XentRun& run, const void* h, const vo
     run.rows = rows;
     run.place = place;
     run.coef = coef;
-    const Tails tails = {{p.x.dh.tail, p.x.dw.tail, p.x.dw_last.tail}};
-    hipLaunchKernelGGL(token_rows_kernel, dim3(1), dim3(1024), 0, st, targets, p.x.T, p.x.V, live, rows, place, kept,
-                       coef, logp, loss, tails, p.gradients ? run.at<TpTail>(p.x.o_tails) : nullptr);
-    SC_RUN(hipGetLastError());
-    SC_RUN(run.operands(dh));
+    const Rows r{targets, p.x.T, p.x.V, live, rows, place, kept, coef, logp, loss,
+                 run.at<TpTail>(p.x.o_tails),
+                 {{p.x.tails[0], p.x.tails[1], p.x.tails[2], p.x.tails[3], p.x.tails[4]}}};
+    if (p.x.T <= kFewRows) {
+        const int64_t groups = p.x.T * (p.x.Hh / 8);
+        const int64_t blocks = (groups + 256 * kGroups - 1) / (256 * kGroups);
+        const dim3 grid((unsigned)(blocks < 1024 ? blocks : 1024));
+#define SC_FEW(E_, ENDS_)                                                                                          \
+    hipLaunchKernelGGL((few_rows_kernel<E_, ENDS_>), grid, dim3(256), 0, st, r, (const E_*)h, (int)p.x.H,          \
+                       run.at<uint16_t>(p.x.o_h), p.x.Hh, p.x.T * p.x.Hh, (E_*)dh);
+        SC_BY_ENDS(p.x.bf16, p.x.H, SC_FEW)
+#undef SC_FEW
+        SC_RUN(hipGetLastError());
+    } else {
+        hipLaunchKernelGGL(token_rows_kernel, dim3(1), dim3(1024), 0, st, r);
+        SC_RUN(hipGetLastError());
+        SC_RUN(run.h_operand(dh));
+    }
+    SC_RUN(run.w_planes());
     SC_RUN(run.logits());
     return run.log_sums(nullptr, logp);
 }

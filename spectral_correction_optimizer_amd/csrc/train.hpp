@@ -29,18 +29,21 @@ struct TpTailQuery {
     int M = 0, K = 0, live_k = 0;  // live_k: the tokens are k, else the rows
     int bm = 1, turn_k = 1, tiles_n = 0, nseg = 1, slots = 1;
     int turn_ns = 0, tile_ns = 0, join_ns = 0;
-    int most = 0;  // parts that there is room for
+    int pass_ns = 0;  // of the weights or their gradient through memory
+    int most = 0;     // parts that there is room for
     __host__ __device__ int tiles(int live) const { return ((live_k || M < live ? M : live) + bm - 1) / bm * tiles_n; }
     __host__ __device__ int total(int live) const {
         const int k = live_k && live < K ? live : K;
         return (k > 0 ? (k + turn_k - 1) / turn_k : 1) * nseg;
     }
-    // time of the last round's tiles in s parts, their sums and join included; the largest number where that is
-    // not to be
-    __host__ __device__ int ns(int rest, int total, int s) const {
+    // time of the last of the rounds of `tiles` in s parts, their sums and join included; the largest number where
+    // that is not to be
+    __host__ __device__ int ns(int tiles, int total, int s) const {
+        const int rest = tiles % slots;
         if (s > 1 && (rest * s > most || total < 2 * s)) return 0x7fffffff;
-        return (rest * s + slots - 1) / slots * ((total + s - 1) / s * turn_ns + tile_ns) +
-               (s > 1 ? 4000 + rest * s * join_ns : 0);
+        const int ns = (rest * s + slots - 1) / slots * ((total + s - 1) / s * turn_ns + tile_ns);
+        const int least = tiles < slots ? pass_ns : 0;  // where the last round is all there is
+        return (ns > least ? ns : least) + (s > 1 ? 4000 + rest * s * join_ns : 0);
     }
 };
 
@@ -96,8 +99,11 @@ enum TpKind {
     TPK_LOGIT_GRAD,   // A [M][K], B [N][K]
     TPK_STATES,       // A [M][K], B [K][N]: store, or partial sums when splits > 1
     TPK_WEIGHTS,      // A [K][M], B [K][N]: likewise
-    TPK_STATES_LIVE,  // as TPK_STATES and TPK_WEIGHTS, for sizes that are only known on the device: the tiles
-    TPK_WEIGHTS_LIVE, // that do not fill a round of workgroups are cut along k there
+    // as the ones above, for sizes that are only known on the device: the tiles that do not fill a round of
+    // workgroups are cut along k there
+    TPK_LOGIT_STATS_LIVE,
+    TPK_STATES_LIVE,
+    TPK_WEIGHTS_LIVE,
 };
 
 // Tile shapes, and the choice between them for an M x N product of `steps` 64-deep steps.
@@ -106,14 +112,14 @@ struct TpPlan {
     int bm = 0, bn = 0;
     int tiles_m = 0, tiles_n = 0;
     int splits = 1;
-    int64_t part_bytes = 0;  // float32 partial sums (splits > 1)
-    TpTailQuery tail;        // tp_plan_live
+    int64_t part_bytes = 0;  // float32 partial sums (splits > 1; tp_plan_live: the most there can be)
 };
 // Row stride of an operand that the library lays out itself
 inline int64_t tp_pad(int64_t cols) { return cols % 512 == 0 ? cols + 64 : cols; }
 TpPlan tp_plan(int M, int N, int K, int nseg, bool may_split);
-// For the kinds of live tokens: M, N, K are the most there can be, and live_k tells whether the tokens are k
-TpPlan tp_plan_live(int M, int N, int K, int nseg, bool live_k);
+// For the kinds of live tokens: M, N, K are the most there can be.  The parts of the last round's tiles are at most
+// two rounds of them (64 MiB each with the largest tile), of the logits one.
+TpPlan tp_plan_live(TpKind kind, int M, int N, int K, int nseg, TpTailQuery& tail);
 // A product whose sums join others (TPK_STATES, TPK_WEIGHTS): acc is added before the store;
 // with out_acc the float32 sum goes there and C is not written.  Either asks for args.part
 // also without splits.
@@ -150,6 +156,7 @@ struct XentPlan {
     int64_t ldp;               // columns of P
     int64_t stat_tiles;        // tiles of a row
     TpPlan logits, logits_last, dh, dw, dw_last;
+    TpTailQuery tails[5];      // of live tokens: dh, dw, dw_last, logits, logits_last
     // offsets into the workspace
     int64_t o_factors, o_h, o_scaled, o_w, o_s, o_p, o_tl, o_lse, o_smax, o_ssum, o_part, o_dh, o_tails, o_factor, bytes;
 };
@@ -158,6 +165,16 @@ struct XentPlan {
 // live: the counted tokens' rows are put together (XentRun::rows)
 XentPlan xent_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit, bool gradients = true,
                    bool live = false);
+
+// What a row's log-sum-exp is formed from: its tiles' references (powers of two with pow2) and sums, [tile][T],
+// and its target's logit; and where it goes
+struct LogSums {
+    const float *smax, *ssum;
+    int tiles, pow2;
+    const float* target_logit;
+    float* lse;
+    int64_t T;
+};
 
 // One call's buffers, and the steps that the losses share.  Without `rows` the rows of h are the tokens; with
 // them only the counted ones, in order: row c is token rows[c], *live of them exist, and `targets`, lse
@@ -179,8 +196,10 @@ struct XentRun {
     template <typename E> E* at(int64_t offset) const { return (E*)(ws + offset); }
     // h and, where it needs planes, W as operands.  dh: its rows of tokens that are not counted are cleared
     // (with rows; else NULL)
-    hipError_t operands(void* dh) const;
+    hipError_t h_operand(void* dh) const;
+    hipError_t w_planes() const;
     hipError_t logits() const;                       // row statistics, and what is kept
+    LogSums sums() const;
     hipError_t log_sums(float* loss, float* logp) const;  // lse; the tokens' losses, or with rows their negative
     hipError_t gradients(void* dh, void* dW) const;
 
@@ -194,7 +213,6 @@ hipError_t launch_xent(const XentPlan& p, const void* h, const void* W, const in
 
 struct TokenLossPlan {
     XentPlan x;
-    bool gradients;
     int64_t o_live, o_rows, o_place, o_targets, o_coef, bytes;
 };
 TokenLossPlan token_loss_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit, bool gradients);

@@ -32,6 +32,7 @@
 // split exactly into three planes.
 #include <cmath>
 
+#include "log_sums.hpp"
 #include "tile_product.hpp"
 
 namespace scopt {
@@ -41,67 +42,20 @@ constexpr int64_t kAlign = 256;
 int64_t up(int64_t n, int64_t a) { return (n + a - 1) / a * a; }
 }  // namespace
 
-// 64 rows a workgroup, one a lane, the tiles dealt to 16 wavefronts: a row's log-sum-exp from
-// its tiles' references and sums [tile][T], and its loss.  pow2: the references are powers of
-// two.  A row of -infinity only has no finite log-sum-exp; like a row with NaN or +infinity
-// it gives NaN.  With `rows` the first *live rows are counted tokens, and logp[rows[row]] is the target's
-// log-probability.
-__global__ __launch_bounds__(1024) void xent_lse_kernel(const float* __restrict__ smax,
-                                                        const float* __restrict__ ssum, int tiles, int pow2,
-                                                        const float* __restrict__ target_logit,
-                                                        const int64_t* __restrict__ targets, int64_t T, int64_t V,
-                                                        float* __restrict__ lse, float* __restrict__ loss,
-                                                        const int* __restrict__ live, const int* __restrict__ rows,
-                                                        float* __restrict__ logp) {
+__global__ __launch_bounds__(1024) void xent_lse_kernel(const LogSums a, const int64_t* __restrict__ targets, int64_t V,
+                                                        float* __restrict__ loss) {
     __shared__ float red[16][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t end = rows ? gld(live) : T;
-    if ((int64_t)blockIdx.x * 64 >= end) return;
-    const int64_t t = (int64_t)blockIdx.x * 64 + lane, at = t < end ? t : end - 1;
-    const float none = -__builtin_huge_valf();
-    // a difference of references as a factor; a tile of -infinity has sum 0 (or NaN)
-    auto scaled = [&](float s, float r, float to) {
-        return r == none ? s : s * (pow2 ? exp2f(r - to) : expf(r - to));
-    };
-    // sixteen tiles' values in flight, joined to the running reference and sum
-    float m = none, z = 0.0f;
-    constexpr int U = 16;
-    for (int i0 = wave; i0 < tiles; i0 += 16 * U) {
-        float r[U], s[U], top = m;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t i = i0 + 16 * u < tiles ? i0 + 16 * u : tiles - 1;
-            r[u] = gld(smax + i * T + at);
-            s[u] = gld(ssum + i * T + at);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) top = i0 + 16 * u < tiles ? fmaxf(top, r[u]) : top;
-        z = scaled(z, m, top);
-        m = top;
-#pragma unroll
-        for (int u = 0; u < U; ++u) z += i0 + 16 * u < tiles ? scaled(s[u], r[u], m) : 0.0f;
-    }
-    red[wave][lane] = m;
-    __syncthreads();
-    float top = none;
-#pragma unroll
-    for (int w = 0; w < 16; ++w) top = fmaxf(top, red[w][lane]);
-    z = scaled(z, m, top);
-    m = top;
-    __syncthreads();
-    red[wave][lane] = z;
-    __syncthreads();
-    if (wave > 0 || t >= end) return;
-    z = 0.0f;
-#pragma unroll
-    for (int w = 0; w < 16; ++w) z += red[w][lane];
-    // a power of two's logarithm in two parts: m * ln2 is off by less than 2^-40 of m
-    const float base = pow2 ? m * 0.693145751953125f : m, rest = pow2 ? m * 1.42860682030941723e-6f : 0.0f;
-    const float logz = m == none ? __builtin_nanf("") : logf(z) + rest;
-    gst(lse + t, base + logz);
-    const float off = (base - gld(target_logit + t)) + logz;
-    if (rows) gst(logp + gld(rows + t), -off);
-    else gst(loss + t, tp_target(targets, V, t) >= 0 ? off : 0.0f);
+    log_sums<64>(a, a.T, (int64_t)blockIdx.x * 64, red, [&](int64_t t, float logp) {
+        gst(loss + t, tp_target(targets, V, t) >= 0 ? -logp : 0.0f);
+    });
+}
+// of counted tokens: 16 rows a workgroup, as 64 threads take a row's tiles
+__global__ __launch_bounds__(1024) void token_lse_kernel(const LogSums a, const int* __restrict__ live,
+                                                         const int* __restrict__ rows, float* __restrict__ logp) {
+    __shared__ float red[16][16];
+    const int64_t end = gld(live);
+    if ((int64_t)blockIdx.x * 16 >= end) return;
+    log_sums<16>(a, end, (int64_t)blockIdx.x * 16, red, [&](int64_t t, float lp) { gst(logp + gld(rows + t), lp); });
 }
 
 // softmax - onehot at a token's target, as the logit gradients of live tokens hold it
@@ -245,18 +199,22 @@ XentPlan xent_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit, bo
     p.pieces = (int)((V + p.piece - 1) / p.piece);
     p.ldp = tp_pad(up(p.piece, 256));  // the logits' tiles are stored whole
     const int64_t last = V - (int64_t)(p.pieces - 1) * p.piece;
-    p.logits = tp_plan((int)T, (int)p.piece, (int)H, nseg, false);
-    p.logits_last = tp_plan((int)T, (int)last, (int)H, nseg, false);
+    auto logits = [&](int64_t cols, TpTailQuery& tail) {
+        return live ? tp_plan_live(TPK_LOGIT_STATS_LIVE, (int)T, (int)cols, (int)H, nseg, tail)
+                    : tp_plan((int)T, (int)cols, (int)H, nseg, false);
+    };
+    p.logits = logits(p.piece, p.tails[3]);
+    p.logits_last = logits(last, p.tails[4]);
     if (gradients) {
         const bool join = p.pieces > 1;  // sums over pieces have splits of their own
-        p.dh = live && !join ? tp_plan_live((int)T, (int)H, (int)p.piece, nseg, false)
+        p.dh = live && !join ? tp_plan_live(TPK_STATES_LIVE, (int)T, (int)H, (int)p.piece, nseg, p.tails[0])
                              : tp_plan((int)T, (int)H, (int)p.piece, nseg, true);
-        auto weights = [&](int64_t rows) {
-            return live ? tp_plan_live((int)rows, (int)H, (int)T, nseg, true)
+        auto weights = [&](int64_t rows, TpTailQuery& tail) {
+            return live ? tp_plan_live(TPK_WEIGHTS_LIVE, (int)rows, (int)H, (int)T, nseg, tail)
                         : tp_plan((int)rows, (int)H, (int)T, nseg, true);
         };
-        p.dw = weights(p.piece);
-        p.dw_last = weights(last);
+        p.dw = weights(p.piece, p.tails[1]);
+        p.dw_last = weights(last, p.tails[2]);
     }
     p.stat_tiles = (int64_t)(p.pieces - 1) * p.logits.tiles_n + p.logits_last.tiles_n;
     int64_t o = 0;
@@ -279,14 +237,11 @@ XentPlan xent_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit, bo
     const bool join = gradients && p.pieces > 1;
     int64_t part = p.dh.part_bytes;
     if (join && part == 0) part = 4 * T * H;
-    part = part > p.dw.part_bytes ? part : p.dw.part_bytes;
-    part = part > p.dw_last.part_bytes ? part : p.dw_last.part_bytes;
+    for (const TpPlan* q : {&p.dw, &p.dw_last, &p.logits, &p.logits_last}) part = part > q->part_bytes ? part : q->part_bytes;
     p.o_part = take(part);
     p.o_dh = join ? take(4 * T * H) : 0;
-    if (live && gradients) {
-        p.o_tails = take(3 * sizeof(TpTail));
-        p.o_factor = take(4 * T);
-    }
+    if (live) p.o_tails = take(5 * sizeof(TpTail));
+    if (live && gradients) p.o_factor = take(4 * T);
     p.bytes = o;
     return p;
 }
@@ -297,14 +252,15 @@ XentPlan xent_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit, bo
         if (e_ != hipSuccess) return e_;      \
     } while (0)
 
-hipError_t XentRun::operands(void* dh) const {
+hipError_t XentRun::h_operand(void* dh) const {
     // h is always copied, without the tokens that are not counted or with zeros for them: whatever
     // they hold (a NaN too) reaches no product
-    SC_RUN(launch_to_planes(p->bf16, h, p->T, p->H, at<uint16_t>(p->o_h), p->Hh, p->T * p->Hh,
-                            rows ? nullptr : targets, p->V, st, place, dh));
-    if (p->planes)
-        SC_RUN(launch_to_planes(p->bf16, W, p->V, p->H, at<uint16_t>(p->o_w), p->Hp, p->V * p->Hp, nullptr, 0, st));
-    return hipSuccess;
+    return launch_to_planes(p->bf16, h, p->T, p->H, at<uint16_t>(p->o_h), p->Hh, p->T * p->Hh,
+                            rows ? nullptr : targets, p->V, st, place, dh);
+}
+hipError_t XentRun::w_planes() const {
+    if (!p->planes) return hipSuccess;
+    return launch_to_planes(p->bf16, W, p->V, p->H, at<uint16_t>(p->o_w), p->Hp, p->V * p->Hp, nullptr, 0, st);
 }
 
 // planes (A | B << 2) of the six products of two split operands, smallest first
@@ -344,15 +300,27 @@ hipError_t XentRun::logits() const {
         TpArgs a = logit_args(i);
         a.keep = !p->keep ? TP_KEEP_NONE : p->bf16 ? TP_KEEP_EXP : TP_KEEP_LOGIT;
         a.P = p->bf16 ? at<void>(p->o_p) : at<void>(p->o_s);
-        SC_RUN(launch_tile_product(TPK_LOGIT_STATS, i + 1 < p->pieces ? p->logits : p->logits_last, a, TpSum{}, st));
+        a.part = at<float>(p->o_part);
+        const bool last = i + 1 == p->pieces;
+        a.tail = at<TpTail>(p->o_tails) + (last ? 4 : 3);
+        SC_RUN(launch_tile_product(live ? TPK_LOGIT_STATS_LIVE : TPK_LOGIT_STATS, last ? p->logits_last : p->logits, a,
+                                   TpSum{}, st));
     }
     return hipSuccess;
 }
 
+LogSums XentRun::sums() const {
+    return LogSums{at<float>(p->o_smax), at<float>(p->o_ssum), (int)p->stat_tiles, p->keep && p->bf16,
+                   at<float>(p->o_tl),   at<float>(p->o_lse),  p->T};
+}
+
 hipError_t XentRun::log_sums(float* loss, float* logp) const {
-    hipLaunchKernelGGL(xent_lse_kernel, dim3((unsigned)((p->T + 63) / 64)), dim3(1024), 0, st, at<float>(p->o_smax),
-                       at<float>(p->o_ssum), (int)p->stat_tiles, p->keep && p->bf16, at<float>(p->o_tl), targets, p->T,
-                       p->V, at<float>(p->o_lse), loss, live, rows, logp);
+    if (rows)
+        hipLaunchKernelGGL(token_lse_kernel, dim3((unsigned)((p->T + 15) / 16)), dim3(1024), 0, st, sums(), live, rows,
+                           logp);
+    else
+        hipLaunchKernelGGL(xent_lse_kernel, dim3((unsigned)((p->T + 63) / 64)), dim3(1024), 0, st, sums(), targets, p->V,
+                           loss);
     return hipGetLastError();
 }
 
@@ -460,7 +428,8 @@ hipError_t launch_xent(const XentPlan& p, const void* h, const void* W, const in
     run.targets = targets;
     run.ws = (char*)workspace;
     run.st = st;
-    SC_RUN(run.operands(nullptr));
+    SC_RUN(run.h_operand(nullptr));
+    SC_RUN(run.w_planes());
     SC_RUN(run.logits());
     SC_RUN(run.log_sums(loss, nullptr));
     hipLaunchKernelGGL(xent_mean_kernel, dim3(1), dim3(1024), 0, st, loss, targets, p.T, p.V,

@@ -139,10 +139,10 @@ def test_workspace_queries_without_tokens(lib):
 
 
 def test_token_logp_holds_no_logits(lib):
-    """Its workspace is the rows' statistics: far from T x V."""
+    """Its workspace is the rows' statistics, a copy of h and one round of tiles' partial sums: far from T x V."""
     n = ctypes.c_int64()
     assert lib.sc_token_logp_workspace(1, 8192, 131072, 2048, ctypes.byref(n)) == 0
-    assert n.value < 8192 * 131072 * 2 // 16
+    assert n.value < 8192 * 131072 * 2 // 12
 
 
 def test_binding_refuses_cpu_tensors_and_shapes():

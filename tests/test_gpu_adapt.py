@@ -731,3 +731,24 @@ def test_policy_few_tokens(T, V, H, kind, limit):
     for _ in range(2):
         for a, b in zip(out, sco().policy_loss(*args, ref_logp=refl.cuda(), kl=0.02, limit=limit)):
             assert torch.equal(a, b)
+
+
+# few tokens against many columns: the logits' tiles that are made for reading the weights
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("T,V,H,kind", [(64, 20000, 520, "half"), (5, 16384, 1000, "none"), (128, 17001, 136, "none"),
+                                        (100, 40000, 2048, "runs"), (65, 33000, 77, "but last")])
+def test_token_logp_few_tokens(T, V, H, kind, dtype):
+    say(f"case: token_logp few tokens T {T} V {V} H {H} {kind} {dtype}")
+    g = gen(65)
+    h, W, tgt = _xent_case(g, T, V, H, dtype)
+    tgt = _mask(tgt, kind, V)
+    ref = Tokens(h, W, tgt, dtype)
+    got = sco().token_logp(h, W, tgt)
+    within("logp", got.cpu(), ref.logp, ref.dlogp)
+    for limit in (0, 1):
+        out = sco().policy_loss(h, W, tgt, got, torch.ones_like(got), limit=limit)
+        within("logp of the loss", out.logp.cpu(), ref.logp, ref.dlogp)
+        c = torch.where(ref.ok, 1.0, 0.0).to(F64) / max(1, int(ref.ok.sum()))  # every ratio is 1, next to none
+        dh, dW, tdh, tdW = ref.gradients(c, c * (torch.expm1(2 * ref.dlogp) + 4 * U))
+        within("dh", out.dh.cpu(), dh, tdh)
+        within("dW", out.dW.cpu(), dW, tdW)
