@@ -267,10 +267,13 @@ class SpectralAdamW:
         _check(self._lib.sc_refresh_pending(self._h, ctypes.byref(p)))
         return bool(p.value)
 
-    def step(self, W, G_mask):
-        """One spectral-corrected AdamW step; W is updated in place."""
-        _check(self._lib.sc_step(self._h, self._ptrs(W, self.w_dtype, "W"),
-                                 self._ptrs(G_mask, self.g_dtype, "G_mask"), self._stream()))
+    def step(self, W, G_mask, max_norm: float = None):
+        """One spectral-corrected AdamW step; W is updated in place.  max_norm: G_mask is first
+        scaled to at most that global norm, in place (clip_grads), and the GradNorm is returned."""
+        w, g = self._ptrs(W, self.w_dtype, "W"), self._ptrs(G_mask, self.g_dtype, "G_mask")
+        norm = None if max_norm is None else clip_grads(G_mask, max_norm)
+        _check(self._lib.sc_step(self._h, w, g, self._stream()))
+        return norm
 
     def step_noalloc(self, W, G_mask):
         """The same step through the allocation-free entry point (intermediates in

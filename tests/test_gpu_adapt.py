@@ -752,3 +752,95 @@ def test_token_logp_few_tokens(T, V, H, kind, dtype):
         dh, dW, tdh, tdW = ref.gradients(c, c * (torch.expm1(2 * ref.dlogp) + 4 * U))
         within("dh", out.dh.cpu(), dh, tdh)
         within("dW", out.dW.cpu(), dW, tdW)
+
+
+# ---- the operators together ------------------------------------------------------------------
+
+@pytest.mark.parametrize("loss", ["policy", "preference"])
+def test_example_runs(loss):
+    """The example's model, adapted by its own loop."""
+    from examples.policy_step import train
+    losses, norms = train(steps=6, loss=loss)
+    assert len(losses) == len(norms) == 6
+    assert all(math.isfinite(x) for x in losses) and all(0 < x < math.inf for x in norms)
+    if loss == "preference":  # model and reference are the same: nothing is preferred yet
+        assert losses[0] == pytest.approx(math.log(2), rel=1e-5)
+
+
+@pytest.mark.parametrize("loss", ["policy", "preference"])
+def test_example_gradients_against_differences(loss):
+    """The loss changes along the gradients by their squared norm, to first order.  The first norm's checkpoint (half
+    a step of 1/64 of a block's largest power of two, at most 1% of the largest value, twice) bounds what
+    the gradients that read it are off by; float32 losses are off by 80 U."""
+    from examples.policy_step import Batch, Model
+    g = gen(71)
+    m = Model(V=64, H=64, seed=3)
+    ref_model = Model(V=64, H=64, seed=4)
+    follow = torch.randperm(64, generator=g, device="cuda")
+    b = Batch(m, follow, 16, 18, g)
+    old = m.logp(b.ids, b.targets) + 0.05  # no ratio near the clip
+    ref = ref_model.logp(b.ids, b.targets)
+    pair_ref = ref_model.logp(b.pair_ids, b.pair_targets)
+    if loss == "policy":
+        f = lambda h, W: sco().policy_loss(h, W, b.targets, old, b.advantages, ref_logp=ref, kl=0.1)
+        run = lambda: m.step(b.ids, f)
+    else:
+        f = lambda h, W: sco().preference_loss(h, W, b.pair_targets, b.starts, ref_logp=pair_ref, beta=0.5)
+        run = lambda: m.step(b.pair_ids, f)
+    value = lambda out: float(out.total if loss == "policy" else out.mean)
+    out, grads, vectors = run()
+    params, every = m.matrices() + m.vectors(), grads + vectors
+    norm2 = sum((d.double() ** 2).sum() for d in every)
+    t = 1e-3 / float(norm2.sqrt())
+    found = []
+    for sign in (1, -1):
+        for p, d in zip(params, every):
+            p.add_(sign * t * d)
+        found.append(value(run()[0]))
+        for p, d in zip(params, every):
+            p.sub_(sign * t * d)
+    slope = (found[0] - found[1]) / (2 * t)
+    # the losses' terms, of which 80 U each is float32's: of order 1 and, for a policy, as large as the advantages
+    size = 1 + float(b.advantages.abs().max())
+    assert abs(slope - float(norm2)) <= 80 * U * size / t + 0.04 * float(norm2)
+
+
+def test_optimizer_step_clips():
+    """SpectralAdamW.step with max_norm is clip_grads in place, then the step."""
+    m, g = sco(), gen(72)
+    shapes = [(96, 64), (64, 160)]
+    runs = []
+    for way in range(2):
+        opt = m.SpectralAdamW(shapes, device=torch.device("cuda", 0))
+        gg = gen(73)
+        W, G = [randn(gg, *s) for s in shapes], [randn(gg, *s) for s in shapes]
+        opt.anchor_update([x.clone() for x in G])
+        if way == 0:
+            r = opt.step(W, G, max_norm=0.5)
+        else:
+            r = m.clip_grads(G, 0.5)
+            assert opt.step(W, G) is None
+        torch.cuda.synchronize()
+        runs.append([*W, *G, r.norm, r.scale])
+        opt.close()
+    for a, b in zip(*runs):
+        assert torch.equal(a, b)
+    total = sum((x.to(F64) ** 2).sum() for x in runs[0][2:4]).sqrt()
+    assert abs(total.item() - 0.5) < 1e-5
+
+
+def test_clip_refuses_other_lists():
+    m = sco()
+    x, y = torch.ones(4, 6, device="cuda"), torch.ones(6, 4, device="cuda")
+    for bad in ([x.t()], [x.half()], [x.cpu()], [x, y.cpu()], [x, 3], [x, x.t()]):
+        with pytest.raises(ValueError):
+            m.clip_grads(bad, 1.0)
+    for out in ([], [y], [x.bfloat16()], [torch.ones(6, 4, device="cuda").t()]):
+        with pytest.raises(ValueError):
+            m.clip_grads([x], 1.0, out=out)
+    for s in (torch.ones((), device="cuda"), torch.ones(1, dtype=F64, device="cuda"), torch.ones((), dtype=F64)):
+        with pytest.raises(ValueError):
+            m.clip_grads([x], 1.0, sumsq=s)
+    with pytest.raises(m.ScoptError):
+        m.clip_grads([x], -1.0)
+    assert torch.equal(x, torch.ones(4, 6, device="cuda"))
