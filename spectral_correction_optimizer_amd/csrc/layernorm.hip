@@ -355,16 +355,18 @@ static void ln_rows(int64_t T, hipStream_t st, int8_t* q, A... args) {
     else hipLaunchKernelGGL((layernorm_kernel<E, ENDS, TPR, C, false>), grid, blk, 0, st, args...);
 }
 template <typename E, int ENDS, typename... A>
-static void ln_sizes(int H, A... args) {
-    if (ENDS == ROW_SHORT || H <= 512) ln_rows<E, ENDS, 64, 1>(args...);
+static void ln_sizes(int H, int64_t T, A... args) {
+    if (ENDS == ROW_SHORT || H <= 512) ln_rows<E, ENDS, 64, 1>(T, args...);
     else if constexpr (ENDS != ROW_SHORT) {
-        if (H <= 1024) ln_rows<E, ENDS, 64, 2>(args...);
-        else if (H <= 1536) ln_rows<E, ENDS, 64, 3>(args...);
-        else if (H <= 2048) ln_rows<E, ENDS, 64, 4>(args...);
-        else if (H <= 4096) ln_rows<E, ENDS, 256, 2>(args...);
-        else if (H <= 6144) ln_rows<E, ENDS, 256, 3>(args...);
-        else if (H <= 8192) ln_rows<E, ENDS, 256, 4>(args...);
-        else ln_rows<E, ENDS, 512, 4>(args...);
+        if (H <= 1024) ln_rows<E, ENDS, 64, 2>(T, args...);
+        // (32 rows of 2048: 4.5 us, a wavefront each 7.3)
+        else if (H <= 2048 && T <= 1024) ln_rows<E, ENDS, 256, 1>(T, args...);
+        else if (H <= 1536) ln_rows<E, ENDS, 64, 3>(T, args...);
+        else if (H <= 2048) ln_rows<E, ENDS, 64, 4>(T, args...);
+        else if (H <= 4096) ln_rows<E, ENDS, 256, 2>(T, args...);
+        else if (H <= 6144) ln_rows<E, ENDS, 256, 3>(T, args...);
+        else if (H <= 8192) ln_rows<E, ENDS, 256, 4>(T, args...);
+        else ln_rows<E, ENDS, 512, 4>(T, args...);
     }
 }
 template <typename E, int ENDS, int I>

@@ -30,6 +30,24 @@ __device__ __forceinline__ Split8 split8_any(const float (&f)[8]) {
     return Split8{__builtin_bit_cast(v8bf, h), __builtin_bit_cast(v8bf, m), __builtin_bit_cast(v8bf, l)};
 }
 
+// 2^14 .. 2^15 of a row's largest finite magnitude: the exponent of the power of two that takes it there
+__device__ __forceinline__ int half_exponent(float most) {
+    const int e = (int)(__float_as_uint(most) >> 23) - 127;  // (a denormal number: -127, and the row stays small)
+    return most > 0.0f ? min(14 - e, 126) : 0;
+}
+// x 2^e as two float16 values, h + l: off by at most 2^-22 of it or 2^-39 of the row's largest one.  An infinity is its
+// own first value, beside 0.
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+__device__ __forceinline__ void split8_half(const float (&f)[8], int e, v8h& h, v8h& l) {
+    const float unit = __uint_as_float((uint32_t)(e + 127) << 23);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float x = f[i] * unit;
+        h[i] = (_Float16)x;
+        l[i] = fabsf(x) == __builtin_huge_valf() ? (_Float16)0.0f : (_Float16)(x - (float)h[i]);
+    }
+}
+
 // planes[p][at(r)][c]: kGroups groups of eight columns a thread (ld is a multiple of 8).  Where at(r) is negative the
 // row of `cleared` (or NULL) is set to zeros instead; a row that is not live(r) is one of zeros.
 template <typename E, int ENDS, typename At, typename Live>

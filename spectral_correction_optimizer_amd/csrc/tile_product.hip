@@ -123,6 +123,11 @@ __global__ __launch_bounds__(256) void tp_stats_tail_kernel(const TpArgs P) {
 #pragma unroll
             for (int c = 0; c < C; ++c) v[c] += x[c];
         }
+        if (P.a_exp) {
+            const int e = gld(P.a_exp + m);
+#pragma unroll
+            for (int c = 0; c < C; ++c) v[c] = ldexpf(v[c], e + gld(P.b_exp + min(n + c, P.N - 1)));
+        }
         float mx = -__builtin_huge_valf();
 #pragma unroll
         for (int c = 0; c < C; ++c) mx = fmaxf(mx, v[c]);
@@ -232,7 +237,8 @@ TpPlan tp_plan_live(TpKind kind, int M, int N, int K, int nseg, TpTailQuery& tai
         const int live = live_k ? K : M, tiles = q.tiles(live), total = q.total(live);
         // what the tokens do not change goes by at about 5 TB/s (the logits of 64 tokens, 32000 x 2048: whole 25 us,
         // cut in two and joined 35)
-        const int64_t bytes = live_k ? (int64_t)M * N * (nseg > 1 ? 4 : 2) : (int64_t)N * K * (nseg > 1 ? 6 : 2);
+        const int64_t bytes = live_k ? (int64_t)M * N * (nseg > 1 ? 4 : 2)
+                                     : (int64_t)N * K * (nseg == 6 ? 6 : nseg == 3 ? 4 : 2);
         q.pass_ns = (int)(bytes / 5000 < 1 << 30 ? bytes / 5000 : 1 << 30);
         // parts of any number of live tokens, none of fewer than two turns
         const int64_t parts = total < 4 ? 0 : (int64_t)tiles * (total / 2 < 64 ? total / 2 : 64);
@@ -257,7 +263,9 @@ TpPlan tp_plan_live(TpKind kind, int M, int N, int K, int nseg, TpTailQuery& tai
 namespace {
 template <class S>
 hipError_t launch_few(const TpPlan& plan, const TpArgs& P, hipStream_t st) {
-    hipLaunchKernelGGL((tile_product_kernel<S, true, true, TP_STATS_TAIL>), dim3(kCus * S::PER_CU), dim3(S::NT), 0, st, P);
+    auto kernel = P.a_exp ? tile_product_kernel<S, true, true, TP_STATS_TAIL, true>
+                          : tile_product_kernel<S, true, true, TP_STATS_TAIL, false>;
+    hipLaunchKernelGGL(kernel, dim3(kCus * S::PER_CU), dim3(S::NT), 0, st, P);
     if (plan.part_bytes > 0)
         hipLaunchKernelGGL((tp_stats_tail_kernel<S::BM, S::BN>), dim3(2048), dim3(256), 0, st, P);
     return hipGetLastError();
@@ -265,7 +273,9 @@ hipError_t launch_few(const TpPlan& plan, const TpArgs& P, hipStream_t st) {
 template <class S>
 hipError_t launch_tail(TpKind kind, const TpPlan& plan, const TpArgs& P, hipStream_t st) {
     const dim3 grid(kCus * S::PER_CU), blk(S::NT);
-    if (kind == TPK_LOGIT_STATS_LIVE)
+    if (kind == TPK_LOGIT_STATS_LIVE && P.a_exp)
+        hipLaunchKernelGGL((tile_product_kernel<S, true, true, TP_STATS_TAIL, true>), grid, blk, 0, st, P);
+    else if (kind == TPK_LOGIT_STATS_LIVE)
         hipLaunchKernelGGL((tile_product_kernel<S, true, true, TP_STATS_TAIL>), grid, blk, 0, st, P);
     else if (kind == TPK_STATES_LIVE)
         hipLaunchKernelGGL((tile_product_kernel<S, true, false, TP_TAIL>), grid, blk, 0, st, P);
@@ -286,7 +296,8 @@ hipError_t launch_shape(TpKind kind, const TpArgs& P, bool part, hipStream_t st)
             hipLaunchKernelGGL((tile_product_kernel<S, true, true, TP_STATS>), grid, blk, 0, st, P);
             break;
         case TPK_LOGIT_GRAD:
-            hipLaunchKernelGGL((tile_product_kernel<S, true, true, TP_GRAD>), grid, blk, 0, st, P);
+            if (P.a_exp) hipLaunchKernelGGL((tile_product_kernel<S, true, true, TP_GRAD, true>), grid, blk, 0, st, P);
+            else hipLaunchKernelGGL((tile_product_kernel<S, true, true, TP_GRAD>), grid, blk, 0, st, P);
             break;
         case TPK_STATES:
             if (part) hipLaunchKernelGGL((tile_product_kernel<S, true, false, TP_PART>), grid, blk, 0, st, P);
@@ -355,6 +366,98 @@ __global__ __launch_bounds__(256) void to_planes_kernel(const E* __restrict__ sr
             const int64_t t = targets ? gld(targets + r) : 0;
             return t >= 0 && t < vocab;
         });
+}
+
+// A wavefront a row; up to 2048 columns stay in registers between its largest magnitude and its planes.
+template <int ENDS, bool PLANES>
+__global__ __launch_bounds__(256) void half_rows_kernel(const float* __restrict__ src, int64_t rows, int cols, int64_t ld,
+                                                        uint16_t* __restrict__ half, int* __restrict__ exps,
+                                                        uint16_t* __restrict__ planes, const int* __restrict__ place,
+                                                        float* __restrict__ cleared) {
+    constexpr int C = 4;
+    const int lane = threadIdx.x & 63;
+    const int64_t plane = rows * ld;
+    for (int64_t r = (int64_t)blockIdx.x * 4 + threadIdx.x / 64; r < rows; r += (int64_t)gridDim.x * 4) {
+        const float* from = src + r * cols;
+        Group8<float, ENDS> w[C], more[C];
+#pragma unroll
+        for (int j = 0; j < C; ++j) w[j].load(from, (j * 64 + lane) * 8, cols);
+        const int64_t to = place ? gld(place + r) : r;
+        if (to < 0) {
+            const float none[8] = {};
+            if (cleared)
+                for (int c = lane * 8; c < cols; c += 512) store8(cleared + r * cols + c, cols - c, none);
+            continue;
+        }
+        float most = 0.0f;
+        auto take = [&](const Group8<float, ENDS>& g, int c) __attribute__((always_inline)) {
+            float f[8];
+            value8(g, c, cols, f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float a = fabsf(f[i]);
+                most = fmaxf(most, a < __builtin_huge_valf() ? a : 0.0f);
+            }
+        };
+#pragma unroll
+        for (int j = 0; j < C; ++j) take(w[j], (j * 64 + lane) * 8);
+        for (int c0 = C * 512; c0 < cols; c0 += C * 512) {
+#pragma unroll
+            for (int j = 0; j < C; ++j) more[j].load(from, c0 + (j * 64 + lane) * 8, cols);
+#pragma unroll
+            for (int j = 0; j < C; ++j) take(more[j], c0 + (j * 64 + lane) * 8);
+        }
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor(most, o));
+        const int e = half_exponent(most);
+        if (lane == 0) gst(exps + to, -e);
+        auto put = [&](const Group8<float, ENDS>& g, int c) __attribute__((always_inline)) {
+            if (c >= ld) return;
+            float f[8];
+            value8(g, c, cols, f);
+            v8h h, l;
+            split8_half(f, e, h, l);
+            uint16_t* o = half + to * ld + c;
+            *(SC_GLOBAL v8h*)o = h;
+            *(SC_GLOBAL v8h*)(o + plane) = l;
+            if constexpr (PLANES) {
+                const Split8 s = split8_any(f);
+                uint16_t* p = planes + to * ld + c;
+                *(SC_GLOBAL v8bf*)p = s.h;
+                *(SC_GLOBAL v8bf*)(p + plane) = s.m;
+                *(SC_GLOBAL v8bf*)(p + 2 * plane) = s.l;
+            }
+        };
+#pragma unroll
+        for (int j = 0; j < C; ++j) put(w[j], (j * 64 + lane) * 8);
+        for (int c0 = C * 512; c0 < ld; c0 += C * 512) {
+#pragma unroll
+            for (int j = 0; j < C; ++j) more[j].load(from, c0 + (j * 64 + lane) * 8, cols);
+#pragma unroll
+            for (int j = 0; j < C; ++j) put(more[j], c0 + (j * 64 + lane) * 8);
+        }
+    }
+}
+
+hipError_t launch_half_rows(const float* src, int64_t rows, int64_t cols, int64_t ld, uint16_t* half, int* exps,
+                            uint16_t* planes, hipStream_t st, const int* place, float* cleared) {
+    if (rows <= 0) return hipSuccess;
+    const int64_t blocks = (rows + 3) / 4;
+    const dim3 grid((unsigned)(blocks < 16384 ? blocks : 16384));
+#define SC_HALF(ENDS_)                                                                                              \
+    if (planes)                                                                                                    \
+        hipLaunchKernelGGL((half_rows_kernel<ENDS_, true>), grid, dim3(256), 0, st, src, rows, (int)cols, ld, half, \
+                           exps, planes, place, cleared);                                                          \
+    else                                                                                                           \
+        hipLaunchKernelGGL((half_rows_kernel<ENDS_, false>), grid, dim3(256), 0, st, src, rows, (int)cols, ld, half, \
+                           exps, planes, place, cleared);
+    switch (row_ends(cols)) {
+        case ROW_WHOLE: SC_HALF(ROW_WHOLE) break;
+        case ROW_CUT: SC_HALF(ROW_CUT) break;
+        case ROW_SHORT: SC_HALF(ROW_SHORT) break;
+    }
+#undef SC_HALF
+    return hipGetLastError();
 }
 
 hipError_t launch_to_planes(bool bf16, const void* src, int64_t rows, int64_t cols, uint16_t* dst, int64_t ld,

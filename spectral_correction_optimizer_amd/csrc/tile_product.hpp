@@ -9,7 +9,9 @@
 // operand is split exactly into three planes x = hi + mid + lo (common.hpp), and the six
 // largest of the nine plane products (three when the other operand is exact in one plane)
 // run through the same loop, smallest first, into the same accumulators: the parts left
-// out are below 2^-23 of |a b|.
+// out are below 2^-23 of |a b|.  With HALF the planes are float16: two of them hold 22 bits of a row that a
+// power of two takes into their range, three products leave out below 3 2^-22 of |a b| (2^-37 of the
+// rows' largest values), and the powers of two come back with the sums.
 //
 // A workgroup owns a BM x BN tile; buffers in LDS hold 64 k of it.  Both operand tiles go
 // from memory straight into LDS (16 bytes per lane, no registers); each wave multiplies a
@@ -57,6 +59,7 @@ namespace scopt {
 
 typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
 typedef short v4s __attribute__((ext_vector_type(4)));
+typedef int v4i __attribute__((ext_vector_type(4)));
 typedef short v8s __attribute__((ext_vector_type(8)));
 
 #define SC_LDS __attribute__((address_space(3)))
@@ -298,7 +301,7 @@ __device__ __forceinline__ void tp_lds_barrier() {
     asm volatile("" ::: "memory");
 }
 
-template <class S, bool AKC, bool BKC, int EPI>
+template <class S, bool AKC, bool BKC, int EPI, bool HALF = false>
 __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpArgs P) {
     constexpr int BM = S::BM, BN = S::BN, NT = S::NT;
     constexpr int NBUF = S::NBUF;
@@ -415,9 +418,14 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
     // moves sums about and spills fragments.
     auto product = [&](int cur, int grp, int p) SC_INLINE {
         const int i = p / NI, j = p % NI;  // transposed: a lane's four sums are consecutive n
-        asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0"
-                     : "+a"(acc[grp * MG + i][j])
-                     : "v"(fb[cur][j]), "v"(fa[cur][grp][i]));
+        if constexpr (HALF)
+            asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0"
+                         : "+a"(acc[grp * MG + i][j])
+                         : "v"(fb[cur][j]), "v"(fa[cur][grp][i]));
+        else
+            asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0"
+                         : "+a"(acc[grp * MG + i][j])
+                         : "v"(fb[cur][j]), "v"(fa[cur][grp][i]));
     };
     // The products of a group, and spread between them the next step's reads of A's group and,
     // with the first group, of B.
@@ -646,13 +654,19 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
                 row_block(i);
                 float v = -__builtin_huge_valf();
                 v4f x[NI];  // (see TP_TAIL: one place)
+                int ea = 0;
+                if constexpr (HALF) ea = gld(P.a_exp + min(lm + 16 * i, M - 1));
 #pragma unroll
                 for (int j = 0; j < NI; ++j) {
+                    v4i eb;
+                    if constexpr (HALF) eb = *(const SC_GLOBAL v4i*)(P.b_exp + ln + 16 * j);
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         x[j][r] = acc[i][j][r];
+                        if constexpr (HALF) x[j][r] = cut ? x[j][r] : ldexpf(x[j][r], ea + eb[r]);
                         v = fmaxf(v, x[j][r]);
                     }
+                    if constexpr (HALF) acc[i][j] = x[j];
                 }
                 if (tp_cuts(EPI) && cut) {
 #pragma unroll
@@ -732,6 +746,8 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
                 // a row without weight is one of zeros, whatever its logits are
                 const int64_t tgt = alpha != 0.0f ? tp_target(P.targets, P.vocab, m) : -1;
                 const float lse = gld(P.lse + m);
+                int ea = 0;
+                if constexpr (HALF) ea = gld(P.a_exp + m);
                 // (the rows' factors are made for the target's entry as the statistics' pass saw it)
                 const float tl = P.coef_zeros ? gld(P.target_logit + m) : 0.0f;
                 auto at_target = [&](int n, float x) SC_INLINE {
@@ -742,12 +758,14 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
                     const int n = ln + 16 * j;
                     float v[4];
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        v[r] = tgt >= 0 && n + r < N ? (__builtin_amdgcn_exp2f((at_target(n + r, acc[i][j][r]) - lse) *
-                                                                               kLog2e) -
+                    for (int r = 0; r < 4; ++r) {
+                        float s = acc[i][j][r];
+                        if constexpr (HALF) s = ldexpf(s, ea + gld(P.b_exp + min(n + r, N - 1)));
+                        v[r] = tgt >= 0 && n + r < N ? (__builtin_amdgcn_exp2f((at_target(n + r, s) - lse) * kLog2e) -
                                                         (P.n_first + n + r == tgt ? 1.0f : 0.0f)) *
                                                            alpha
                                                      : 0.0f;
+                    }
                     tp_store_planes((uint16_t*)P.P, P.p_planes, P.p_plane, (int64_t)m * P.ldp + n, v);
                 }
             }

@@ -122,7 +122,7 @@ __global__ __launch_bounds__(1024) void token_rows_kernel(const Rows a) {
     tell_tails(a, base);
 }
 
-// The same and h's operand in one launch, for up to kFewRows tokens: every workgroup finds all positions by
+// The same and h's bfloat16 operand in one launch, for up to kFewRows tokens: every workgroup finds all positions by
 // itself.  (64 tokens x 2048: 6.5 us, the two kernels 3.7 and 4.4; 8192 tokens, half of them counted: 18 and 17 us
 // as two.)
 constexpr int64_t kFewRows = 8192;
@@ -296,8 +296,8 @@ TokenLossPlan token_loss_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_
 
 namespace {
 // The counted tokens' rows, the operands, and every token's log-probability
-hipError_t forward(const TokenLossPlan& p, XentRun& run, const void* h, const void* W, const int64_t* targets,
-                   float* logp, float* loss, void* dh, void* workspace, hipStream_t st) {
+hipError_t forward(const TokenLossPlan& p, XentRun& run, bool gradients, const void* h, const void* W,
+                   const int64_t* targets, float* logp, float* loss, void* dh, void* workspace, hipStream_t st) {
     run.p = &p.x;
     run.h = h;
     run.W = W;
@@ -314,15 +314,20 @@ hipError_t forward(const TokenLossPlan& p, XentRun& run, const void* h, const vo
     const Rows r{targets, p.x.T, p.x.V, live, rows, place, kept, coef, logp, loss,
                  run.at<TpTail>(p.x.o_tails),
                  {{p.x.tails[0], p.x.tails[1], p.x.tails[2], p.x.tails[3], p.x.tails[4]}}};
-    if (p.x.T <= kFewRows) {
+    run.gradients_follow = gradients;
+    if (p.x.T <= kFewRows && !p.x.half) {
         const int64_t groups = p.x.T * (p.x.Hh / 8);
         const int64_t blocks = (groups + 256 * kGroups - 1) / (256 * kGroups);
         const dim3 grid((unsigned)(blocks < 1024 ? blocks : 1024));
-#define SC_FEW(E_, ENDS_)                                                                                          \
-    hipLaunchKernelGGL((few_rows_kernel<E_, ENDS_>), grid, dim3(256), 0, st, r, (const E_*)h, (int)p.x.H,          \
-                       run.at<uint16_t>(p.x.o_h), p.x.Hh, p.x.T * p.x.Hh, (E_*)dh);
-        SC_BY_ENDS(p.x.bf16, p.x.H, SC_FEW)
-#undef SC_FEW
+        auto few = [&](auto kernel) {
+            hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, r, (const uint16_t*)h, (int)p.x.H,
+                               run.at<uint16_t>(p.x.o_h), p.x.Hh, p.x.T * p.x.Hh, (uint16_t*)dh);
+        };
+        switch (row_ends(p.x.H)) {
+            case ROW_WHOLE: few(few_rows_kernel<uint16_t, ROW_WHOLE>); break;
+            case ROW_CUT: few(few_rows_kernel<uint16_t, ROW_CUT>); break;
+            case ROW_SHORT: few(few_rows_kernel<uint16_t, ROW_SHORT>); break;
+        }
         SC_RUN(hipGetLastError());
     } else {
         hipLaunchKernelGGL(token_rows_kernel, dim3(1), dim3(1024), 0, st, r);
@@ -339,7 +344,7 @@ hipError_t launch_token_logp(const TokenLossPlan& p, const void* h, const void* 
                              float* logp, void* workspace, hipStream_t st) {
     if (p.x.T == 0) return hipSuccess;
     XentRun run;
-    return forward(p, run, h, W, targets, logp, nullptr, nullptr, workspace, st);
+    return forward(p, run, false, h, W, targets, logp, nullptr, nullptr, workspace, st);
 }
 
 hipError_t launch_policy_loss(const TokenLossPlan& p, const void* h, const void* W, const int64_t* targets,
@@ -351,7 +356,7 @@ hipError_t launch_policy_loss(const TokenLossPlan& p, const void* h, const void*
         return launch_zero(dW, p.x.V * p.x.H * (p.x.bf16 ? 2 : 4), st);
     }
     XentRun run;
-    SC_RUN(forward(p, run, h, W, targets, a.logp, a.loss, dh, workspace, st));
+    SC_RUN(forward(p, run, true, h, W, targets, a.logp, a.loss, dh, workspace, st));
     hipLaunchKernelGGL(policy_kernel, dim3(1), dim3(1024), 0, st, run.live, run.rows, a, run.at<float>(p.o_coef));
     SC_RUN(hipGetLastError());
     return run.gradients(dh, dW);
@@ -360,7 +365,7 @@ hipError_t launch_policy_loss(const TokenLossPlan& p, const void* h, const void*
 hipError_t launch_preference_loss(const TokenLossPlan& p, const void* h, const void* W, const int64_t* targets,
                                   const PreferenceArgs& a, void* dh, void* dW, void* workspace, hipStream_t st) {
     XentRun run;
-    if (p.x.T > 0) SC_RUN(forward(p, run, h, W, targets, a.logp, nullptr, dh, workspace, st));
+    if (p.x.T > 0) SC_RUN(forward(p, run, true, h, W, targets, a.logp, nullptr, dh, workspace, st));
     if (a.pairs > 0) {
         hipLaunchKernelGGL(preference_kernel, dim3((unsigned)a.pairs), dim3(1024), 0, st, run.place, p.x.T, a,
                            (float*)((char*)workspace + p.o_coef));

@@ -91,6 +91,9 @@ struct TpArgs {
     int live_rows = 0;          // set by the launch: live counts the rows of C
     const int* rows = nullptr;  // TP_TAIL, reduction: row m is stored as row rows[m] (NULL: m)
     const TpTail* tail = nullptr;  // TP_TAIL: on the device
+    // Operands in float16: row m of A stands for 2^a_exp[m] times its planes, row n of B for 2^b_exp[n] times
+    // (16-byte aligned, readable to the end of the last tile)
+    const int *a_exp = nullptr, *b_exp = nullptr;
 };
 
 // The product's operand layouts and what is done with its sums.
@@ -146,6 +149,12 @@ hipError_t launch_to_planes(bool bf16, const void* src, int64_t rows, int64_t co
                             int64_t plane, const int64_t* targets, int64_t vocab, hipStream_t st,
                             const int* place = nullptr, void* cleared = nullptr);
 
+// Rows of a float32 matrix [rows][cols] as operands of a product of live tokens: two float16 planes half[2][rows][ld] of
+// each row times a power of two (its exponent's negative is `exps`), and with `planes` the three bfloat16 ones too
+// ([3][rows][ld]).  place, cleared: as launch_to_planes.
+hipError_t launch_half_rows(const float* src, int64_t rows, int64_t cols, int64_t ld, uint16_t* half, int* exps,
+                            uint16_t* planes, hipStream_t st, const int* place = nullptr, float* cleared = nullptr);
+
 // ---- losses over a large vocabulary (xent.hip, token_loss.hip) -------------------------
 struct XentPlan {
     bool bf16, planes;         // planes: W is copied into planes (float32, or H % 8), as h always is
@@ -157,8 +166,10 @@ struct XentPlan {
     int64_t stat_tiles;        // tiles of a row
     TpPlan logits, logits_last, dh, dw, dw_last;
     TpTailQuery tails[5];      // of live tokens: dh, dw, dw_last, logits, logits_last
+    bool half;                 // live tokens in float32: the logits' operands are float16 planes
     // offsets into the workspace
-    int64_t o_factors, o_h, o_scaled, o_w, o_s, o_p, o_tl, o_lse, o_smax, o_ssum, o_part, o_dh, o_tails, o_factor, bytes;
+    int64_t o_factors, o_h, o_scaled, o_w, o_s, o_p, o_tl, o_lse, o_smax, o_ssum, o_part, o_dh, o_tails, o_factor;
+    int64_t o_half_h, o_half_w, o_exp_h, o_exp_w, bytes;
 };
 // limit: bytes that the kept probabilities (or a piece's) may take; gradients = false: only the logits'
 // statistics are taken, and there is room for nothing else
@@ -191,6 +202,7 @@ struct XentRun {
     // of a sequence's tokens would be rounded the same way in all of them.  Without coef the factor is factors[1], and the stores of dh and dW
     // multiply by factors[0].
     const float* coef = nullptr;
+    bool gradients_follow = true;
     hipStream_t st = nullptr;
 
     template <typename E> E* at(int64_t offset) const { return (E*)(ws + offset); }

@@ -187,6 +187,8 @@ XentPlan xent_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit, bo
     p.Hp = p.planes ? tp_pad(up(H, 64)) : H;
     p.Hh = tp_pad(up(H, 64));
     const int nseg = bf16 ? 1 : 6;
+    p.half = live && !bf16;
+    const int logit_seg = p.half ? 3 : nseg;
     // bytes of a vocabulary column: the kept exponentials, or the logits and d's planes
     const int64_t col_kept = T * (bf16 ? 2 : 10), col_piece = T * (bf16 ? 2 : 6);
     p.keep = gradients && up(V, 256) * col_kept <= limit;
@@ -200,7 +202,7 @@ XentPlan xent_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit, bo
     p.ldp = tp_pad(up(p.piece, 256));  // the logits' tiles are stored whole
     const int64_t last = V - (int64_t)(p.pieces - 1) * p.piece;
     auto logits = [&](int64_t cols, TpTailQuery& tail) {
-        return live ? tp_plan_live(TPK_LOGIT_STATS_LIVE, (int)T, (int)cols, (int)H, nseg, tail)
+        return live ? tp_plan_live(TPK_LOGIT_STATS_LIVE, (int)T, (int)cols, (int)H, logit_seg, tail)
                     : tp_plan((int)T, (int)cols, (int)H, nseg, false);
     };
     p.logits = logits(p.piece, p.tails[3]);
@@ -225,9 +227,16 @@ XentPlan xent_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit, bo
     };
     const int np = bf16 ? 1 : 3;
     p.o_factors = take(8);
-    p.o_h = take(2 * np * T * p.Hh);
+    const bool whole = gradients || !p.half;  // the gradients' operands, or the logits' too
+    p.o_h = whole ? take(2 * np * T * p.Hh) : 0;
     p.o_scaled = live && gradients && bf16 && !p.keep ? take(2 * T * p.Hh) : p.o_h;
-    p.o_w = p.planes ? take(2 * np * V * p.Hp) : 0;
+    p.o_w = p.planes && whole ? take(2 * np * V * p.Hp) : 0;
+    if (p.half) {
+        p.o_half_h = take(4 * T * p.Hh);
+        p.o_half_w = take(4 * V * p.Hp);
+        p.o_exp_h = take(4 * T);
+        p.o_exp_w = take(4 * up(V, 256));  // (the last tile's columns are read whole)
+    }
     p.o_s = !bf16 && p.keep ? take(4 * T * p.ldp) : 0;
     p.o_p = gradients ? take(2 * np * T * p.ldp) : 0;
     p.o_tl = take(4 * T);
@@ -253,6 +262,9 @@ XentPlan xent_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit, bo
     } while (0)
 
 hipError_t XentRun::h_operand(void* dh) const {
+    if (p->half)
+        return launch_half_rows((const float*)h, p->T, p->H, p->Hh, at<uint16_t>(p->o_half_h), at<int>(p->o_exp_h),
+                                gradients_follow ? at<uint16_t>(p->o_h) : nullptr, st, place, (float*)dh);
     // h is always copied, without the tokens that are not counted or with zeros for them: whatever
     // they hold (a NaN too) reaches no product
     return launch_to_planes(p->bf16, h, p->T, p->H, at<uint16_t>(p->o_h), p->Hh, p->T * p->Hh,
@@ -260,6 +272,9 @@ hipError_t XentRun::h_operand(void* dh) const {
 }
 hipError_t XentRun::w_planes() const {
     if (!p->planes) return hipSuccess;
+    if (p->half)
+        return launch_half_rows((const float*)W, p->V, p->H, p->Hp, at<uint16_t>(p->o_half_w), at<int>(p->o_exp_w),
+                                gradients_follow ? at<uint16_t>(p->o_w) : nullptr, st);
     return launch_to_planes(p->bf16, W, p->V, p->H, at<uint16_t>(p->o_w), p->Hp, p->V * p->Hp, nullptr, 0, st);
 }
 
@@ -292,6 +307,14 @@ TpArgs XentRun::logit_args(int i) const {
     a.stat_first = (int64_t)i * p->logits.tiles_n;
     a.lse = at<float>(p->o_lse);
     a.live = live;
+    if (p->half) {
+        a.A = at<uint16_t>(p->o_half_h);
+        a.B = at<uint16_t>(p->o_half_w) + v0 * p->Hp;
+        a.nseg = 3;
+        a.segs = 0x0 << 8 | 0x4 << 4 | 0x1;  // the products with a second plane, then the largest
+        a.a_exp = at<int>(p->o_exp_h);
+        a.b_exp = at<int>(p->o_exp_w) + v0;
+    }
     return a;
 }
 
