@@ -395,8 +395,8 @@ int sc_mask_unpack(sc_dtype dtype, const void* packed, const int32_t* idx, int64
  * that is not given as another one; h, W, dy and workspaces must be 16-byte
  * aligned.  Calls that take a workspace need at least the bytes that their
  * query returns for the same sizes, keep nothing in it between calls, and
- * allocate nothing; every call only enqueues.  Results do not depend on timing
- * (no floating-point atomics).  Token ids and targets are int64; one outside
+ * allocate nothing; every call only enqueues.  Outputs overlap no other tensor
+ * unless said.  Results do not depend on timing (no floating-point atomics).  Token ids and targets are int64; one outside
  * [0, V) is no token: a zero row in sc_embed, no gradient in sc_embed_grad, not
  * counted in the losses.  T = 0 is allowed everywhere.
  * Errors: SC_ERR_INVALID_ARG (NULL or misaligned pointer, unknown dtype, too
@@ -521,8 +521,8 @@ int sc_grad_sumsq(int n, const sc_dtype* dtypes, const int64_t* sizes, const voi
                   void* workspace, int64_t workspace_bytes, void* stream);
 
 /* norm = sqrt(sumsq), scale = min(1, max_norm / (norm + 1e-6)) (float32 [1] each) and out[i] = grads[i] * scale;
- * out[i] may be grads[i], which then stays as it is where scale is 1.  An infinite norm gives scale 0,
- * NaN gives NaN.  max_norm >= 0. */
+ * out[i] may be grads[i], which then stays as it is where scale is 1; otherwise no output overlaps another
+ * tensor.  An infinite norm gives scale 0, NaN gives NaN.  max_norm >= 0. */
 int sc_clip_grads(int n, const sc_dtype* dtypes, const int64_t* sizes, const void* const* grads, void* const* out,
                   const double* sumsq, float max_norm, float* norm, float* scale, void* stream);
 

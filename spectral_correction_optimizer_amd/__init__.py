@@ -830,13 +830,15 @@ GradNorm.__doc__ = "Of clip_grads: the norm and the factor (float32, 0-dim) and 
 
 @functools.lru_cache(maxsize=None)
 def _marshal():
+    """tensor_table and overlap of csrc/marshal.cpp."""
     path = os.path.join(_HERE, "libscopt_marshal.so")
     if not os.path.exists(path):
         raise ScoptError(-100, f"{path} is missing; build it with __graft_entry__.build()")
-    f = ctypes.PyDLL(path).scopt_tensor_table
-    f.restype = ctypes.c_int
-    f.argtypes = [ctypes.py_object, ctypes.c_void_p, ctypes.c_int, ctypes.c_int] + [ctypes.c_void_p] * 3
-    return f
+    lib, vp, i32 = ctypes.PyDLL(path), ctypes.c_void_p, ctypes.c_int
+    table, overlap = lib.scopt_tensor_table, lib.scopt_overlap
+    table.restype, table.argtypes = i32, [ctypes.py_object, vp, i32, i32, vp, vp, vp]
+    overlap.restype, overlap.argtypes = i32, [i32, vp, vp, vp, vp]
+    return table, overlap
 
 
 def _grad_table(who, tensors, like=None):
@@ -850,7 +852,7 @@ def _grad_table(who, tensors, like=None):
     if dev.type != "cuda":
         raise ValueError(f"{who}: tensors must be on a GPU, got {dev}")
     dtypes, sizes, where = (ctypes.c_int * n)(), (ctypes.c_int64 * n)(), (ctypes.c_void_p * n)()
-    bad = _marshal()(tensors, None if like is None else id(like), n, dev.index, dtypes, sizes, where)
+    bad = _marshal()[0](tensors, None if like is None else id(like), n, dev.index, dtypes, sizes, where)
     if bad >= 0:
         t = tensors[bad]
         if not isinstance(t, torch.Tensor):
@@ -879,14 +881,18 @@ def grad_sumsq(grads) -> "torch.Tensor":
 
 def clip_grads(grads, max_norm: float, out=None, sumsq: "torch.Tensor" = None) -> GradNorm:
     """Gradients scaled to a global norm of at most max_norm: norm = sqrt(sum of all squares),
-    scale = min(1, max_norm / (norm + 1e-6)), in place or into the tensors of out.  sumsq: the sum of
-    squares where it is known already (grad_sumsq, added over the ranks)."""
+    scale = min(1, max_norm / (norm + 1e-6)), in place or into the tensors of out, none of which may share
+    memory with another one.  sumsq: the sum of squares where it is known already (grad_sumsq, added over
+    the ranks)."""
     grads = list(grads)
     dev, n, dtypes, sizes, where = _grad_table("clip_grads", grads)
     to, where_to = grads, where
     if out is not None:
         to = list(out)
         where_to = _grad_table("clip_grads", to, like=grads)[4]
+    bad = _marshal()[1](n, dtypes, sizes, where, where_to)
+    if bad >= 0:
+        raise ValueError(f"clip_grads: output {bad} shares memory with another tensor")
     both = torch.empty(4, dtype=torch.float32, device=dev)  # the norm, the factor, and room for a float64
     if sumsq is None:
         total = both.data_ptr() + 8

@@ -4,6 +4,9 @@
 #include <Python.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
+#include <vector>
+
 #include "scopt.h"
 
 namespace {
@@ -38,6 +41,42 @@ extern "C" __attribute__((visibility("default"))) int scopt_tensor_table(PyObjec
         }
     } catch (...) {
         return i;
+    }
+    return -1;
+}
+
+// Whether tensors can be written while others are read: no two outputs share memory, and an output shares an
+// input's only where it is that input (the same entry, from its start).  Returns -1, or the index of the first output
+// found that is not so.
+extern "C" __attribute__((visibility("default"))) int scopt_overlap(int n, const int* dtypes, const int64_t* sizes,
+                                                                   void* const* in, void* const* out) {
+    struct Range {
+        uintptr_t from, to;
+        int i;
+    };
+    try {
+        auto range = [&](void* const* p, int i) {
+            const uintptr_t from = (uintptr_t)p[i];
+            return Range{from, from + (uintptr_t)sizes[i] * (dtypes[i] == SC_BF16 ? 2 : 4), i};
+        };
+        std::vector<Range> written;
+        written.reserve(n);
+        for (int i = 0; i < n; ++i)
+            if (sizes[i] > 0) written.push_back(range(out, i));
+        std::sort(written.begin(), written.end(), [](const Range& a, const Range& b) { return a.from < b.from; });
+        for (size_t k = 1; k < written.size(); ++k)
+            if (written[k].from < written[k - 1].to) return written[k].i;
+        if (in == out) return -1;
+        for (int i = 0; i < n; ++i) {
+            if (sizes[i] == 0) continue;
+            const Range r = range(in, i);
+            auto w = std::upper_bound(written.begin(), written.end(), r.from,
+                                      [](uintptr_t at, const Range& x) { return at < x.to; });  // the first that ends behind
+            for (; w != written.end() && w->from < r.to; ++w)
+                if (w->i != i || w->from != r.from) return w->i;
+        }
+    } catch (...) {
+        return 0;
     }
     return -1;
 }

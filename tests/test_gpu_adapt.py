@@ -363,7 +363,7 @@ def test_preference_starts_outside():
 # ---- layer norm ----------------------------------------------------------------------------
 
 NORM_SIZES = [(1, 1), (3, 5), (9, 64), (130, 257), (6, 512), (5, 1000), (7, 2048), (4, 2051), (3, 4100), (2, 6144),
-              (2, 8192), (2, 16384), (1, 16383)]
+              (2, 8192), (2, 16384), (1, 16383), (1100, 1030), (2500, 1536), (1025, 2041)]
 
 
 @pytest.mark.parametrize("dtype", DT)
@@ -481,7 +481,8 @@ def test_layernorm_grad_against_differences():
 
 
 @pytest.mark.parametrize("dtype", DT)
-@pytest.mark.parametrize("T,H", [(40, 1000), (700, 4100), (300, 2049), (9, 8191), (5, 9001), (64, 7), (33, 2048)])
+@pytest.mark.parametrize("T,H", [(40, 1000), (700, 4100), (300, 2049), (9, 8191), (5, 9001), (64, 7), (33, 2048), (3000, 1501),
+                                 (2100, 2047), (50, 1030)])
 def test_layernorm_in_place(T, H, dtype):
     """The C entries allow h = x, h = residual, dx = dy and dx = dh."""
     say(f"case: layernorm in place T {T} H {H} {dtype}")
@@ -844,3 +845,14 @@ def test_clip_refuses_other_lists():
     with pytest.raises(m.ScoptError):
         m.clip_grads([x], -1.0)
     assert torch.equal(x, torch.ones(4, 6, device="cuda"))
+    # a tensor twice, tensors that overlap, outputs that are other inputs' memory
+    b = torch.ones(100, device="cuda")
+    for grads, out in (([x, x], None), ([b[:60], b[50:]], None), ([b[:50], b[50:]], [b[50:], b[:50]]),
+                       ([b[:40]], [b[1:41]]), ([x, y], [torch.empty_like(x), x.view(6, 4)])):
+        with pytest.raises(ValueError, match="shares memory"):
+            m.clip_grads(grads, 1.0, out=out)
+    assert torch.equal(b, torch.ones_like(b))
+    # read twice is no conflict, nor are neighbours or an input as its own output
+    m.clip_grads([b, b], 1e9, out=[torch.empty_like(b), torch.empty_like(b)])
+    m.clip_grads([b[:50], b[50:], b[:0]], 1e9)
+    m.clip_grads([b[:50], b[50:]], 1e9, out=[b[:50], torch.empty(50, device="cuda")])
