@@ -467,15 +467,19 @@ int sc_token_logp(sc_dtype dtype, const void* h, const void* W, const int64_t* t
 /* The clipped policy loss with a KL term.  For each counted token, with r = exp(logp - old_logp), A its
  * advantage and x = ref_logp - logp:
  *   loss = -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A) + kl (exp(x) - x - 1)
- * and total = the sum of weights * loss (weights NULL: the mean over the counted tokens; weight 0: the token
- * counts for nothing), with the gradients of total: dh [T][H], dW [V][H].  A token whose ratio is past the
- * clip on its advantage's side has the KL term's gradient only.  old_logp, advantages, ref_logp (NULL: kl
- * must be 0 and kl_mean NULL) and weights are float32 [T] and are not read where a token is not counted.
- * Written: loss, logp float32 [T] (0 where not counted), total, kl_mean (NULL or the mean of
- * exp(x) - x - 1), clipped (the share of tokens past the clip), float32 [1] each.  limit and workspace as
- * sc_xent's, 20 bytes a token more.  0 <= clip_low <= 1, clip_high, kl >= 0.
+ * and total = the sum of weights * loss (weights NULL: the mean over the counted tokens; a token of weight 0
+ * adds nothing to total and dW, finite or not, and its row of dh is 0), with the gradients of total:
+ * dh [T][H], dW [V][H].  A token whose ratio is past the clip on its advantage's side has the KL term's
+ * gradient only.  old_logp, advantages, ref_logp (NULL: kl must be 0 and kl_mean NULL) and weights are float32
+ * [T] and are not read where a token is not counted.  Written: loss, logp float32 [T] (0 where not counted),
+ * total, kl_mean (NULL or the mean of exp(x) - x - 1) and clipped (the share of tokens past the clip), float32
+ * [1] each; both are over all counted tokens, whatever their weights.  limit as sc_xent's; the workspace holds
+ * besides the counted tokens' places and factors, partial sums of products, and in float32 4 bytes an element
+ * of h and W for the logits.  0 <= clip_low <= 1, clip_high, kl >= 0.
  *
- * The gradients' products run over the counted tokens only; logit gradients are rounded as sc_xent's are. */
+ * The products run over the counted tokens only.  bfloat16: softmax - onehot is rounded as sc_xent's gradients
+ * are, and the rows of h that dW is summed from, times the tokens' factors, once more.  float32: a logit's
+ * factors are taken to 2^-22 of themselves (or 2^-39 of their row's largest, if that is more). */
 int sc_token_loss_workspace(sc_dtype dtype, int64_t T, int64_t V, int H, int64_t limit, int64_t* bytes);
 int sc_policy_loss(sc_dtype dtype, const void* h, const void* W, const int64_t* targets, const float* old_logp,
                    const float* advantages, const float* ref_logp, const float* weights, int64_t T, int64_t V, int H,

@@ -77,6 +77,18 @@ __device__ __forceinline__ void scale_row(int64_t t, float coef, const float* ta
         *(SC_GLOBAL v4u*)(to + t * H + i) = o;
     }
 }
+// and of float32 operands, whose coefficients are in d: row t of h's three planes becomes one of zeros where coef is 0
+__device__ __forceinline__ void clear_row(int64_t t, float coef, uint16_t* h, int64_t plane, int64_t H) {
+    if (coef != 0.0f) return;
+    for (int64_t i = 8 * threadIdx.x; i < H; i += 8 * 256)
+#pragma unroll
+        for (int k = 0; k < 3; ++k) *(SC_GLOBAL v4u*)(h + k * plane + t * H + i) = v4u{0, 0, 0, 0};
+}
+__global__ __launch_bounds__(256) void clear_rows_kernel(const int* __restrict__ live, const float* __restrict__ coef,
+                                                         uint16_t* h, int64_t plane, int64_t H) {
+    const int64_t t = blockIdx.x;
+    if (t < gld(live)) clear_row(t, gld(coef + t), h, plane, H);
+}
 __global__ __launch_bounds__(256) void scale_rows_kernel(const int* __restrict__ live, const float* __restrict__ coef,
                                                          const float* __restrict__ target_logit,
                                                          const float* __restrict__ lse, float* __restrict__ factor,
@@ -87,8 +99,8 @@ __global__ __launch_bounds__(256) void scale_rows_kernel(const int* __restrict__
 }
 
 // d from what the logits product kept: exponentials in 16 bits (in place) or float32 logits
-// (into three planes).  `chunks` workgroups a row; a thread takes 8 columns at a time.  With coef and EXP the
-// row's first workgroup scales its row of h, and d has only coef's zeros.
+// (into three planes).  `chunks` workgroups a row; a thread takes 8 columns at a time.  With coef the row's first
+// workgroup also sees to its row of h (EXP: scaled, and d has only coef's zeros).
 template <bool EXP>
 __global__ __launch_bounds__(256) void xent_dlogits_kernel(const float* __restrict__ logits, uint16_t* P,
                                                            int64_t plane, int64_t ldp, int N, int bn,
@@ -104,9 +116,14 @@ __global__ __launch_bounds__(256) void xent_dlogits_kernel(const float* __restri
     const int64_t t = blockIdx.x / chunks;
     if (live && t >= gld(live)) return;
     float scale = gld(coef ? coef + t : scale_at);
-    if (EXP && coef) {
-        if (blockIdx.x % chunks == 0) scale_row(t, scale, target_logit, lse, factor, h, h, Hh);
-        scale = scale != 0.0f ? 1.0f : 0.0f;
+    if (coef) {
+        if (blockIdx.x % chunks == 0) {
+            if constexpr (EXP)
+                scale_row(t, scale, target_logit, lse, factor, h, h, Hh);
+            else
+                clear_row(t, scale, h, T * Hh, Hh);
+        }
+        if constexpr (EXP) scale = scale != 0.0f ? 1.0f : 0.0f;
     }
     // a row without weight is one of zeros, whatever its logits are
     const int64_t tgt = scale != 0.0f ? tp_target(targets, V, t) : -1;
@@ -357,6 +374,10 @@ hipError_t XentRun::gradients(void* dh, void* dW) const {
         hipLaunchKernelGGL(scale_rows_kernel, dim3((unsigned)T), dim3(256), 0, st, live, coef, at<float>(p->o_tl),
                            at<float>(p->o_lse), at<float>(p->o_factor), at<uint16_t>(p->o_h),
                            at<uint16_t>(p->o_scaled), p->Hh);
+        SC_RUN(hipGetLastError());
+    } else if (coef && !p->bf16 && !p->keep) {
+        hipLaunchKernelGGL(clear_rows_kernel, dim3((unsigned)T), dim3(256), 0, st, live, coef, at<uint16_t>(p->o_h),
+                           T * p->Hh, p->Hh);
         SC_RUN(hipGetLastError());
     }
     for (int i = 0; i < p->pieces; ++i) {

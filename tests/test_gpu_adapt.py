@@ -294,7 +294,7 @@ def test_token_losses_of_nothing(dtype):
 
 
 @pytest.mark.parametrize("dtype", DT)
-@pytest.mark.parametrize("limit", [0, 1])
+@pytest.mark.parametrize("limit", [0, 1])  # (1: in pieces)
 def test_policy_nonfinite_and_weightless_tokens(dtype, limit):
     """A counted token with NaN states has a NaN loss and gradient and leaves the other tokens' losses; with
     weight 0 it changes no gradient but its own row's, which is zero."""
@@ -320,6 +320,12 @@ def test_policy_nonfinite_and_weightless_tokens(dtype, limit):
     assert out.loss[20].isinf()
     assert torch.equal(out.total, want.total) and torch.equal(out.dh, want.dh) and torch.equal(out.dW, want.dW)
     assert torch.count_nonzero(out.dh[20]) == 0
+    # and states that are not finite, of a token without weight: its own loss alone
+    for x in (math.nan, math.inf):
+        bad[20, 5] = x
+        out = m.policy_loss(bad, W, tgt, old, f, weights=w, limit=limit)
+        assert out.loss[20].isnan() and torch.equal(out.loss[rest], want.loss[rest])
+        assert torch.equal(out.total, want.total) and torch.equal(out.dh, want.dh) and torch.equal(out.dW, want.dW)
 
 
 def test_policy_clip_sides():
@@ -844,7 +850,6 @@ def test_clip_refuses_other_lists():
             m.clip_grads([x], 1.0, sumsq=s)
     with pytest.raises(m.ScoptError):
         m.clip_grads([x], -1.0)
-    assert torch.equal(x, torch.ones(4, 6, device="cuda"))
     # a tensor twice, tensors that overlap, outputs that are other inputs' memory
     b = torch.ones(100, device="cuda")
     for grads, out in (([x, x], None), ([b[:60], b[50:]], None), ([b[:50], b[50:]], [b[50:], b[:50]]),
@@ -856,3 +861,4 @@ def test_clip_refuses_other_lists():
     m.clip_grads([b, b], 1e9, out=[torch.empty_like(b), torch.empty_like(b)])
     m.clip_grads([b[:50], b[50:], b[:0]], 1e9)
     m.clip_grads([b[:50], b[50:]], 1e9, out=[b[:50], torch.empty(50, device="cuda")])
+    assert torch.equal(x, torch.ones(4, 6, device="cuda"))
