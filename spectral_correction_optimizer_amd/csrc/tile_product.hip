@@ -147,8 +147,12 @@ __global__ __launch_bounds__(256) void tp_stats_tail_kernel(const TpArgs P) {
         for (int o = 32; o > 0; o >>= 1) z += __shfl_xor(z, o);
         if (pow2) {
             uint32_t* to = (uint32_t*)((uint16_t*)P.P + (int64_t)m * P.ldp + n);
+            const float row_ref = P.row_ref ? gld(P.row_ref + m) : 0.0f;
+            const bool by_row = P.row_ref && tp_by_row(ref, row_ref);
+            const float unit = __builtin_amdgcn_exp2f(ref - row_ref);
 #pragma unroll
-            for (int c = 0; c < C; c += 2) gst(to + c / 2, tp_pack_unit(e[c], e[c + 1]));
+            for (int c = 0; c < C; c += 2)
+                gst(to + c / 2, by_row ? pack_bf16x2(e[c] * unit, e[c + 1] * unit) : tp_pack_unit(e[c], e[c + 1]));
         } else if (P.keep == TP_KEEP_LOGIT) {
             float* to = (float*)P.P + (int64_t)m * P.ldp + n;
 #pragma unroll

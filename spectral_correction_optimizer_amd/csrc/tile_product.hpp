@@ -260,6 +260,13 @@ __device__ __forceinline__ uint32_t tp_pack_unit(float a, float b) {
 __device__ __forceinline__ float tp_unit_lo(uint32_t w) { return __uint_as_float((w & 0xffffu) << 14); }
 __device__ __forceinline__ float tp_unit_hi(uint32_t w) { return __uint_as_float(w >> 16 << 14); }
 
+// Where the references of the rows are known beforehand (TpArgs::row_ref), a tile's exponentials are kept
+// relative to its row's, and are the row's gradients but for a factor: as long as the tile's own reference is no
+// more than 2^kByRow above it (a NaN is no such reference).  Bfloat16's exponents leave room for the
+// products of such values and for the factors, their inverses.
+constexpr float kByRow = 64.0f;
+__device__ __forceinline__ bool tp_by_row(float ref, float row_ref) { return ref - row_ref <= kByRow; }
+
 // What becomes of a tile's sums.
 enum TpEpi {
     TP_STORE = 0,   // C = acc * alpha * gain[n], bfloat16 or float32
@@ -695,7 +702,15 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
 #pragma unroll
                 for (int w = 1; w < S::WVN; ++w) mx = fmaxf(mx, red[w * BM + wm + 16 * i + (lane & 15)]);
                 const float ref = tp_reference(mx, pow2);
-                float z = 0.0f;
+                float z = 0.0f, unit = 1.0f;
+                bool by_row = false;
+                if constexpr (EPI == TP_STATS_TAIL && !HALF) {
+                    if (P.row_ref) {
+                        const float to = gld(P.row_ref + min(m, M - 1));
+                        by_row = tp_by_row(ref, to);
+                        unit = __builtin_amdgcn_exp2f(ref - to);
+                    }
+                }
                 uint32_t d[NI][2];
                 if (pow2) {
 #pragma unroll
@@ -706,8 +721,13 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
                             e[r] = __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], kLog2e, -ref));
                             z += e[r];
                         }
-                        d[j][0] = tp_pack_unit(e[0], e[1]);
-                        d[j][1] = tp_pack_unit(e[2], e[3]);
+                        if (by_row) {
+                            d[j][0] = pack_bf16x2(e[0] * unit, e[1] * unit);
+                            d[j][1] = pack_bf16x2(e[2] * unit, e[3] * unit);
+                        } else {
+                            d[j][0] = tp_pack_unit(e[0], e[1]);
+                            d[j][1] = tp_pack_unit(e[2], e[3]);
+                        }
                     }
                     uint16_t* p = (uint16_t*)P.P + (int64_t)m * P.ldp;
                     const int c = tp_gather_row<NI>(d);

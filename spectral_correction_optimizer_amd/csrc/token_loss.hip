@@ -335,6 +335,7 @@ hipError_t forward(const TokenLossPlan& p, XentRun& run, bool gradients, const v
         SC_RUN(run.h_operand(dh));
     }
     SC_RUN(run.w_planes());
+    SC_RUN(run.row_references());
     SC_RUN(run.logits());
     return run.log_sums(nullptr, logp);
 }

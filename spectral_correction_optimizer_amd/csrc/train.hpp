@@ -94,6 +94,9 @@ struct TpArgs {
     // Operands in float16: row m of A stands for 2^a_exp[m] times its planes, row n of B for 2^b_exp[n] times
     // (16-byte aligned, readable to the end of the last tile)
     const int *a_exp = nullptr, *b_exp = nullptr;
+    // The live logits' statistics with TP_KEEP_EXP: a power of two for each row (its exponent, or NULL).  A tile's row
+    // is kept relative to it, in bfloat16, where tp_by_row says so.
+    const float* row_ref = nullptr;
 };
 
 // The product's operand layouts and what is done with its sums.
@@ -167,8 +170,9 @@ struct XentPlan {
     TpPlan logits, logits_last, dh, dw, dw_last;
     TpTailQuery tails[5];      // of live tokens: dh, dw, dw_last, logits, logits_last
     bool half;                 // live tokens in float32: the logits' operands are float16 planes
+    bool by_row;               // kept exponentials of live tokens are relative to a reference of their row
     // offsets into the workspace
-    int64_t o_factors, o_h, o_scaled, o_w, o_s, o_p, o_tl, o_lse, o_smax, o_ssum, o_part, o_dh, o_tails, o_factor;
+    int64_t o_factors, o_h, o_scaled, o_w, o_s, o_p, o_tl, o_lse, o_smax, o_ssum, o_part, o_dh, o_tails, o_factor, o_ref;
     int64_t o_half_h, o_half_w, o_exp_h, o_exp_w, bytes;
 };
 // limit: bytes that the kept probabilities (or a piece's) may take; gradients = false: only the logits'
@@ -210,6 +214,7 @@ struct XentRun {
     // (with rows; else NULL)
     hipError_t h_operand(void* dh) const;
     hipError_t w_planes() const;
+    hipError_t row_references() const;
     hipError_t logits() const;                       // row statistics, and what is kept
     LogSums sums() const;
     hipError_t log_sums(float* loss, float* logp) const;  // lse; the tokens' losses, or with rows their negative

@@ -58,16 +58,49 @@ __global__ __launch_bounds__(1024) void token_lse_kernel(const LogSums a, const 
     log_sums<16>(a, end, (int64_t)blockIdx.x * 16, red, [&](int64_t t, float lp) { gst(logp + gld(rows + t), lp); });
 }
 
+// The power of two that a token's exponentials are kept relative to (XentPlan::by_row): 2^32 times its target's, whose
+// logit is formed here for that alone.  A wavefront a row.
+__global__ __launch_bounds__(256) void row_reference_kernel(const int* __restrict__ live,
+                                                            const uint16_t* __restrict__ h, int64_t ldh,
+                                                            const uint16_t* __restrict__ W, int64_t ldw,
+                                                            const int64_t* __restrict__ targets, int H,
+                                                            float* __restrict__ ref) {
+    const int64_t t = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
+    if (t >= gld(live)) return;
+    const uint16_t *a = h + t * ldh, *b = W + gld(targets + t) * ldw;
+    float s = 0.0f;
+#pragma unroll 4
+    for (int i = 8 * (threadIdx.x & 63); i < H; i += 512) {
+        const v4u x = *(const SC_GLOBAL v4u*)(a + i), y = *(const SC_GLOBAL v4u*)(b + i);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            s = fmaf(bf16_lo(x[k]), bf16_lo(y[k]), s);
+            s = fmaf(bf16_hi(x[k]), bf16_hi(y[k]), s);
+        }
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
+    // (none for a logit past 2^16, whose last bits are the order of its sum)
+    if ((threadIdx.x & 63) == 0)
+        gst(ref + t, fabsf(s) < 0x1p16f ? ceilf(s * kLog2e) + 32.0f : __builtin_nanf(""));
+}
+// Whether all of a row's tiles are kept relative to its reference: no tile's own is above the next power of two
+// of the row's sum by more than one.
+__device__ __forceinline__ bool kept_by_row(float lse, float row_ref) {
+    return tp_by_row(fmaf(lse, kLog2e, 3.0f), row_ref);
+}
 // softmax - onehot at a token's target, as the logit gradients of live tokens hold it
 __device__ __forceinline__ float target_entry(float target_logit, float lse) {
     return __builtin_amdgcn_exp2f((target_logit - lse) * kLog2e) - 1.0f;
 }
 // 256 threads: row t's factor, coef times what bfloat16's rounding took from the target's entry, and its H states
-// times that.  A coefficient of 0 gives zeros, whatever the states are.
-__device__ __forceinline__ void scale_row(int64_t t, float coef, const float* target_logit, const float* lse,
-                                          float* factor, const uint16_t* from, uint16_t* to, int64_t H) {
-    const float q = target_entry(gld(target_logit + t), gld(lse + t)), r = bf16_to_f32(f32_to_bf16(q));
-    const float c = coef != 0.0f && r != 0.0f ? coef * (q / r) : coef;
+// times that.  A coefficient of 0 gives zeros, whatever the states are.  d's row is softmax - onehot times 2^up;
+// returns its target's entry.
+__device__ __forceinline__ float scale_row(int64_t t, float coef, float up, const float* target_logit, const float* lse,
+                                           float* factor, const uint16_t* from, uint16_t* to, int64_t H) {
+    const float q = target_entry(gld(target_logit + t), gld(lse + t)), unit = __builtin_amdgcn_exp2f(up);
+    const float r = bf16_to_f32(f32_to_bf16(q * unit));
+    const float c = coef != 0.0f && r != 0.0f ? coef * (q / r) : coef / unit;
     if (threadIdx.x == 0) gst(factor + t, c);
     for (int64_t i = 8 * threadIdx.x; i < H; i += 8 * 256) {
         const v4u w = *(const SC_GLOBAL v4u*)(from + t * H + i);
@@ -76,6 +109,7 @@ __device__ __forceinline__ void scale_row(int64_t t, float coef, const float* ta
         for (int k = 0; k < 4; ++k) o[k] = coef != 0.0f ? pack_bf16x2(bf16_lo(w[k]) * c, bf16_hi(w[k]) * c) : 0u;
         *(SC_GLOBAL v4u*)(to + t * H + i) = o;
     }
+    return r;
 }
 // and of float32 operands, whose coefficients are in d: row t of h's three planes becomes one of zeros where coef is 0
 __device__ __forceinline__ void clear_row(int64_t t, float coef, uint16_t* h, int64_t plane, int64_t H) {
@@ -95,12 +129,14 @@ __global__ __launch_bounds__(256) void scale_rows_kernel(const int* __restrict__
                                                          const uint16_t* __restrict__ from, uint16_t* __restrict__ to,
                                                          int64_t H) {
     const int64_t t = blockIdx.x;
-    if (t < gld(live)) scale_row(t, gld(coef + t), target_logit, lse, factor, from, to, H);
+    if (t < gld(live)) (void)scale_row(t, gld(coef + t), 0.0f, target_logit, lse, factor, from, to, H);
 }
 
 // d from what the logits product kept: exponentials in 16 bits (in place) or float32 logits
 // (into three planes).  `chunks` workgroups a row; a thread takes 8 columns at a time.  With coef the row's first
-// workgroup also sees to its row of h (EXP: scaled, and d has only coef's zeros).
+// workgroup also sees to its row of h (EXP: scaled, and d has only coef's zeros).  A row that was kept relative to
+// row_ref is softmax - onehot already, but for its target's entry and a factor, which joins coef: where the
+// reference is ref, 2^ref / exp(lse).  (8192 tokens, half of them counted, x 131072: 425 us for all rows anew.)
 template <bool EXP>
 __global__ __launch_bounds__(256) void xent_dlogits_kernel(const float* __restrict__ logits, uint16_t* P,
                                                            int64_t plane, int64_t ldp, int N, int bn,
@@ -112,17 +148,23 @@ __global__ __launch_bounds__(256) void xent_dlogits_kernel(const float* __restri
                                                            const float* __restrict__ scale_at,
                                                            const int* __restrict__ live,
                                                            const float* __restrict__ coef, float* factor, uint16_t* h,
-                                                           int64_t Hh) {
+                                                           int64_t Hh, const float* __restrict__ row_ref) {
     const int64_t t = blockIdx.x / chunks;
     if (live && t >= gld(live)) return;
     float scale = gld(coef ? coef + t : scale_at);
+    const float to_row = EXP && row_ref ? gld(row_ref + t) : 0.0f;
+    const bool done = EXP && row_ref && kept_by_row(gld(lse + t), to_row);
     if (coef) {
         if (blockIdx.x % chunks == 0) {
-            if constexpr (EXP)
-                scale_row(t, scale, target_logit, lse, factor, h, h, Hh);
-            else
+            if constexpr (EXP) {
+                const float up = done ? fmaf(gld(lse + t), kLog2e, -to_row) : 0.0f;
+                const float r = scale_row(t, scale, up, target_logit, lse, factor, h, h, Hh);
+                if (done && threadIdx.x == 0) gst(P + t * ldp + gld(targets + t), f32_to_bf16(r));
+            } else {
                 clear_row(t, scale, h, T * Hh, Hh);
+            }
         }
+        if (done) return;
         if constexpr (EXP) scale = scale != 0.0f ? 1.0f : 0.0f;
     }
     // a row without weight is one of zeros, whatever its logits are
@@ -139,11 +181,13 @@ __global__ __launch_bounds__(256) void xent_dlogits_kernel(const float* __restri
         float v[8];
         if constexpr (EXP) {
             const v4u w = *(const SC_GLOBAL v4u*)p;
-            const float f = __builtin_amdgcn_exp2f(gld(smax + (int64_t)(c / bn) * T + t) - ls2) * scale;
+            const float ref = gld(smax + (int64_t)(c / bn) * T + t);
+            const bool by_row = row_ref && tp_by_row(ref, to_row);
+            const float f = __builtin_amdgcn_exp2f((by_row ? to_row : ref) - ls2) * scale;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                v[2 * i] = tp_unit_lo(w[i]) * f;
-                v[2 * i + 1] = tp_unit_hi(w[i]) * f;
+                v[2 * i] = (by_row ? bf16_lo(w[i]) : tp_unit_lo(w[i])) * f;
+                v[2 * i + 1] = (by_row ? bf16_hi(w[i]) : tp_unit_hi(w[i])) * f;
             }
         } else {
             const v4f a = gld4(logits + t * ldp + c), b = gld4(logits + t * ldp + c + 4);
@@ -268,6 +312,8 @@ XentPlan xent_plan(bool bf16, int64_t T, int64_t V, int64_t H, int64_t limit, bo
     p.o_dh = join ? take(4 * T * H) : 0;
     if (live) p.o_tails = take(5 * sizeof(TpTail));
     if (live && gradients) p.o_factor = take(4 * T);
+    p.by_row = live && bf16 && p.keep && T * V >= 1 << 24;
+    if (p.by_row) p.o_ref = take(4 * T);
     p.bytes = o;
     return p;
 }
@@ -293,6 +339,13 @@ hipError_t XentRun::w_planes() const {
         return launch_half_rows((const float*)W, p->V, p->H, p->Hp, at<uint16_t>(p->o_half_w), at<int>(p->o_exp_w),
                                 gradients_follow ? at<uint16_t>(p->o_w) : nullptr, st);
     return launch_to_planes(p->bf16, W, p->V, p->H, at<uint16_t>(p->o_w), p->Hp, p->V * p->Hp, nullptr, 0, st);
+}
+
+hipError_t XentRun::row_references() const {
+    if (!p->by_row) return hipSuccess;
+    hipLaunchKernelGGL(row_reference_kernel, dim3((unsigned)((p->T + 3) / 4)), dim3(256), 0, st, live,
+                       at<uint16_t>(p->o_h), p->Hh, w_operand(), p->Hp, targets, (int)up(p->H, 8), at<float>(p->o_ref));
+    return hipGetLastError();
 }
 
 // planes (A | B << 2) of the six products of two split operands, smallest first
@@ -324,6 +377,7 @@ TpArgs XentRun::logit_args(int i) const {
     a.stat_first = (int64_t)i * p->logits.tiles_n;
     a.lse = at<float>(p->o_lse);
     a.live = live;
+    if (p->by_row) a.row_ref = at<float>(p->o_ref);
     if (p->half) {
         a.A = at<uint16_t>(p->o_half_h);
         a.B = at<uint16_t>(p->o_half_w) + v0 * p->Hp;
@@ -392,7 +446,8 @@ hipError_t XentRun::gradients(void* dh, void* dW) const {
             hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, p->bf16 ? nullptr : at<float>(p->o_s), P, T * p->ldp,
                                p->ldp, n, p->logits.bn, chunk, chunks, at<float>(p->o_smax), T, at<float>(p->o_lse),
                                at<float>(p->o_tl), targets, V, factors + 1, live, coef,
-                               at<float>(p->o_factor), at<uint16_t>(p->o_h), p->Hh);
+                               at<float>(p->o_factor), at<uint16_t>(p->o_h), p->Hh,
+                               p->by_row ? at<float>(p->o_ref) : nullptr);
             SC_RUN(hipGetLastError());
         } else {
             TpArgs a = logit_args(i);

@@ -328,6 +328,46 @@ def test_policy_nonfinite_and_weightless_tokens(dtype, limit):
         assert torch.equal(out.total, want.total) and torch.equal(out.dh, want.dh) and torch.equal(out.dW, want.dW)
 
 
+@pytest.mark.parametrize("spread", [1.0, 12.0, 60.0])
+@pytest.mark.parametrize("kind", ["runs", "none"])
+def test_policy_many_logits(kind, spread):
+    """Enough bfloat16 logits for them to be kept relative to their rows' references (2^24): also in rows whose
+    targets are far from likely, where some tiles are out of the reference's reach or all are, and in rows of
+    weight 0 or that are not finite."""
+    m, g = sco(), gen(39)
+    T, V, H, clip = 700, 24100, 72, (0.2, 0.28)
+    h, W, tgt = _xent_case(g, T, V, H, torch.bfloat16)
+    h[::3] *= spread  # (a power of two or not: the reference reads what the product reads)
+    tgt = _mask(tgt, kind, V)
+    ref = Tokens(h, W, tgt, torch.bfloat16)
+    old, adv, refl, w = _policy_inputs(g, ref, clip)
+    args = dict(ref_logp=refl.cuda(), weights=w.cuda() / T, clip=clip, kl=0.05)
+    w = w / T
+    out = m.policy_loss(h, W, tgt, old.cuda(), adv.cuda(), **args)
+    loss, dloss, total, dtotal, k3, clipped, c, dc, count = _policy_ref(ref, old, adv, refl, w, clip, 0.05)
+    within("logp", out.logp.cpu(), ref.logp, ref.dlogp)
+    within("loss", out.loss.cpu(), loss, dloss)
+    within("total", out.total.cpu(), total, dtotal)
+    dh, dW, tdh, tdW = ref.gradients(c, dc)
+    within("dh", out.dh.cpu(), dh, tdh)
+    within("dW", out.dW.cpu(), dW, tdW)
+    for a, b in zip(out, m.policy_loss(h, W, tgt, old.cuda(), adv.cuda(), **args)):
+        assert torch.equal(a, b)
+    # tokens of weight 0 (every fifth) whose states are not finite
+    bad = h.clone()
+    bad[60, 7], bad[65, 3], bad[70] = math.nan, math.inf, -math.inf
+    other = m.policy_loss(bad, W, tgt, old.cuda(), adv.cuda(), **args)
+    assert torch.equal(other.dW, out.dW) and torch.equal(other.dh, out.dh) and torch.equal(other.total, out.total)
+    # and one with a weight: its own row, and no other
+    row = 71 if kind == "runs" else 2
+    row = next(t for t in range(row, T) if ref.ok[t] and t % 5)
+    bad = h.clone()
+    bad[row, 7] = math.nan
+    other = m.policy_loss(bad, W, tgt, old.cuda(), adv.cuda(), **args)
+    rest = torch.arange(T, device="cuda") != row
+    assert torch.equal(other.dh[rest], out.dh[rest]) and other.dh[row].isnan().all() and other.dW.isnan().all()
+
+
 def test_policy_clip_sides():
     """On either side of the clip, with advantages of either sign and none: which tokens are stopped."""
     m, g = sco(), gen(37)
