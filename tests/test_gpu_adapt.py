@@ -902,3 +902,21 @@ def test_clip_refuses_other_lists():
     m.clip_grads([b[:50], b[50:], b[:0]], 1e9)
     m.clip_grads([b[:50], b[50:]], 1e9, out=[b[:50], torch.empty(50, device="cuda")])
     assert torch.equal(x, torch.ones(4, 6, device="cuda"))
+
+
+def test_clip_more_chunks_than_workgroups():
+    """Enough elements for the workgroups to take several chunks each; odd ends, some tensors in place."""
+    m = sco()
+    sizes = [200_000_003, 8192 * 9000, 5, 1_000_001]
+    grads = [torch.full((n,), 0.5, device="cuda", dtype=torch.bfloat16) for n in sizes]
+    out = [grads[0], torch.zeros_like(grads[1]), grads[2], torch.zeros_like(grads[3])]
+    norm = 0.5 * math.sqrt(sum(sizes))
+    r = m.clip_grads(grads, norm / 2, out=out)
+    assert r.norm.item() == pytest.approx(norm, rel=2 * U) and r.scale.item() == pytest.approx(0.5, rel=1e-6)
+    for x in out:  # 0.25 but for the factor's last bits, which bfloat16 has none of
+        assert (x == 0.25).all()
+    assert (grads[1] == 0.5).all() and (grads[3] == 0.5).all()
+    r = m.clip_grads([grads[1]], 1e9)  # not reached: as they are
+    assert r.scale.item() == 1.0 and (grads[1] == 0.5).all()
+    r = m.clip_grads([grads[1]], 1e9, out=[out[1]])
+    assert torch.equal(out[1], grads[1])
