@@ -920,3 +920,48 @@ def test_clip_more_chunks_than_workgroups():
     assert r.scale.item() == 1.0 and (grads[1] == 0.5).all()
     r = m.clip_grads([grads[1]], 1e9, out=[out[1]])
     assert torch.equal(out[1], grads[1])
+
+
+@pytest.mark.parametrize("T,V,kind", [(128, 140001, "half"), (100, 170001, "none")])
+def test_policy_few_tokens_many_logits(T, V, kind):
+    """Few tokens' own products of logits and weights' gradient, with logits relative to their rows' references."""
+    H = 72
+    g = gen(67)
+    h, W, tgt = _xent_case(g, T, V, H, torch.bfloat16)
+    h[1::4] *= 40.0  # some out of their references' reach
+    tgt = _mask(tgt, kind, V)
+    ref = Tokens(h, W, tgt, torch.bfloat16)
+    old, adv, refl, _ = _policy_inputs(g, ref, (0.2, 0.2))
+    out = sco().policy_loss(h, W, tgt, old.cuda(), adv.cuda(), ref_logp=refl.cuda(), kl=0.02)
+    loss, dloss, _, _, _, _, c, dc, _ = _policy_ref(ref, old, adv, refl, None, (0.2, 0.2), 0.02)
+    within("loss", out.loss.cpu(), loss, dloss)
+    dh, dW, tdh, tdW = ref.gradients(c, dc)
+    within("dh", out.dh.cpu(), dh, tdh)
+    within("dW", out.dW.cpu(), dW, tdW)
+
+
+def test_many_logits_graph_replays():
+    """Losses whose logits are relative to their rows' references, captured and replayed on other tokens."""
+    m, g = sco(), gen(68)
+    T, V, H = 640, 27000, 128
+    h, W, tgt = _xent_case(g, T, V, H, torch.bfloat16)
+    f = randn(g, T, std=0.3)
+    starts = torch.tensor([0, 200, 380, 500, 640], device="cuda")
+
+    def step():
+        lp = m.token_logp(h, W, tgt)
+        return [lp, *m.policy_loss(h, W, tgt, lp + f, f, ref_logp=lp - f, kl=0.1), *m.preference_loss(h, W, tgt, starts)]
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for k, share in enumerate((0.5, 0.0, 1.0, 0.1)):
+        h.copy_(randn(g, T, H, std=(0.1, 1.0, 0.3, 4.0)[k], dtype=torch.bfloat16))
+        t = torch.randint(0, V, (T,), generator=g, device="cuda")
+        tgt.copy_(torch.where(torch.rand(T, generator=g, device="cuda") < share, -1, t))
+        want = [x.clone() for x in step()]
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(want, out):
+            assert torch.equal(a, b), k
