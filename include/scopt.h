@@ -530,6 +530,10 @@ int sc_grad_sumsq(int n, const sc_dtype* dtypes, const int64_t* sizes, const voi
 int sc_clip_grads(int n, const sc_dtype* dtypes, const int64_t* sizes, const void* const* grads, void* const* out,
                   const double* sumsq, float max_norm, float* norm, float* scale, void* stream);
 
+/* Both in one call.  Workspace: sc_grad_sumsq_workspace. */
+int sc_clip_norm(int n, const sc_dtype* dtypes, const int64_t* sizes, const void* const* grads, void* const* out,
+                 float max_norm, float* norm, float* scale, void* workspace, int64_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

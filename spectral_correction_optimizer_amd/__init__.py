@@ -43,7 +43,7 @@ EXPORTED_SYMBOLS = (
     "sc_rmsnorm_grad_workspace", "sc_rmsnorm_grad", "sc_act_wgrad_workspace", "sc_act_wgrad",
     "sc_xent_workspace", "sc_xent", "sc_token_logp_workspace", "sc_token_logp", "sc_token_loss_workspace",
     "sc_policy_loss", "sc_preference_loss", "sc_layernorm", "sc_layernorm_grad_workspace", "sc_layernorm_grad",
-    "sc_grad_sumsq_workspace", "sc_grad_sumsq", "sc_clip_grads",
+    "sc_grad_sumsq_workspace", "sc_grad_sumsq", "sc_clip_grads", "sc_clip_norm",
 )
 
 SC_F32, SC_BF16 = 0, 1
@@ -161,6 +161,7 @@ def load_library():
         "sc_grad_sumsq_workspace": (i32, [i32, vp, vp, i64p]),
         "sc_grad_sumsq": (i32, [i32, vp, vp, vp, vp, vp, i64, vp]),
         "sc_clip_grads": (i32, [i32, vp, vp, vp, vp, vp, f32, vp, vp, vp]),
+        "sc_clip_norm": (i32, [i32, vp, vp, vp, vp, f32, vp, vp, vp, i64, vp]),
     })
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -787,8 +788,8 @@ def layernorm(x: "torch.Tensor", gain: "torch.Tensor", bias: "torch.Tensor" = No
     mean, rstd = torch.empty(2, T, dtype=torch.float32, device=dev).unbind()
     kept = None
     if keep:
-        kept = ActCheckpoint(torch.empty((T, H), dtype=torch.int8, device=dev),
-                             torch.empty((T, -(-H // 32)), dtype=torch.uint8, device=dev))
+        kept = ActCheckpoint(torch.empty(T, H, dtype=torch.int8, device=dev),
+                             torch.empty(T, -(-H // 32), dtype=torch.uint8, device=dev))
     _run(dev, load_library().sc_layernorm, _DT[x.dtype], x.data_ptr(), _ptr(residual), gain.data_ptr(), _ptr(bias),
          float(eps), T, H, None if residual is None else h.data_ptr(), y.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
          kept.q.data_ptr() if keep else None, kept.e.data_ptr() if keep else None)
@@ -841,8 +842,9 @@ def _marshal():
     return table, overlap
 
 
-def _grad_table(who, tensors, like=None):
-    """Device and host arrays (types, sizes, pointers) of a list of gradients; like: the list that they have to match."""
+def _grad_table(who, tensors, like=None, arrays=None):
+    """Device and host arrays (types, sizes, pointers) of a list of gradients; like: the list that they have to match,
+    arrays: its types and sizes."""
     n = len(tensors)
     if n == 0:
         raise ValueError(f"{who}: no tensors")
@@ -851,7 +853,8 @@ def _grad_table(who, tensors, like=None):
     dev = (tensors if like is None else like)[0].device
     if dev.type != "cuda":
         raise ValueError(f"{who}: tensors must be on a GPU, got {dev}")
-    dtypes, sizes, where = (ctypes.c_int * n)(), (ctypes.c_int64 * n)(), (ctypes.c_void_p * n)()
+    dtypes, sizes = arrays or ((ctypes.c_int * n)(), (ctypes.c_int64 * n)())
+    where = (ctypes.c_void_p * n)()
     bad = _marshal()[0](tensors, None if like is None else id(like), n, dev.index, dtypes, sizes, where)
     if bad >= 0:
         t = tensors[bad]
@@ -863,19 +866,20 @@ def _grad_table(who, tensors, like=None):
     return dev, n, dtypes, sizes, where
 
 
-def _sumsq(dev, n, dtypes, sizes, where, sumsq):
-    lib, size = load_library(), ctypes.c_int64()
-    _check(lib.sc_grad_sumsq_workspace(n, dtypes, sizes, ctypes.byref(size)))
-    ws = torch.empty(size.value, dtype=torch.uint8, device=dev)
-    _run(dev, lib.sc_grad_sumsq, n, dtypes, sizes, where, sumsq, ws.data_ptr(), size.value)
+def _sumsq_workspace(n, dtypes, sizes):
+    size = ctypes.c_int64()
+    _check(load_library().sc_grad_sumsq_workspace(n, dtypes, sizes, ctypes.byref(size)))
+    return size.value
 
 
 def grad_sumsq(grads) -> "torch.Tensor":
     """The sum of squares (float64, 0-dim) of a list of float32 or bfloat16 tensors of any shapes, in a
     fixed order.  Where gradients are sharded, the ranks' sums added up go to clip_grads."""
-    dev, *table = _grad_table("grad_sumsq", list(grads))
+    dev, n, dtypes, sizes, where = _grad_table("grad_sumsq", list(grads))
     sumsq = torch.empty((), dtype=torch.float64, device=dev)
-    _sumsq(dev, *table, sumsq.data_ptr())
+    size = _sumsq_workspace(n, dtypes, sizes)
+    ws = torch.empty(size, dtype=torch.uint8, device=dev)
+    _run(dev, load_library().sc_grad_sumsq, n, dtypes, sizes, where, sumsq.data_ptr(), ws.data_ptr(), size)
     return sumsq
 
 
@@ -889,18 +893,18 @@ def clip_grads(grads, max_norm: float, out=None, sumsq: "torch.Tensor" = None) -
     to, where_to = grads, where
     if out is not None:
         to = list(out)
-        where_to = _grad_table("clip_grads", to, like=grads)[4]
+        where_to = _grad_table("clip_grads", to, like=grads, arrays=(dtypes, sizes))[4]
     bad = _marshal()[1](n, dtypes, sizes, where, where_to)
     if bad >= 0:
         raise ValueError(f"clip_grads: output {bad} shares memory with another tensor")
-    both = torch.empty(4, dtype=torch.float32, device=dev)  # the norm, the factor, and room for a float64
+    norm, scale = torch.empty(2, dtype=torch.float32, device=dev).unbind()
     if sumsq is None:
-        total = both.data_ptr() + 8
-        _sumsq(dev, n, dtypes, sizes, where, total)
+        size = _sumsq_workspace(n, dtypes, sizes)
+        ws = torch.empty(size, dtype=torch.uint8, device=dev)
+        _run(dev, load_library().sc_clip_norm, n, dtypes, sizes, where, where_to, float(max_norm), norm.data_ptr(),
+             scale.data_ptr(), ws.data_ptr(), size)
     else:
         _train_check("clip_grads", torch.float32, dev, ("sumsq", sumsq, torch.float64, ()))
-        total = sumsq.data_ptr()
-    _run(dev, load_library().sc_clip_grads, n, dtypes, sizes, where, where_to, total, float(max_norm),
-         both.data_ptr(), both.data_ptr() + 4)
-    norm, scale, _, _ = both.unbind()
+        _run(dev, load_library().sc_clip_grads, n, dtypes, sizes, where, where_to, sumsq.data_ptr(), float(max_norm),
+             norm.data_ptr(), scale.data_ptr())
     return GradNorm(norm, scale, to)

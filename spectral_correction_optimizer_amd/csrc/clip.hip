@@ -5,7 +5,7 @@
 //
 // Two passes, each bound by HBM: 112 matrices, 3.9 GB in float32, are read in 0.69 ms (5.7 TB/s) and scaled into
 // others in 1.43 ms (5.4).  A second read is not to be had from the 256 MB cache but for its end; gradients that fit
-// there, 4 MB in 130 tensors, take 6.4, 2.0 and 7.3 us, less than the host's 25.  The tensors' addresses come with the
+// there, 4 MB in 130 tensors, take 6.4 and 8 us, less than the host's 20.  The tensors' addresses come with the
 // launch (kernel arguments, so the calls can be captured and hold nothing between them); a workgroup finds its tensor
 // by the number of chunks before it.  Squares are summed in 64 bits: those of float32's largest and smallest gradients
 // are out of its own range.
@@ -19,7 +19,7 @@ namespace scopt {
 constexpr int kClipThreads = 256, kClipGroups = 4;
 constexpr int64_t kClipChunk = (int64_t)kClipThreads * kClipGroups * 8;  // elements of a chunk
 constexpr int kClipTensors = 140;  // a launch takes 4 KiB of arguments
-constexpr int kSumsqGrid = 2048;
+constexpr int kSumsqGrid = 2048, kFewParts = 4 * kClipThreads;
 // (112 matrices, a chunk each 2120 us, 8192 workgroups 2150, 32768 2112)
 constexpr int kClipGrid = 32768;
 
@@ -81,8 +81,8 @@ __global__ __launch_bounds__(kClipThreads) void sumsq_kernel(const ClipTable t, 
     if (threadIdx.x == 0) gst(part + blockIdx.x, s);
 }
 
-__global__ __launch_bounds__(1024) void sumsq_join_kernel(const double* __restrict__ part, int parts,
-                                                          double* __restrict__ sumsq) {
+// (sumsq may be the first part)
+__global__ __launch_bounds__(1024) void sumsq_join_kernel(const double* part, int parts, double* sumsq) {
     __shared__ double red[16];
     double s = 0.0;
     for (int i = threadIdx.x; i < parts; i += 1024) s += gld(part + i);
@@ -90,10 +90,20 @@ __global__ __launch_bounds__(1024) void sumsq_join_kernel(const double* __restri
     if (threadIdx.x == 0) gst(sumsq, s);
 }
 
+// The sum of squares in at most kFewParts parts, which each workgroup adds up for itself: for few chunks that is less
+// than another launch (130 small tensors: the call 24.5 us with it, 19.9 without).
 template <typename E>
-__global__ __launch_bounds__(kClipThreads) void clip_kernel(const ClipTable t, const double* __restrict__ sumsq,
+__global__ __launch_bounds__(kClipThreads) void clip_kernel(const ClipTable t, const double* __restrict__ sumsq, int parts,
                                                             float max_norm, float* norm, float* scale_out) {
-    const double n = sqrt(gld(sumsq));
+    __shared__ double red[kClipThreads / 64];
+    double all = parts == 1 ? gld(sumsq) : 0.0;
+    if (parts != 1) {
+#pragma unroll
+        for (int i = 0; i < kFewParts; i += kClipThreads)
+            all += i + (int)threadIdx.x < parts ? gld(sumsq + i + threadIdx.x) : 0.0;
+        all = block_sum_f64(all, red);
+    }
+    const double n = sqrt(all);
     const double want = (double)max_norm / (n + 1e-6);
     const float scale = want < 1.0 || want != want ? (float)want : 1.0f;
     if (norm && blockIdx.x == 0 && threadIdx.x == 0) {
@@ -180,8 +190,9 @@ int64_t grad_sumsq_parts(const GradTensors& g) {
     return parts;
 }
 
-hipError_t launch_grad_sumsq(const GradTensors& g, double* sumsq, double* part, hipStream_t st) {
-    int64_t parts = 0;
+// the partial sums, and how many
+static hipError_t launch_parts(const GradTensors& g, double* part, int64_t& parts, hipStream_t st) {
+    parts = 0;
     for (int b = 0; b < 2; ++b) {
         const hipError_t e = each_table(g, b, [&](const ClipTable& t) {
             const int grid = sumsq_grid(t);
@@ -192,11 +203,32 @@ hipError_t launch_grad_sumsq(const GradTensors& g, double* sumsq, double* part, 
         });
         if (e != hipSuccess) return e;
     }
+    return hipSuccess;
+}
+
+hipError_t launch_grad_sumsq(const GradTensors& g, double* sumsq, double* part, hipStream_t st) {
+    int64_t parts;
+    const hipError_t e = launch_parts(g, part, parts, st);
+    if (e != hipSuccess) return e;
     hipLaunchKernelGGL(sumsq_join_kernel, dim3(1), dim3(1024), 0, st, part, (int)parts, sumsq);
     return hipGetLastError();
 }
 
-hipError_t launch_clip(const GradTensors& g, const double* sumsq, float max_norm, float* norm, float* scale,
+hipError_t launch_clip_norm(const GradTensors& g, float max_norm, float* norm, float* scale, double* part,
+                            hipStream_t st) {
+    int64_t parts;
+    hipError_t e = launch_parts(g, part, parts, st);
+    if (e != hipSuccess) return e;
+    if (parts > kFewParts) {
+        hipLaunchKernelGGL(sumsq_join_kernel, dim3(1), dim3(1024), 0, st, part, (int)parts, part);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        parts = 1;
+    }
+    return launch_clip(g, part, (int)parts, max_norm, norm, scale, st);
+}
+
+hipError_t launch_clip(const GradTensors& g, const double* sumsq, int parts, float max_norm, float* norm, float* scale,
                        hipStream_t st) {
     bool told = false;
     for (int b = 0; b < 2; ++b) {
@@ -205,8 +237,10 @@ hipError_t launch_clip(const GradTensors& g, const double* sumsq, float max_norm
             const dim3 grid(chunks < (uint32_t)kClipGrid ? chunks : (uint32_t)kClipGrid);
             float* to = told ? nullptr : norm;
             told = true;
-            if (b) hipLaunchKernelGGL(clip_kernel<uint16_t>, grid, dim3(kClipThreads), 0, st, t, sumsq, max_norm, to, scale);
-            else hipLaunchKernelGGL(clip_kernel<float>, grid, dim3(kClipThreads), 0, st, t, sumsq, max_norm, to, scale);
+            if (b) hipLaunchKernelGGL(clip_kernel<uint16_t>, grid, dim3(kClipThreads), 0, st, t, sumsq, parts, max_norm, to,
+                                      scale);
+            else hipLaunchKernelGGL(clip_kernel<float>, grid, dim3(kClipThreads), 0, st, t, sumsq, parts, max_norm, to,
+                                    scale);
             return hipGetLastError();
         });
         if (e != hipSuccess) return e;
@@ -215,7 +249,8 @@ hipError_t launch_clip(const GradTensors& g, const double* sumsq, float max_norm
     ClipTable none;  // no element at all: the norm is still told
     none.count = none.in_place = 0;
     none.first[0] = 0;
-    hipLaunchKernelGGL(clip_kernel<float>, dim3(1), dim3(kClipThreads), 0, st, none, sumsq, max_norm, norm, scale);
+    hipLaunchKernelGGL(clip_kernel<float>, dim3(1), dim3(kClipThreads), 0, st, none, sumsq, parts, max_norm, norm,
+                       scale);
     return hipGetLastError();
 }
 

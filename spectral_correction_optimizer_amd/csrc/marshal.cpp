@@ -63,7 +63,8 @@ extern "C" __attribute__((visibility("default"))) int scopt_overlap(int n, const
         written.reserve(n);
         for (int i = 0; i < n; ++i)
             if (sizes[i] > 0) written.push_back(range(out, i));
-        std::sort(written.begin(), written.end(), [](const Range& a, const Range& b) { return a.from < b.from; });
+        auto before = [](const Range& a, const Range& b) { return a.from < b.from; };
+        if (!std::is_sorted(written.begin(), written.end(), before)) std::sort(written.begin(), written.end(), before);
         for (size_t k = 1; k < written.size(); ++k)
             if (written[k].from < written[k - 1].to) return written[k].i;
         if (in == out) return -1;

@@ -284,7 +284,11 @@ struct GradTensors {  // host arrays
 };
 int64_t grad_sumsq_parts(const GradTensors& g);  // float64 partial sums
 hipError_t launch_grad_sumsq(const GradTensors& g, double* sumsq, double* part, hipStream_t st);
-hipError_t launch_clip(const GradTensors& g, const double* sumsq, float max_norm, float* norm, float* scale,
+// both: the norm of the gradients, and what it makes of them
+hipError_t launch_clip_norm(const GradTensors& g, float max_norm, float* norm, float* scale, double* part,
+                            hipStream_t st);
+// sumsq: its value, or some parts of it (as many as launch_clip_norm leaves)
+hipError_t launch_clip(const GradTensors& g, const double* sumsq, int parts, float max_norm, float* norm, float* scale,
                        hipStream_t st);
 
 struct WgradPlan {

@@ -429,7 +429,22 @@ int sc_clip_grads(int n, const sc_dtype* dtypes, const int64_t* sizes, const voi
     SC_TRY(check_ptr("sumsq", sumsq, 8));
     SC_TRY(check_ptr("norm", norm, 4));
     SC_TRY(check_ptr("scale", scale, 4));
-    HIP_TRY(launch_clip(GradTensors{n, dtypes, sizes, grads, out}, sumsq, max_norm, norm, scale, (hipStream_t)stream));
+    HIP_TRY(launch_clip(GradTensors{n, dtypes, sizes, grads, out}, sumsq, 1, max_norm, norm, scale,
+                        (hipStream_t)stream));
+    return SC_OK;
+}
+
+int sc_clip_norm(int n, const sc_dtype* dtypes, const int64_t* sizes, const void* const* grads, void* const* out,
+                 float max_norm, float* norm, float* scale, void* workspace, int64_t workspace_bytes, void* stream) {
+    SC_TRY(check_grads(n, dtypes, sizes));
+    SC_TRY(check_tensors("a gradient", n, dtypes, sizes, grads));
+    SC_TRY(check_tensors("an output", n, dtypes, sizes, out));
+    if (!(max_norm >= 0.0f)) return fail(SC_ERR_INVALID_ARG, "max_norm must be >= 0");
+    SC_TRY(check_ptr("norm", norm, 4));
+    SC_TRY(check_ptr("scale", scale, 4));
+    const GradTensors g{n, dtypes, sizes, grads, out};
+    SC_TRY(check_workspace(workspace, workspace_bytes, 8 * grad_sumsq_parts(g)));
+    HIP_TRY(launch_clip_norm(g, max_norm, norm, scale, (double*)workspace, (hipStream_t)stream));
     return SC_OK;
 }
 

@@ -160,3 +160,19 @@ def test_binding_refuses_cpu_tensors_and_shapes():
                  lambda: sco.clip_grads([], 1.0), lambda: sco.grad_sumsq([])):
         with pytest.raises(ValueError):
             call()
+
+
+def test_clip_norm_refusals(lib):
+    dts, sizes = (ctypes.c_int * 2)(0, 1), (ctypes.c_int64 * 2)(100, 9)
+    ptrs = (ctypes.c_void_p * 2)(4096, 8192)
+    c = lib.sc_clip_norm
+    assert c(2, dts, sizes, None, ptrs, 1.0, P, P, P, 16, None) == INVALID
+    assert c(2, dts, sizes, ptrs, None, 1.0, P, P, P, 16, None) == INVALID
+    assert c(2, dts, sizes, ptrs, (ctypes.c_void_p * 2)(4096, 4097), 1.0, P, P, P, 16, None) == INVALID
+    assert c(2, dts, sizes, ptrs, ptrs, -1.0, P, P, P, 16, None) == INVALID
+    assert c(2, dts, sizes, ptrs, ptrs, float("nan"), P, P, P, 16, None) == INVALID
+    assert c(2, dts, sizes, ptrs, ptrs, 1.0, None, P, P, 16, None) == INVALID
+    assert c(2, dts, sizes, ptrs, ptrs, 1.0, P, None, P, 16, None) == INVALID
+    assert c(2, dts, sizes, ptrs, ptrs, 1.0, P, P, P, 15, None) == INVALID
+    assert c(2, dts, sizes, ptrs, ptrs, 1.0, P, P, None, 16, None) == INVALID
+    assert c(2, dts, (ctypes.c_int64 * 2)(100, -1), ptrs, ptrs, 1.0, P, P, P, 16, None) == SHAPE

@@ -965,3 +965,27 @@ def test_many_logits_graph_replays():
         torch.cuda.synchronize()
         for a, b in zip(want, out):
             assert torch.equal(a, b), k
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("chunks", [1, 255, 256, 257, 1000, 1023, 1024, 1025, 2300])
+def test_clip_by_number_of_partial_sums(chunks, dtype):
+    """One call for norm and clipping, whose partial sums are added up in one way or the other, against the sum given."""
+    m, g = sco(), gen(69)
+    n = 8192 * chunks - 5
+    grads = [randn(g, n - n // 3, dtype=dtype), randn(g, n // 3, dtype=dtype)] if chunks > 1 else [randn(g, n, dtype=dtype)]
+    total = sum((x.to(F64) ** 2).sum() for x in grads)
+    s = m.grad_sumsq(grads)
+    # sums of 64 bits in other orders
+    assert abs(s - total) <= 1e-12 * total
+    out = [torch.empty_like(x) for x in grads]
+    a, b = m.clip_grads(grads, 3.0, out=out), m.clip_grads(grads, 3.0, out=[torch.empty_like(x) for x in grads], sumsq=s)
+    norm = total.sqrt()
+    assert abs(a.norm.to(F64) - norm) <= (U + 1e-12) * norm and abs(b.norm.to(F64) - norm) <= (U + 1e-12) * norm
+    scale = 3.0 / (norm + 1e-6)
+    assert abs(a.scale.to(F64) - scale) <= (U + 1e-12) * scale
+    for x, y, z in zip(grads, a.grads, b.grads):
+        want = x.to(F64) * scale
+        for got in (y, z):  # the factor's rounding, the product's, the output's
+            assert ((got.to(F64) - want).abs() <= (HALF[dtype] + 3 * U) * want.abs() + TINY).all()
+    assert torch.equal(a.norm, m.clip_grads(grads, 3.0, out=out).norm)
