@@ -64,6 +64,15 @@ __device__ __forceinline__ void log_sums(const LogSums& a, int64_t end, int64_t 
     z = 0.0f;
 #pragma unroll
     for (int w = 0; w < 16; ++w) z += red[w][lane];
+    if constexpr (ROWS < 64) {
+        // Losses add up log-probabilities of many tokens, and float32's logarithm is low by 3e-7 on the average at such
+        // sums (300 to 1100), as much as a rounding of the result.
+        const double base = a.pow2 ? m * 0.693147180559945309417 : (double)m;
+        const double l = m == none ? __builtin_nan("") : base + log((double)z);
+        gst(a.lse + t, (float)l);
+        tell(t, (float)((double)gld(a.target_logit + t) - l));
+        return;
+    }
     // a power of two's logarithm in two parts: m * ln2 is off by less than 2^-40 of m
     const float base = a.pow2 ? m * 0.693145751953125f : m, rest = a.pow2 ? m * 1.42860682030941723e-6f : 0.0f;
     const float logz = m == none ? __builtin_nanf("") : logf(z) + rest;
