@@ -989,3 +989,23 @@ def test_clip_by_number_of_partial_sums(chunks, dtype):
         for got in (y, z):  # the factor's rounding, the product's, the output's
             assert ((got.to(F64) - want).abs() <= (HALF[dtype] + 3 * U) * want.abs() + TINY).all()
     assert torch.equal(a.norm, m.clip_grads(grads, 3.0, out=out).norm)
+
+
+@pytest.mark.parametrize("T,V,H,kind", [(9001, 2000, 72, "half"), (20000, 1030, 40, "runs")])
+def test_policy_many_tokens(T, V, H, kind):
+    """More tokens than find their rows in one launch with the operand, with logits relative to their rows' references."""
+    g = gen(70)
+    h, W, tgt = _xent_case(g, T, V, H, torch.bfloat16)
+    tgt = _mask(tgt, kind, V)
+    ref = Tokens(h, W, tgt, torch.bfloat16)
+    old, adv, refl, _ = _policy_inputs(g, ref, (0.2, 0.2))
+    out = sco().policy_loss(h, W, tgt, old.cuda(), adv.cuda(), ref_logp=refl.cuda(), kl=0.02)
+    loss, dloss, total, dtotal, _, _, c, dc, _ = _policy_ref(ref, old, adv, refl, None, (0.2, 0.2), 0.02)
+    within("logp", out.logp.cpu(), ref.logp, ref.dlogp)
+    within("loss", out.loss.cpu(), loss, dloss)
+    within("total", out.total.cpu(), total, dtotal)
+    dh, dW, tdh, tdW = ref.gradients(c, dc)
+    within("dh", out.dh.cpu(), dh, tdh)
+    within("dW", out.dW.cpu(), dW, tdW)
+    for off in ((out.dh.cpu().to(F64) - dh).norm() / dh.norm(), (out.dW.cpu().to(F64) - dW).norm() / dW.norm()):
+        assert off <= 4 * HALF[torch.bfloat16], off
