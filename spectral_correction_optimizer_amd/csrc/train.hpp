@@ -200,11 +200,11 @@ struct XentRun {
     const int64_t* targets = nullptr;
     char* ws = nullptr;
     const int *live = nullptr, *rows = nullptr, *place = nullptr;  // place[t]: token t's row, or -1
-    // The logit gradients are (softmax - onehot) times coef[row].  In bfloat16 the matrix keeps softmax - onehot,
-    // and coef joins dh's rows as they are stored and the rows of h that dW reads, times what makes the target's
-    // entry exact (factor): the target's share of the gradients is the largest, and one coefficient for all
-    // of a sequence's tokens would be rounded the same way in all of them.  Without coef the factor is factors[1], and the stores of dh and dW
-    // multiply by factors[0].
+    // The logit gradients are (softmax - onehot) times coef[row].  In bfloat16 the matrix keeps softmax - onehot, or
+    // with by_row that times a power of two of the row, and coef joins dh's rows as they are stored and the rows of h
+    // that dW reads, times what makes the target's entry exact (factor): the target's share of the gradients is the
+    // largest, and one coefficient for all of a sequence's tokens would be rounded the same way in all of them.
+    // Without coef the factor is factors[1], and the stores of dh and dW multiply by factors[0].
     const float* coef = nullptr;
     bool gradients_follow = true;
     hipStream_t st = nullptr;
