@@ -137,10 +137,11 @@ int sc_refresh(sc_handle h, void* stream);
  * got: which factors a step uses never depends on timing.  sc_refresh_wait
  * orders its stream after the refresh and switches the following steps to the
  * new factors; every other entry point except sc_step, sc_set_lr,
- * sc_set_step, sc_get_step and sc_refresh_pending completes a pending refresh
- * the same way first (with a host wait where it takes no stream).
- * G_anc: as for sc_anchor_update; the matrices must stay valid and unchanged
- * until the refresh has been completed.  A second call while one is pending
+ * sc_set_step, sc_get_step, sc_refresh_pending and sc_anchor_read_wait completes
+ * a pending refresh the same way first (with a host wait where it takes no
+ * stream).  G_anc: as for sc_anchor_update; the matrices must stay valid and
+ * unchanged until the refresh has been completed, or until work queued after
+ * sc_anchor_read_wait on its stream.  A second call while one is pending
  * completes the pending one first.  SC_ERR_INVALID_ARG while kernel timing is on
  * (sc_profile).  The copy of the step operands takes about as much device
  * memory as the weights (allocated at the first call, kept by the handle). */
@@ -151,6 +152,11 @@ int sc_anchor_update_async(sc_handle h, const void* const* G_anc, void* stream);
  * refresh's device work, and switch later steps to its factors; reports the
  * refresh's error, if any.  SC_OK when none is pending. */
 int sc_refresh_wait(sc_handle h, void* stream);
+
+/* Make `stream` wait until a pending asynchronous anchor update has read G_anc
+ * (its EMA, not its refresh): work queued on it afterwards may change them, as
+ * clipping these gradients in place does.  SC_OK when none is pending. */
+int sc_anchor_read_wait(sc_handle h, void* stream);
 
 /* *pending = 1 while the host thread of a pending asynchronous refresh is still
  * queueing it, else 0 (then sc_refresh_wait returns without blocking the host;
@@ -526,7 +532,8 @@ int sc_grad_sumsq(int n, const sc_dtype* dtypes, const int64_t* sizes, const voi
 
 /* norm = sqrt(sumsq), scale = min(1, max_norm / (norm + 1e-6)) (float32 [1] each) and out[i] = grads[i] * scale;
  * out[i] may be grads[i], which then stays as it is where scale is 1; otherwise no output overlaps another
- * tensor.  An infinite norm gives scale 0, NaN gives NaN.  max_norm >= 0. */
+ * tensor.  An infinite norm gives scale 0, NaN gives NaN.  max_norm >= 0.  Gradients that a pending
+ * sc_anchor_update_async was given are clipped in place after sc_anchor_read_wait. */
 int sc_clip_grads(int n, const sc_dtype* dtypes, const int64_t* sizes, const void* const* grads, void* const* out,
                   const double* sumsq, float max_norm, float* norm, float* scale, void* stream);
 

@@ -34,7 +34,8 @@ _lib = None
 
 EXPORTED_SYMBOLS = (
     "sc_default_hparams", "sc_opt_create", "sc_opt_destroy", "sc_anchor_update", "sc_refresh",
-    "sc_anchor_update_async", "sc_refresh_wait", "sc_refresh_pending", "sc_step", "sc_step_noalloc", "sc_set_lr", "sc_set_tau", "sc_set_state", "sc_get_state", "sc_set_step",
+    "sc_anchor_update_async", "sc_refresh_wait", "sc_anchor_read_wait", "sc_refresh_pending",
+    "sc_step", "sc_step_noalloc", "sc_set_lr", "sc_set_tau", "sc_set_state", "sc_get_state", "sc_set_step",
     "sc_get_step", "sc_set_factors", "sc_get_factors", "sc_keep_proj", "sc_get_filtered",
     "sc_set_solve_waves", "sc_set_fused_gram", "sc_set_v_rounds", "sc_set_sweep_stop", "sc_set_quad",
     "sc_get_stats", "sc_get_sweep_counts", "sc_profile", "sc_get_kernel_times", "sc_last_error",
@@ -100,6 +101,7 @@ def load_library():
         "sc_refresh": (ctypes.c_int, [vp, vp]),
         "sc_anchor_update_async": (ctypes.c_int, [vp, ctypes.POINTER(vp), vp]),
         "sc_refresh_wait": (ctypes.c_int, [vp, vp]),
+        "sc_anchor_read_wait": (ctypes.c_int, [vp, vp]),
         "sc_refresh_pending": (ctypes.c_int, [vp, ctypes.POINTER(ctypes.c_int)]),
         "sc_step": (ctypes.c_int, [vp, ctypes.POINTER(vp), ctypes.POINTER(vp), vp]),
         "sc_step_noalloc": (ctypes.c_int, [vp, ctypes.POINTER(vp), ctypes.POINTER(vp), vp]),
@@ -254,7 +256,8 @@ class SpectralAdamW:
     def anchor_update_async(self, G_anc):
         """EMA with G_anc and SVD refresh beside the following steps, which use the
         previous factors until refresh_wait().  G_anc must stay valid and
-        unchanged until then."""
+        unchanged until then, or until work that is queued after
+        anchor_read_wait(); step() with max_norm waits for that itself."""
         _check(self._lib.sc_anchor_update_async(self._h, self._ptrs(G_anc, self.g_dtype, "G_anc"),
                                                 self._stream()))
 
@@ -263,6 +266,11 @@ class SpectralAdamW:
         and later steps use its factors."""
         _check(self._lib.sc_refresh_wait(self._h, self._stream()))
 
+    def anchor_read_wait(self):
+        """The current stream waits until a pending asynchronous update has read its
+        G_anc (not for its refresh): later work on it may change those tensors."""
+        _check(self._lib.sc_anchor_read_wait(self._h, self._stream()))
+
     def refresh_pending(self) -> bool:
         p = ctypes.c_int()
         _check(self._lib.sc_refresh_pending(self._h, ctypes.byref(p)))
@@ -270,9 +278,13 @@ class SpectralAdamW:
 
     def step(self, W, G_mask, max_norm: float = None):
         """One spectral-corrected AdamW step; W is updated in place.  max_norm: G_mask is first
-        scaled to at most that global norm, in place (clip_grads), and the GradNorm is returned."""
+        scaled to at most that global norm, in place (clip_grads), and the GradNorm is returned;
+        gradients that a pending anchor_update_async was given too are scaled once it has read them."""
         w, g = self._ptrs(W, self.w_dtype, "W"), self._ptrs(G_mask, self.g_dtype, "G_mask")
-        norm = None if max_norm is None else clip_grads(G_mask, max_norm)
+        norm = None
+        if max_norm is not None:
+            self.anchor_read_wait()
+            norm = clip_grads(G_mask, max_norm)
         _check(self._lib.sc_step(self._h, w, g, self._stream()))
         return norm
 
@@ -887,7 +899,8 @@ def clip_grads(grads, max_norm: float, out=None, sumsq: "torch.Tensor" = None) -
     """Gradients scaled to a global norm of at most max_norm: norm = sqrt(sum of all squares),
     scale = min(1, max_norm / (norm + 1e-6)), in place or into the tensors of out, none of which may share
     memory with another one.  sumsq: the sum of squares where it is known already (grad_sumsq, added over
-    the ranks)."""
+    the ranks).  Gradients that SpectralAdamW.anchor_update_async was given are clipped in place after its
+    anchor_read_wait."""
     grads = list(grads)
     dev, n, dtypes, sizes, where = _grad_table("clip_grads", grads)
     to, where_to = grads, where

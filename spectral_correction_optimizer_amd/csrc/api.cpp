@@ -248,7 +248,7 @@ struct sc_opt {
     std::vector<PubBuf> pub;
     char* pub_arena = nullptr;
     hipStream_t astream = nullptr;
-    hipEvent_t a_ready = nullptr, a_pub = nullptr, a_done = nullptr;
+    hipEvent_t a_ready = nullptr, a_pub = nullptr, a_read = nullptr, a_done = nullptr;  // a_read: G_anc was read
     std::thread worker;
     std::atomic<bool> a_finished{false};
     bool a_pending = false;
@@ -1013,6 +1013,7 @@ int ensure_async(sc_opt* h) {
     HIP_TRY(hipStreamCreateWithFlags(&h->astream, hipStreamNonBlocking));
     HIP_TRY(hipEventCreateWithFlags(&h->a_ready, hipEventDisableTiming));
     HIP_TRY(hipEventCreateWithFlags(&h->a_pub, hipEventDisableTiming));
+    HIP_TRY(hipEventCreateWithFlags(&h->a_read, hipEventDisableTiming));
     HIP_TRY(hipEventCreateWithFlags(&h->a_done, hipEventDisableTiming));
     return build_step_groups(h, 1);
 }
@@ -1666,7 +1667,7 @@ void release(sc_opt* h) {
         if (e) (void)hipEventDestroy(e);
     if (h->status_h) (void)hipHostFree(h->status_h);
     if (h->astream) (void)hipStreamDestroy(h->astream);
-    for (hipEvent_t e : {h->a_ready, h->a_pub, h->a_done})
+    for (hipEvent_t e : {h->a_ready, h->a_pub, h->a_read, h->a_done})
         if (e) (void)hipEventDestroy(e);
     if (h->pub_arena) (void)hipFree(h->pub_arena);
     for (auto& r : h->prof.recs) {
@@ -1826,6 +1827,7 @@ int sc_anchor_update_async(sc_handle h, const void* const* G_anc, void* stream) 
     PtrTable pt = make_table(h, G_anc);
     HIP_TRY(launch_ema(h->md, h->chunks_d, h->nchunks, pt, h->gdt == SC_BF16, h->hp.beta_anc,
                        h->status_d + 1, h->astream));
+    HIP_TRY(hipEventRecord(h->a_read, h->astream));  // the refresh reads the momentum only
     h->any_stale = false;  // the refresh below covers every matrix
     h->a_rc = SC_OK;
     h->a_err.clear();
@@ -1855,6 +1857,15 @@ int sc_refresh_wait(sc_handle h, void* stream) {
     if ((rc = check_handle(h))) return rc;
     DeviceGuard g(h->device);
     return finish_async(h, (hipStream_t)stream, false);
+}
+
+int sc_anchor_read_wait(sc_handle h, void* stream) {
+    int rc;
+    if ((rc = check_handle(h))) return rc;
+    if (!h->a_pending) return SC_OK;  // (completed: ordered by that)
+    DeviceGuard g(h->device);
+    HIP_TRY(hipStreamWaitEvent((hipStream_t)stream, h->a_read, 0));
+    return SC_OK;
 }
 
 int sc_refresh_pending(sc_handle h, int* pending) {

@@ -176,3 +176,7 @@ def test_clip_norm_refusals(lib):
     assert c(2, dts, sizes, ptrs, ptrs, 1.0, P, P, P, 15, None) == INVALID
     assert c(2, dts, sizes, ptrs, ptrs, 1.0, P, P, None, 16, None) == INVALID
     assert c(2, dts, (ctypes.c_int64 * 2)(100, -1), ptrs, ptrs, 1.0, P, P, P, 16, None) == SHAPE
+
+
+def test_anchor_read_wait_refuses_no_handle(lib):
+    assert lib.sc_anchor_read_wait(None, None) == INVALID
