@@ -1,9 +1,9 @@
 // The weights' gradient of few tokens (at most 128, bfloat16): dW[v][n] = sum over tokens of d[t][v] h[t][n].
 // Such a product is a write of dW: the general kernel's tiles are mostly their own beginning and end (32000 x
 // 2048 from 72 tokens 46 us, 2.9 TB/s).  Here a workgroup keeps its 256 columns of h, all tokens deep, in
-// registers and goes down the rows of dW, 64 at a time: their d comes through LDS one step ahead, and the
-// stores of a step are not waited for before the next one's products.  The same
-// product takes 31 us (4.2 TB/s).
+// registers and goes down the rows of dW, 64 at a time: their d comes through LDS one step ahead, asked for before
+// the step's stores, and those are waited for a step later only (the compiler's wait before the next step's reads of
+// LDS, behind the loads after it).  The same product takes 31 us (4.2 TB/s).
 #include "tile_product.hpp"
 
 namespace scopt {
@@ -59,6 +59,8 @@ __global__ __launch_bounds__(256, 4) void few_tokens_kernel(const uint16_t* __re
         __builtin_amdgcn_s_barrier();  // every wave's part of this step's d is there, and the last step's was read
         asm volatile("" ::: "memory");
         issue(blk + 1, next);
+        // the loads go out before this step's reads and stores: the wait at its end counts on that
+        __builtin_amdgcn_sched_barrier(0x6);  // (scalar and vector arithmetic may pass)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             v4f acc[4];
