@@ -654,19 +654,22 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void tile_product_kernel(const TpA
                 const int64_t c = t - (n0 + wn);
                 hit[i] = lm + 16 * i < M && t < N && c >= 0 && c < WN ? (int)c : -1;
             }
-            const bool pow2 = P.keep == TP_KEEP_EXP;
+            const bool pow2 = !HALF && P.keep == TP_KEEP_EXP;  // (float32 logits are kept as such)
             float* sums = red + S::WVN * BM;
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
                 row_block(i);
                 float v = -__builtin_huge_valf();
                 v4f x[NI];  // (see TP_TAIL: one place)
-                int ea = 0;
-                if constexpr (HALF) ea = gld(P.a_exp + min(lm + 16 * i, M - 1));
+                int ea = 0, eb_at = ln;
+                if constexpr (HALF) {
+                    ea = gld(P.a_exp + min(lm + 16 * i, M - 1));
+                    asm volatile("" : "+v"(eb_at));  // read anew for each row block: kept, they would be spilled
+                }
 #pragma unroll
                 for (int j = 0; j < NI; ++j) {
                     v4i eb;
-                    if constexpr (HALF) eb = *(const SC_GLOBAL v4i*)(P.b_exp + ln + 16 * j);
+                    if constexpr (HALF) eb = *(const SC_GLOBAL v4i*)(P.b_exp + eb_at + 16 * j);
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         x[j][r] = acc[i][j][r];
