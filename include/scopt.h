@@ -516,8 +516,9 @@ int sc_layernorm(sc_dtype dtype, const void* x, const void* residual, const void
 
 /* With a = dy * gain: dx = dh + rstd * (a - mean(a) - n * mean(a * n)), the gradient of x and of the
  * residual; dgain, dbias [H] float32 = sums over tokens of dy * n and of dy.  n comes from the
- * checkpoint (q, e; then h and mean are NULL), or is (h - mean) * rstd (then q and e are NULL).  dh and dbias may
- * be NULL; dx may be dy or dh. */
+ * checkpoint (q, e; then h and mean are NULL), or is (h - mean) * rstd (then q and e are NULL), where mean stands
+ * for the row's own if that is what it is but for its rounding (2^-22 of it).  h that was rounded (a residual
+ * sum, bfloat16) is taken as it is.  dh and dbias may be NULL; dx may be dy or dh. */
 int sc_layernorm_grad_workspace(int64_t T, int H, int64_t* bytes);
 int sc_layernorm_grad(sc_dtype dtype, const void* dy, const void* gain, const float* rstd, const int8_t* q,
                       const uint8_t* e, const void* h, const float* mean, const void* dh, int64_t T, int H, void* dx,

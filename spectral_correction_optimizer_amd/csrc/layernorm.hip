@@ -4,10 +4,11 @@
 //   a = dy g,  dx = dh + rstd (a - mean(a) - n mean(a n)),  dg = sum over tokens of dy n,  db = of dy
 //
 // The gradient reads n from the 8-bit checkpoint that the norm may leave (act.hip), or forms it from
-// h, mu and rstd.  Each element passes once, so HBM bounds both: the row stays in registers between
-// its sums and the outputs.  65536 x 2048 in bfloat16 with a residual: norm 197 us (5.5 TB/s), 236 us with the
-// checkpoint (5.1); gradient from the checkpoint 179 us (5.3), from h 196 us (5.5); a copy of 1 GiB
-// reaches 5.1.
+// h, mu and rstd: mu in float32 is half a step off, the same for the whole row, and in a row far from 0 a step is
+// much of the deviation (mean 100, deviation 0.001: 0.4%), so the mean of n is taken off again.  Each element passes
+// once, so HBM bounds both: the row stays in registers between its sums and the outputs.  65536 x 2048 in bfloat16
+// with a residual: norm 197 us (5.5 TB/s), 236 us with the checkpoint (5.1); gradient from the checkpoint 174 us
+// (5.4), from h 194 us (5.5); a copy of 1 GiB reaches 5.1.
 #include <cmath>
 
 #include "rows.hpp"
@@ -194,7 +195,8 @@ template <typename E> struct LnGradArgs {
 template <typename E, int ENDS, int TPR, int C, int ROWS, bool KEPT>
 __global__ __launch_bounds__(TPR * ROWS) void layernorm_grad_kernel(const LnGradArgs<E> P) {
     constexpr bool JOINT = ROWS > 1 && TPR > 64;  // the rows share barriers: all of them take every turn
-    __shared__ float red[ROWS][2][TPR / 64][2];
+    constexpr int SUMS = KEPT ? 2 : 3;
+    __shared__ float red[ROWS][2][TPR / 64][SUMS];
     __shared__ float sums[ROWS > 1 ? TPR * 16 : 1];
     const int in = threadIdx.x % TPR, row = threadIdx.x / TPR;
     const int H = P.H, nb = (H + kActBlock - 1) / kActBlock;
@@ -236,7 +238,7 @@ __global__ __launch_bounds__(TPR * ROWS) void layernorm_grad_kernel(const LnGrad
         } else {
             fetch(live ? t : T - 1, cur);
         }
-        float a[C][8], n[C][8], s[2] = {0.0f, 0.0f};
+        float a[C][8], n[C][8], s[SUMS] = {};
 #pragma unroll
         for (int j = 0; j < C; ++j) {
             const int c = (j * TPR + in) * 8;
@@ -255,6 +257,7 @@ __global__ __launch_bounds__(TPR * ROWS) void layernorm_grad_kernel(const LnGrad
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 dg[j][i] = fmaf(a[j][i], n[j][i], dg[j][i]);
+                if constexpr (!KEPT) s[2] += n[j][i];
                 db[j][i] += a[j][i];
                 a[j][i] *= g[j][i];
                 s[0] += a[j][i];
@@ -270,7 +273,27 @@ __global__ __launch_bounds__(TPR * ROWS) void layernorm_grad_kernel(const LnGrad
             }
         }
         row_sums<TPR>(s, red[row], turn);
-        const float c0 = s[0] / (float)H, c1 = s[1] / (float)H;
+        const float c0 = s[0] / (float)H;
+        float c1 = s[1] / (float)H;
+        if constexpr (!KEPT) {
+            // What the mean's rounding left in the row comes off: not where it is more than that, as the mean is
+            // another one, nor where it is no more than the rounding of n itself.
+            const float shift = s[2] / (float)H;
+            if (fabsf(shift) > 0x1p-23f && fabsf(shift) <= 0x1p-22f * fabsf(cur.mu) * cur.rs) {
+                c1 = fmaf(-shift, c0, c1);
+#pragma unroll
+                for (int j = 0; j < C; ++j) {
+                    const int c = (j * TPR + in) * 8;
+                    float dy[8];
+                    value8(cur.dy[j], c, H, dy);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        n[j][i] -= c + i < H ? shift : 0.0f;
+                        dg[j][i] = fmaf(live ? dy[i] : 0.0f, -shift, dg[j][i]);
+                    }
+                }
+            }
+        }
 #pragma unroll
         for (int j = 0; j < C; ++j) {
             const int c = (j * TPR + in) * 8, left = H - c;
