@@ -862,7 +862,10 @@ def _grad_table(who, tensors, like=None, arrays=None):
         raise ValueError(f"{who}: no tensors")
     if like is not None and len(like) != n:
         raise ValueError(f"{who}: {n} outputs for {len(like)} gradients")
-    dev = (tensors if like is None else like)[0].device
+    first = (tensors if like is None else like)[0]
+    if not isinstance(first, torch.Tensor):
+        raise ValueError(f"{who}: entry 0 is a {type(first).__name__}, not a tensor")
+    dev = first.device
     if dev.type != "cuda":
         raise ValueError(f"{who}: tensors must be on a GPU, got {dev}")
     dtypes, sizes = arrays or ((ctypes.c_int * n)(), (ctypes.c_int64 * n)())
