@@ -533,8 +533,8 @@ int sc_grad_sumsq(int n, const sc_dtype* dtypes, const int64_t* sizes, const voi
 
 /* norm = sqrt(sumsq), scale = min(1, max_norm / (norm + 1e-6)) (float32 [1] each) and out[i] = grads[i] * scale;
  * out[i] may be grads[i], which then stays as it is where scale is 1; otherwise no output overlaps another
- * tensor.  An infinite norm gives scale 0, NaN gives NaN.  max_norm >= 0.  Gradients that a pending
- * sc_anchor_update_async was given are clipped in place after sc_anchor_read_wait. */
+ * tensor.  An infinite norm gives scale 0 (1 where max_norm is infinite), NaN gives NaN.  max_norm >= 0.
+ * Gradients that a pending sc_anchor_update_async was given are clipped in place after sc_anchor_read_wait. */
 int sc_clip_grads(int n, const sc_dtype* dtypes, const int64_t* sizes, const void* const* grads, void* const* out,
                   const double* sumsq, float max_norm, float* norm, float* scale, void* stream);
 

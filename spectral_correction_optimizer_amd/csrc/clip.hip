@@ -104,7 +104,8 @@ __global__ __launch_bounds__(kClipThreads) void clip_kernel(const ClipTable t, c
         all = block_sum_f64(all, red);
     }
     const double n = sqrt(all);
-    const double want = (double)max_norm / (n + 1e-6);
+    // (no limit: nothing is scaled, an infinite norm's gradients neither)
+    const double want = n == n && max_norm == __builtin_huge_valf() ? 1.0 : (double)max_norm / (n + 1e-6);
     const float scale = want < 1.0 || want != want ? (float)want : 1.0f;
     if (norm && blockIdx.x == 0 && threadIdx.x == 0) {
         gst(norm, (float)n);
