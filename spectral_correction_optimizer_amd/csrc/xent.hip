@@ -63,8 +63,8 @@ __global__ __launch_bounds__(1024) void token_lse_kernel(const LogSums a, const 
     log_sums<16>(a, end, (int64_t)blockIdx.x * 16, red, [&](int64_t t, float lp) { gst(logp + gld(rows + t), lp); });
 }
 
-// The power of two that a token's exponentials are kept relative to (XentPlan::by_row): 2^32 times its target's, whose
-// logit is formed here for that alone.  A wavefront a row.
+// The power of two that a token's exponentials are kept relative to (XentPlan::by_row): its target's, whose logit is
+// formed here for that alone, so that none is smaller there than its probability is.  A wavefront a row.
 __global__ __launch_bounds__(256) void row_reference_kernel(const int* __restrict__ live,
                                                             const uint16_t* __restrict__ h, int64_t ldh,
                                                             const uint16_t* __restrict__ W, int64_t ldw,
@@ -87,7 +87,7 @@ __global__ __launch_bounds__(256) void row_reference_kernel(const int* __restric
     for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
     // (none for a logit past 2^16, whose last bits are the order of its sum)
     if ((threadIdx.x & 63) == 0)
-        gst(ref + t, fabsf(s) < 0x1p16f ? ceilf(s * kLog2e) + 32.0f : __builtin_nanf(""));
+        gst(ref + t, fabsf(s) < 0x1p16f ? ceilf(s * kLog2e) : __builtin_nanf(""));
 }
 // Whether all of a row's tiles are kept relative to its reference: no tile's own is above the next power of two
 // of the row's sum by more than one.
@@ -188,11 +188,14 @@ __global__ __launch_bounds__(256) void xent_dlogits_kernel(const float* __restri
             const v4u w = *(const SC_GLOBAL v4u*)p;
             const float ref = gld(smax + (int64_t)(c / bn) * T + t);
             const bool by_row = row_ref && tp_by_row(ref, to_row);
-            const float f = __builtin_amdgcn_exp2f((by_row ? to_row : ref) - ls2) * scale;
+            // (a row's own reference may be below the smallest number where the tile's, 2^64 above it, is not)
+            const float x = (by_row ? to_row : ref) - ls2;
+            const bool below = by_row && x < -64.0f;
+            const float f = __builtin_amdgcn_exp2f(below ? x + 64.0f : x) * scale, low = below ? 0x1p-64f : 1.0f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                v[2 * i] = (by_row ? bf16_lo(w[i]) : tp_unit_lo(w[i])) * f;
-                v[2 * i + 1] = (by_row ? bf16_hi(w[i]) : tp_unit_hi(w[i])) * f;
+                v[2 * i] = (by_row ? bf16_lo(w[i]) : tp_unit_lo(w[i])) * f * low;
+                v[2 * i + 1] = (by_row ? bf16_hi(w[i]) : tp_unit_hi(w[i])) * f * low;
             }
         } else {
             const v4f a = gld4(logits + t * ldp + c), b = gld4(logits + t * ldp + c + 4);
