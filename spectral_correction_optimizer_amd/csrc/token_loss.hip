@@ -15,10 +15,12 @@
 // What is a token's or a pair's is computed in 64 bits: a KL term is a difference near zero, and a
 // sequence's log-probability a long sum.
 // The three products bound both losses at many tokens, reading W and writing dW at few.  Policy of 8192 tokens,
-// 4096 of them counted, 131072 x 2048 in bfloat16: logits 2.02 ms (1090 TFLOP/s), dh 1.64 (1340), dW 1.84 (1200),
-// all else 0.09, the call 5.56; of 1000 tokens, 700 counted, 50021 x 1001 in float32 1.29 ms: logits 0.27 ms in three
-// float16 products, dh 0.41 and dW 0.44 in six, planes 0.14 and the gradients of the logits 0.08.  Preference of a pair of
-// 96 tokens, 32000 x 2048: logits 45 us (2.9 TB/s), dh 28 and dW 30 (4.3 TB/s), five small launches 30.
+// 4096 of them counted, 131072 x 2048 in bfloat16: logits 2.01 ms (1090 TFLOP/s), dh 1.64 (1340), dW 1.83 (1200),
+// all else 0.09, the call 5.51 to 5.65; of 1000 tokens, 700 counted, 50021 x 1001 in float32 1.27 to 1.29 ms: logits
+// 0.26 ms in three float16 products, dh 0.41 and dW 0.43 in six, planes 0.14 and the gradients of the logits 0.08.
+// Preference of a pair of 96 tokens, 32000 x 2048: logits 45 us (2.9 TB/s; 34 where no exponentials are kept behind a
+// write of as much), dh 28 and dW 30 (4.4 TB/s), five small launches 30.  (Tiles are chosen by T: 60 counted tokens of
+// 1000 take 182 us, alone 134.)
 #include <cmath>
 
 #include "common.hpp"

@@ -34,7 +34,8 @@
 // of its own, which in bfloat16 goes onto its row of dh and its row of h before dW (one rounding more; rows of dW
 // against 64 bits 0.0024 of their norm off where a target is met once, dh 0.0017, the rounding of the outputs
 // alone 0.0017), so that what is kept can be relative to any power of two of the row (XentPlan::by_row): where that
-// is known before the logits, no pass turns exponentials into d.
+// is known before the logits, no pass turns exponentials into d.  The factor also undoes the rounding of the target's
+// entry, the largest, and moves the row's other entries together by that much, 2^-8 of themselves at most.
 #include <cmath>
 
 #include "log_sums.hpp"
