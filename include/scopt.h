@@ -484,8 +484,9 @@ int sc_token_logp(sc_dtype dtype, const void* h, const void* W, const int64_t* t
  * of h and W for the logits.  0 <= clip_low <= 1, clip_high, kl >= 0.
  *
  * The products run over the counted tokens only.  bfloat16: softmax - onehot is rounded as sc_xent's gradients
- * are, and the rows of h that dW is summed from, times the tokens' factors, once more.  float32: a logit's
- * factors are taken to 2^-22 of themselves (or 2^-39 of their row's largest, if that is more). */
+ * are, and the rows of h that dW is summed from, times the tokens' factors, once more; the target's entry is
+ * exact, and the others of its row are off by its rounding, at most 2^-8, together.  float32: a logit's factors
+ * are taken to 2^-22 of themselves (or 2^-39 of their row's largest, if that is more). */
 int sc_token_loss_workspace(sc_dtype dtype, int64_t T, int64_t V, int H, int64_t limit, int64_t* bytes);
 int sc_policy_loss(sc_dtype dtype, const void* h, const void* W, const int64_t* targets, const float* old_logp,
                    const float* advantages, const float* ref_logp, const float* weights, int64_t T, int64_t V, int H,
